@@ -45,7 +45,9 @@ typedef enum {
 } ts_status;
 
 /* element types */
-enum { TS_F16 = 1, TS_BF16 = 2, TS_F32 = 3 };
+enum { TS_F16 = 1, TS_BF16 = 2, TS_F32 = 3,
+       TS_E4M3 = 4 };   /* 8-bit float, 4 exponent and 3 mantissa bits, largest value 448
+                           (operands of ts_gemm_epilogue, output of ts_rmsnorm)         */
 
 /* tile order: which output tile a linear tile id denotes */
 enum {
@@ -372,6 +374,126 @@ ts_status ts_schedule_trace_host(int64_t M, int64_t N, int64_t K, int32_t ab_dty
  */
 ts_status ts_query(int64_t M, int64_t N, int64_t K, int32_t ab_dtype, int32_t c_dtype,
                    const ts_schedule* sched, ts_launch_info* out);
+
+/* activations of the fused epilogue */
+enum {
+    TS_ACT_NONE = 0,
+    TS_ACT_RELU = 1,       /* max(z, 0)                                               */
+    TS_ACT_GELU = 2,       /* z Phi(z), Phi the normal distribution function           */
+    TS_ACT_GELU_TANH = 3,  /* 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))          */
+    TS_ACT_SILU = 4        /* z / (1 + exp(-z))                                        */
+};
+
+/* What ts_gemm_epilogue does between the fp32 sums and C. */
+typedef struct {
+    int32_t activation;     /* TS_ACT_*                                                   */
+    int32_t grad;           /* 0: forward; 1: C = z * act'(preact)                        */
+    const void* bias;       /* N elements, contiguous, or NULL                            */
+    int32_t bias_dtype;     /* TS_F16, TS_BF16 or TS_F32 (read when bias is given)        */
+    int32_t reserved;       /* 0                                                          */
+    const void* residual;   /* M x N of C's type, unit column stride, or NULL; may be C   */
+    int64_t stride_rm;      /* elements between its rows (ignored when M <= 1)            */
+    void* preact;           /* M x N of C's type, unit column stride, or NULL: written
+                               when grad is 0, read when it is 1                          */
+    int64_t stride_pm;
+    const float* scale_a;   /* e4m3 operands: M fp32, one per row of A; NULL: 1           */
+    const float* scale_b;   /* e4m3 operands: N fp32, one per column of B; NULL: 1        */
+} ts_epilogue;
+
+/*
+ * The product with a fused epilogue, in one pass over C:
+ *     z = (A @ B) * scale_a[m] * scale_b[n] + bias[n]
+ *     grad 0:  preact = z (if given),  C = act(z) + residual
+ *     grad 1:  C = z * act'(preact)    (the gradient of a product that feeds an
+ *              activation; no bias, no residual)
+ * All of it in fp32 from the fp32 sums; preact and C are each rounded once, to C's
+ * type.  epi == NULL: the plain product.
+ *   ab_dtype / c_dtype: TS_F16 -> TS_F16, TS_F32; TS_BF16 -> TS_BF16, TS_F32;
+ *   TS_E4M3 -> TS_F16, TS_BF16, TS_F32.  Layouts and strides of A, B and C as in
+ *   ts_gemm; with TS_E4M3 only A stored [M][K] and B stored [N][K] (stride_bk == 1).
+ *   Any M, N, K and row stride.  An operand whose rows the direct-to-LDS loads cannot
+ *   take (stored along K: base, row stride and K multiples of 16 bytes; stored along M
+ *   or N: base 4-byte aligned, row stride and row length even) is first copied into
+ *   the workspace, its rows padded with zeros.  K == 0: the sums are zero.
+ *   sched == NULL: order and mode chosen by the library.  TS_MODE_TILED,
+ *   TS_MODE_PERSISTENT and TS_MODE_CROSSTILE run the nested cross-tile loop and give
+ *   bit-identical results; TS_MODE_STREAMK as in ts_gemm.  Tiles: TS_TILE_AUTO,
+ *   TS_TILE_128x128x64, TS_TILE_256x256x64_W8 (others: TS_ERR_UNSUPPORTED); with
+ *   8-bit operands a K step holds 128 values.
+ *   workspace: at least ts_gemm_epilogue_workspace bytes for the same arguments,
+ *   256-byte aligned, contents arbitrary (a stream-K launch clears its own flags);
+ *   calls that share one must not overlap in time.  NULL where none is needed.
+ *   The current device must be the stream's.
+ *   Errors: as ts_gemm; TS_ERR_INVALID_ARG for a bad epilogue; rows of 2^30 bytes per
+ *   tile or more (K of 2^21 16-bit elements on the 256 tile): TS_ERR_UNSUPPORTED.
+ */
+ts_status ts_gemm_epilogue(const void* A, const void* B, void* C,
+                           int64_t M, int64_t N, int64_t K,
+                           int64_t stride_am, int64_t stride_ak,
+                           int64_t stride_bk, int64_t stride_bn,
+                           int64_t stride_cm, int64_t stride_cn,
+                           int32_t ab_dtype, int32_t c_dtype,
+                           const ts_epilogue* epi, const ts_schedule* sched, void* stream,
+                           void* workspace, int64_t workspace_bytes);
+
+/* Bytes of workspace that ts_gemm_epilogue needs for these arguments, or a negative
+   ts_status.  It depends on the addresses and strides of A and B (packing).  Needs a
+   device only for TS_MODE_STREAMK with num_programs == 0. */
+int64_t ts_gemm_epilogue_workspace(const void* A, const void* B,
+                                   int64_t M, int64_t N, int64_t K,
+                                   int64_t stride_am, int64_t stride_ak,
+                                   int64_t stride_bk, int64_t stride_bn,
+                                   int32_t ab_dtype, int32_t c_dtype, const ts_schedule* sched);
+
+/*
+ * Gradient of ts_gemm_epilogue's epilogue, in front of the two products of the backward
+ * pass (dA = dZ @ B^T, dB = A^T @ dZ: ts_gemm_epilogue with a NULL epilogue):
+ *     dZ = dC * act'(preact),   dbias[n] = sum over m of dZ[m][n]
+ * dC and preact: M x N of in_dtype (TS_F16, TS_BF16, TS_F32), dZ: M x N of out_dtype
+ * (in_dtype; from TS_F32 any of the three), unit column strides; dbias: N contiguous
+ * elements of bias_dtype.  dZ or dbias may be NULL (not wanted); preact is read unless
+ * activation is TS_ACT_NONE.  dbias sums the unrounded fp32 products in a fixed order.
+ * dZ may be dC or preact.  M == 0: dbias is set to zero.  workspace (for dbias): at
+ * least ts_act_grad_workspace(M, N) bytes, 256-byte aligned, contents arbitrary, not
+ * shared by calls that overlap in time.  The current device must be the stream's.
+ */
+ts_status ts_act_grad(const void* dC, const void* preact, void* dZ, void* dbias,
+                      int64_t M, int64_t N, int64_t stride_dc, int64_t stride_pm, int64_t stride_dz,
+                      int32_t in_dtype, int32_t out_dtype, int32_t bias_dtype, int32_t activation,
+                      void* stream, void* workspace, int64_t workspace_bytes);
+int64_t ts_act_grad_workspace(int64_t M, int64_t N);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition in front of it:
+ *     h = x + residual,   y = h / sqrt(mean(h^2) + eps) * weight
+ * x, residual, h: M x N of x_dtype (TS_F16, TS_BF16, TS_F32), unit column strides;
+ * weight: N contiguous elements of w_dtype (x_dtype or TS_F32) or NULL (1); y: M x N of
+ * y_dtype, x_dtype or TS_E4M3.  With TS_E4M3 also one fp32 scale per row, max|y| / 448
+ * but at least 2^-100, and y holds y / scale rounded to nearest even: the row operand of
+ * ts_gemm_epilogue (A with scale_a).  A row with a NaN in y has a NaN scale.
+ * residual and h come together or are both NULL.  All of it in fp32; the norm reads the
+ * unrounded sum, h is its one rounding.  h may be x or residual; y of x_dtype may
+ * be x or residual where h is not.  The current device must be the stream's.
+ */
+ts_status ts_rmsnorm(const void* x, const void* residual, const void* weight, void* y, void* h, float* scale,
+                     int64_t M, int64_t N, int64_t stride_x, int64_t stride_r, int64_t stride_y, int64_t stride_h,
+                     int32_t x_dtype, int32_t w_dtype, int32_t y_dtype, float eps, void* stream);
+
+/*
+ * Its gradients, with r = 1 / sqrt(mean(h^2) + eps):
+ *     dx = r weight dy - h r^3 mean(weight dy h) + dh      (x's and the residual's alike)
+ *     dweight[n] = sum over m of dy h r
+ * dy, h, dh (NULL: 0; the gradient that reaches h along the residual stream) and dx:
+ * M x N of dtype; dx may be dy or dh.  weight NULL: 1.  dweight: w_dtype, or NULL.  Sums
+ * in fp32, in a fixed order.  workspace (with dweight, and for rows of more than 32768):
+ * at least ts_rmsnorm_backward_workspace(M, N) bytes, 256-byte aligned, contents
+ * arbitrary, not shared by calls that overlap in time.
+ */
+ts_status ts_rmsnorm_backward(const void* dy, const void* h, const void* weight, const void* dh, void* dx,
+                              void* dweight, int64_t M, int64_t N, int64_t stride_dy, int64_t stride_h,
+                              int64_t stride_dh, int64_t stride_dx, int32_t dtype, int32_t w_dtype, float eps,
+                              void* stream, void* workspace, int64_t workspace_bytes);
+int64_t ts_rmsnorm_backward_workspace(int64_t M, int64_t N);
 
 /* Static, human-readable name of a status code.  This library's own addition
    (the pages define no error reporting). */

@@ -29,7 +29,8 @@ _i32, _i64, _p = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 
 # status codes, element types and schedule enums (include/tsgemm.h)
 TS_OK, TS_ERR_INVALID_ARG, TS_ERR_UNSUPPORTED, TS_ERR_ALIGNMENT, TS_ERR_HIP, TS_ERR_NO_DEVICE = 0, -1, -2, -3, -4, -5
-TS_F16, TS_BF16, TS_F32 = 1, 2, 3
+TS_F16, TS_BF16, TS_F32, TS_E4M3 = 1, 2, 3, 4
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 ORDERS = {"row_major": 0, "grouped": 1, "auto": 2}
 MODES = {"tiled": 0, "persistent": 1, "crosstile": 2, "streamk": 3, "auto": 4}
 INDEX_MATH = {"divide": 0, "mulshift": 1}
@@ -77,11 +78,36 @@ _lib.ts_schedule_trace_host.argtypes = [_i64, _i64, _i64, _i32, _i32, ctypes.POI
 _lib.ts_schedule_trace_host.restype = _i32
 _lib.ts_query.argtypes = [_i64, _i64, _i64, _i32, _i32, ctypes.POINTER(_Schedule), ctypes.POINTER(LaunchInfo)]
 _lib.ts_query.restype = _i32
+
+
+class _Epilogue(ctypes.Structure):
+    _fields_ = [("activation", _i32), ("grad", _i32), ("bias", _p), ("bias_dtype", _i32), ("reserved", _i32),
+                ("residual", _p), ("stride_rm", _i64), ("preact", _p), ("stride_pm", _i64),
+                ("scale_a", _p), ("scale_b", _p)]
+
+
+_lib.ts_gemm_epilogue.argtypes = [_p, _p, _p] + [_i64] * 9 + [_i32, _i32, ctypes.POINTER(_Epilogue),
+                                                               ctypes.POINTER(_Schedule), _p, _p, _i64]
+_lib.ts_gemm_epilogue.restype = _i32
+_lib.ts_gemm_epilogue_workspace.argtypes = [_p, _p] + [_i64] * 7 + [_i32, _i32, ctypes.POINTER(_Schedule)]
+_lib.ts_gemm_epilogue_workspace.restype = _i64
+_lib.ts_rmsnorm.argtypes = [_p] * 6 + [_i64] * 6 + [_i32] * 3 + [ctypes.c_float, _p]
+_lib.ts_rmsnorm.restype = _i32
+_lib.ts_rmsnorm_backward.argtypes = [_p] * 6 + [_i64] * 6 + [_i32] * 2 + [ctypes.c_float, _p, _p, _i64]
+_lib.ts_rmsnorm_backward.restype = _i32
+_lib.ts_rmsnorm_backward_workspace.argtypes = [_i64, _i64]
+_lib.ts_rmsnorm_backward_workspace.restype = _i64
+_lib.ts_act_grad.argtypes = [_p] * 4 + [_i64] * 5 + [_i32] * 4 + [_p, _p, _i64]
+_lib.ts_act_grad.restype = _i32
+_lib.ts_act_grad_workspace.argtypes = [_i64, _i64]
+_lib.ts_act_grad_workspace.restype = _i64
 _lib.ts_status_string.argtypes = [_i32]
 _lib.ts_status_string.restype = ctypes.c_char_p
 
 EXPORTS = ("ts_gemm", "ts_gemm_workspace", "ts_gemm_noalloc", "ts_noalloc_scratch_bytes", "ts_gemm_clocked", "ts_schedule_trace", "ts_schedule_trace_host", "ts_query",
-           "ts_status_string", "ts_mfma_loop_probe", "ts_mfma_phase_probe")
+           "ts_status_string", "ts_mfma_loop_probe", "ts_mfma_phase_probe", "ts_gemm_epilogue",
+           "ts_gemm_epilogue_workspace", "ts_rmsnorm", "ts_rmsnorm_backward", "ts_rmsnorm_backward_workspace",
+           "ts_act_grad", "ts_act_grad_workspace")
 
 
 class TsError(RuntimeError):
@@ -304,3 +330,315 @@ def schedule_trace_host(M: int, N: int, K: int, schedule: Schedule, cu_count: in
     _check(_lib.ts_schedule_trace_host(M, N, K, ab_dtype, c_dtype, ctypes.byref(s), cu_count,
                                        programs_per_cu, out.ctypes.data, rows))
     return out[:rows]
+
+
+# ---- operators around the product ------------------------------------------------------
+
+_DTYPE = {**_TORCH_DTYPE, torch.float8_e4m3fn: TS_E4M3}
+
+
+def _device_of(*tensors) -> torch.device:
+    """The one GPU that every given tensor (None: absent) is on."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors must be on the same GPU")
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a GPU")
+    return dev
+
+
+class _On:
+    """Makes `device` current for the launches inside (and back), and holds its stream."""
+
+    def __init__(self, device: torch.device):
+        self.index = device.index
+        self.stream = torch.cuda.current_stream(device).cuda_stream
+
+    def __enter__(self):
+        self.back = torch.cuda.current_device()
+        if self.back != self.index:
+            torch.cuda.set_device(self.index)
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.back != self.index:
+            torch.cuda.set_device(self.back)
+        return False
+
+
+def _scratch(nbytes: int, device: torch.device):
+    """A workspace of the call's own, from torch's allocator: calls on other streams, and
+    graphs captured one after the other, never share one."""
+    if nbytes < 0:
+        raise TsError(int(nbytes))
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _rows(t: torch.Tensor, shape, what: str, dtype=None) -> int:
+    """Row stride of a matrix with unit column stride, after its checks."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have unit stride along its rows")
+    return t.stride(0)
+
+
+def _vector(t: torch.Tensor, n: int, what: str, dtype=None) -> None:
+    if tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous vector of {n}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
+    if t.dtype not in _TORCH_DTYPE:
+        raise ValueError(f"{what} is {t.dtype}")
+
+
+def _activation(name) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation {name!r}: one of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[name]
+
+
+def _product(a, b, out, out_dtype, epi: _Epilogue, schedule, matrices, bias=None, scales=(None, None)):
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[0]:
+        raise ValueError(f"shapes {tuple(a.shape)} @ {tuple(b.shape)} do not multiply")
+    if a.dtype != b.dtype:
+        raise ValueError(f"A is {a.dtype}, B is {b.dtype}")
+    dev = _device_of(a, b, out, bias, *scales, *(t for t, _, _ in matrices))
+    (M, K), N = a.shape, b.shape[1]
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    elif out.shape != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out has the wrong shape or type")
+    for t, what, put in matrices:
+        if t is not None:
+            put(t.data_ptr(), _rows(t, (M, N), what, out.dtype))
+    if bias is not None:
+        _vector(bias, N, "bias")
+        epi.bias, epi.bias_dtype = bias.data_ptr(), _TORCH_DTYPE[bias.dtype]
+    if scales[0] is not None:
+        _vector(scales[0], M, "scale_a", torch.float32)
+        epi.scale_a = scales[0].data_ptr()
+    if scales[1] is not None:
+        _vector(scales[1], N, "scale_b", torch.float32)
+        epi.scale_b = scales[1].data_ptr()
+    s = ctypes.byref(schedule._c()) if schedule is not None else None
+    ab_t, c_t = _DTYPE.get(a.dtype, 0), _DTYPE.get(out.dtype, 0)
+    pa, pb = a.data_ptr(), b.data_ptr()
+    sizes = (M, N, K, a.stride(0), a.stride(1), b.stride(0), b.stride(1))
+    with _On(dev) as stream:
+        need = _lib.ts_gemm_epilogue_workspace(pa, pb, *sizes, ab_t, c_t, s)
+        ws = _scratch(need, dev)
+        _check(_lib.ts_gemm_epilogue(pa, pb, out.data_ptr(), *sizes, out.stride(0), out.stride(1), ab_t, c_t,
+                                     ctypes.byref(epi), s, stream, ws.data_ptr() if ws is not None else None,
+                                     max(need, 0)))
+    return out
+
+
+def gemm_epilogue(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = None, activation: str = "none",
+                  residual: torch.Tensor | None = None, preact: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                  schedule: Schedule | None = None) -> torch.Tensor:
+    """C = act(A @ B + bias) + residual, A [M,K] and B [K,N] fp16/bf16; C fp16/bf16/fp32.
+
+    ``activation``: "none", "relu", "gelu" (exact), "gelu_tanh" or "silu".  ``bias``: [N],
+    fp16/bf16/fp32.  ``residual``: [M,N] of C's type (may be ``out``).  ``preact``: an [M,N]
+    tensor of C's type that receives A @ B + bias, for the backward pass.  A and B may be
+    transposed views and have any row stride; ``schedule=None`` chooses order, mode and tile.
+    Enqueued on the current stream of A's device.  A 2-D product: batched or 1-D operands
+    are reshaped by the caller.  The gradients: ``gemm_epilogue_backward``.
+    """
+    epi = _Epilogue(activation=_activation(activation))
+
+    def put_r(p, ld):
+        epi.residual, epi.stride_rm = p, ld
+
+    def put_p(p, ld):
+        epi.preact, epi.stride_pm = p, ld
+
+    return _product(a, b, out, out_dtype or (out.dtype if out is not None else a.dtype), epi, schedule,
+                    [(residual, "residual", put_r), (preact, "preact", put_p)], bias)
+
+
+def gemm_dact(a: torch.Tensor, b: torch.Tensor, preact: torch.Tensor, activation: str,
+              out: torch.Tensor | None = None, schedule: Schedule | None = None) -> torch.Tensor:
+    """C = (A @ B) * act'(preact): the gradient that reaches the input of an activation whose
+    output feeds a product, in that product's own backward launch (A the gradient of its
+    output, B its weights transposed).  C has ``preact``'s type."""
+    epi = _Epilogue(activation=_activation(activation), grad=1)
+
+    def put_p(p, ld):
+        epi.preact, epi.stride_pm = p, ld
+
+    return _product(a, b, out, preact.dtype, epi, schedule, [(preact, "preact", put_p)])
+
+
+def gemm_scaled(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor | None = None,
+                scale_b: torch.Tensor | None = None, bias: torch.Tensor | None = None, activation: str = "none",
+                residual: torch.Tensor | None = None, preact: torch.Tensor | None = None,
+                out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                schedule: Schedule | None = None) -> torch.Tensor:
+    """C = act((A @ B) * scale_a[:, None] * scale_b[None, :] + bias) + residual with e4m3 A
+    [M,K] (rows contiguous) and B [K,N] stored [N][K] (a transposed view of [N,K] weights).
+
+    ``scale_a`` [M] and ``scale_b`` [N] are fp32 (None: 1); an element's value is
+    e4m3 * scale, as ``rmsnorm(..., out_dtype=torch.float8_e4m3fn)`` returns them.  C is
+    fp16, bf16 (default) or fp32.  Otherwise as ``gemm_epilogue``.
+    """
+    if a.dtype != torch.float8_e4m3fn:
+        raise ValueError(f"A is {a.dtype}, expected torch.float8_e4m3fn")
+    epi = _Epilogue(activation=_activation(activation))
+
+    def put_r(p, ld):
+        epi.residual, epi.stride_rm = p, ld
+
+    def put_p(p, ld):
+        epi.preact, epi.stride_pm = p, ld
+
+    return _product(a, b, out, out_dtype or (out.dtype if out is not None else torch.bfloat16), epi, schedule,
+                    [(residual, "residual", put_r), (preact, "preact", put_p)], bias, (scale_a, scale_b))
+
+
+def act_grad(dc: torch.Tensor, preact: torch.Tensor | None = None, activation: str = "none",
+             out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, dbias: bool = True,
+             dbias_dtype: torch.dtype = torch.float32):
+    """dZ = dC * act'(preact) and the bias gradient, its column sums; returns (dZ, dbias).
+
+    dC and ``preact`` are [M,N] of one type (fp16, bf16, fp32).  dZ: ``out`` or a new tensor
+    of ``out_dtype`` (dC's type; fp16 or bf16 from fp32).  dbias sums the unrounded fp32
+    products in a fixed order (the same bits on every run); None if ``dbias`` is False.
+    With activation "none", ``preact`` is not read, and dZ is dC itself (not a copy) unless
+    ``out`` or ``out_dtype`` asks for one.
+    """
+    act = _activation(activation)
+    if dc.dim() != 2:
+        raise ValueError("dC must be a matrix")
+    M, N = dc.shape
+    if act and preact is None:
+        raise ValueError("preact is needed for this activation")
+    if not act:
+        preact = None
+    ldc = _rows(dc, (M, N), "dC")
+    ldz = _rows(preact, (M, N), "preact", dc.dtype) if preact is not None else N
+    copy = act or out is not None or out_dtype not in (None, dc.dtype)
+    if out is None and copy:
+        out = torch.empty((M, N), dtype=out_dtype or dc.dtype, device=dc.device)
+    dev = _device_of(dc, preact, out)
+    ldo = _rows(out, (M, N), "out", out_dtype) if out is not None else N
+    db = torch.empty(N, dtype=dbias_dtype, device=dev) if dbias else None
+    if out is None and db is None:
+        return dc, None
+    with _On(dev) as stream:
+        need = _lib.ts_act_grad_workspace(M, N) if dbias else 0
+        ws = _scratch(need, dev)
+        _check(_lib.ts_act_grad(dc.data_ptr(), preact.data_ptr() if preact is not None else None,
+                                out.data_ptr() if out is not None else None, db.data_ptr() if dbias else None,
+                                M, N, ldc, ldz, ldo, _DTYPE.get(dc.dtype, 0),
+                                _DTYPE.get(out.dtype if out is not None else dc.dtype, 0),
+                                _DTYPE.get(dbias_dtype, 0), act, stream,
+                                ws.data_ptr() if ws is not None else None, max(need, 0)))
+    return (out if out is not None else dc), db
+
+
+def gemm_epilogue_backward(dc: torch.Tensor, a: torch.Tensor, b: torch.Tensor, preact: torch.Tensor | None = None,
+                           activation: str = "none", dbias: bool = True,
+                           dbias_dtype: torch.dtype = torch.float32, schedule: Schedule | None = None):
+    """Gradients of C = act(A @ B + bias) + residual given dC: returns (dA, dB, dbias).
+
+    dZ = dC * act'(preact) is formed once, rounded to A's type (an operand of the two
+    products that follow); dA = dZ @ B^T and dB = A^T @ dZ have A's and B's type, dbias
+    (None if not asked for) sums the unrounded dZ.  The residual's gradient is dC itself.
+    ``preact`` is what the forward call stored, of dC's type; not needed for "none".
+    """
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[0] or tuple(dc.shape) != (a.shape[0], b.shape[1]):
+        raise ValueError(f"dC {tuple(dc.shape)} is not the gradient of {tuple(a.shape)} @ {tuple(b.shape)}")
+    if a.dtype not in (torch.float16, torch.bfloat16) or b.dtype != a.dtype:
+        raise ValueError("A and B must be fp16 or bf16, of one type")
+    dz, db = act_grad(dc, preact, activation, out_dtype=a.dtype, dbias=dbias, dbias_dtype=dbias_dtype)
+    da = gemm_epilogue(dz, b.t(), schedule=schedule)
+    dw = gemm_epilogue(a.t(), dz, schedule=schedule)
+    return da, dw, db
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+            eps: float = 1e-6, out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+            h: torch.Tensor | None = None):
+    """h = x + residual;  y = h / sqrt(mean(h^2) + eps) * weight, row by row; returns
+    (y, scale, h).
+
+    x [M,N] fp16, bf16 or fp32; ``residual`` [M,N] of x's type; ``weight`` [N], x's type or
+    fp32 (None: 1).  The norm reads the unrounded fp32 sum; h (x itself without a residual)
+    is its rounding to x's type, what the next block adds to and ``rmsnorm_backward`` takes.
+    The tensor given as ``h`` receives it and may be ``residual`` or x (in place).
+    y has ``out_dtype``: x's type (default) or torch.float8_e4m3fn, which adds one fp32
+    ``scale`` per row, max|y| / 448 (at least 2^-100), with y = e4m3 * scale: the operand and
+    scale_a of ``gemm_scaled``.  Else scale is None.
+    """
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix of rows")
+    if h is not None and residual is None:
+        raise ValueError("h is written only with a residual")
+    M, N = x.shape
+    ldx = _rows(x, (M, N), "x")
+    out_dtype = out_dtype or (out.dtype if out is not None else x.dtype)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    dev = _device_of(x, weight, residual, out, h)
+    ldy = _rows(out, (M, N), "out", out_dtype)
+    ldr = ldh = N
+    if residual is not None:
+        ldr = _rows(residual, (M, N), "residual", x.dtype)
+        if h is None:
+            h = torch.empty((M, N), dtype=x.dtype, device=dev)
+        ldh = _rows(h, (M, N), "h", x.dtype)
+    if weight is not None:
+        _vector(weight, N, "weight")
+    scale = torch.empty(M, dtype=torch.float32, device=dev) if out_dtype == torch.float8_e4m3fn else None
+    with _On(dev) as stream:
+        _check(_lib.ts_rmsnorm(x.data_ptr(), residual.data_ptr() if residual is not None else None,
+                               weight.data_ptr() if weight is not None else None, out.data_ptr(),
+                               h.data_ptr() if h is not None else None,
+                               scale.data_ptr() if scale is not None else None, M, N, ldx, ldr, ldy, ldh,
+                               _TORCH_DTYPE.get(x.dtype, 0),
+                               _TORCH_DTYPE[weight.dtype] if weight is not None else TS_F32,
+                               _DTYPE.get(out_dtype, 0), float(eps), stream))
+    return out, scale, (h if h is not None else x)
+
+
+def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,
+                     dh: torch.Tensor | None = None, dweight: bool = True, out: torch.Tensor | None = None):
+    """Gradients of y = h / sqrt(mean(h^2) + eps) * weight given dy; returns (dx, dweight).
+
+    dx = dL/dh + ``dh``, where ``dh`` is the gradient that reaches h along the residual
+    stream (None: 0): the gradient of x and of the residual alike.  dy, h and dh are [M,N]
+    of one type, dx has it too (``out`` may be dy or dh).  dweight has weight's type, summed
+    in fp32 in a fixed order; None without a weight or if ``dweight`` is False.  The e4m3
+    output of the forward pass is differentiated as y itself (straight through).
+    """
+    if dy.dim() != 2:
+        raise ValueError("dy must be a matrix of rows")
+    M, N = dy.shape
+    ldy = _rows(dy, (M, N), "dy")
+    ldh = _rows(h, (M, N), "h", dy.dtype)
+    lds = _rows(dh, (M, N), "dh", dy.dtype) if dh is not None else N
+    if out is None:
+        out = torch.empty((M, N), dtype=dy.dtype, device=dy.device)
+    dev = _device_of(dy, h, weight, dh, out)
+    ldx = _rows(out, (M, N), "out", dy.dtype)
+    dw = None
+    if weight is not None:
+        _vector(weight, N, "weight")
+        if dweight:
+            dw = torch.empty(N, dtype=weight.dtype, device=dev)
+    with _On(dev) as stream:
+        need = _lib.ts_rmsnorm_backward_workspace(M, N) if dw is not None or N > 32768 else 0
+        ws = _scratch(need, dev)
+        _check(_lib.ts_rmsnorm_backward(dy.data_ptr(), h.data_ptr(), weight.data_ptr() if weight is not None else None,
+                                        dh.data_ptr() if dh is not None else None, out.data_ptr(),
+                                        dw.data_ptr() if dw is not None else None, M, N, ldy, ldh, lds, ldx,
+                                        _TORCH_DTYPE.get(dy.dtype, 0),
+                                        _TORCH_DTYPE[weight.dtype] if weight is not None else TS_F32, float(eps),
+                                        stream, ws.data_ptr() if ws is not None else None, max(need, 0)))
+    return out, dw

@@ -1,0 +1,10 @@
+// Kernel instances with the fused epilogue: the 256x256x64 (8 waves) tile, bf16 operands, every
+// operand layout.
+#include "epilogue.hpp"
+#include "internal.hpp"
+
+namespace ts {
+const void* epi_kernels_cfg256w8_bf16(int out_f32, int path, int kind) {
+    return out_f32 ? epi_kernel<Cfg256w8, InBF16, OutF32>(path, kind) : epi_kernel<Cfg256w8, InBF16, OutBF16>(path, kind);
+}
+}  // namespace ts

@@ -1,0 +1,426 @@
+// C-ABI of the product with a fused epilogue (ts_gemm_epilogue): argument checks, operand
+// packing, launch planning and dispatch.  See include/tsgemm.h for the contract.
+#include <hip/hip_runtime.h>
+
+#include <limits.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <map>
+#include <mutex>
+#include <tuple>
+
+#include "../../include/tsgemm.h"
+#include "epilogue.hpp"
+#include "plan.hpp"
+
+namespace ts {
+
+// Copies rows of row_bytes bytes (any alignment, `pitch` apart) to rows of dst_pitch bytes
+// (a multiple of 16), zero behind the data: 16 bytes of the destination per thread.  Runs
+// in front of a product whose operand the direct-to-LDS loads cannot take as it is (its
+// rows not 16-byte aligned, or K not a multiple of 16 bytes, so that a 16-byte chunk would
+// mix the end of a row with the next one).
+typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
+__global__ void __launch_bounds__(256) pack_rows_kernel(const uint8_t* src, long long pitch, uint8_t* dst,
+                                                        long long dst_pitch, int rows, long long row_bytes) {
+    const long long chunks = dst_pitch / 16;
+    const long long n = chunks * rows;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+        const long long r = i / chunks, b = (i - r * chunks) * 16;
+        const uint8_t* s = src + r * pitch + b;
+        const long long left = row_bytes - b;
+        u32x4 v = {0, 0, 0, 0};
+        if (left >= 16) {
+            v = *reinterpret_cast<const u32x4_a1*>(s);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (e < left) v[e >> 2] |= (uint32_t)s[e] << (8 * (e & 3));
+        }
+        *reinterpret_cast<u32x4*>(dst + r * dst_pitch + b) = v;
+    }
+}
+
+__global__ void clear_flags_kernel(int* p, int n) {
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) p[i] = 0;
+}
+
+namespace {
+
+constexpr int64_t kOffsetLimit = 1LL << 30;   // in-tile byte offsets of the direct-to-LDS loads
+constexpr int kSpin = 1 << 24;                // sleeps before a stream-K wait gives up (about a second)
+
+int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+// One operand as the kernel reads it: rows of `ld` elements, either along K (kmaj) or
+// along M / N.
+struct Operand {
+    bool kmaj;
+    int64_t ld;            // elements between stored rows, as given
+    int64_t rows, cols;    // stored rows and their elements
+    bool pack;             // copied to aligned rows first
+    int64_t packed_bytes;
+};
+
+struct EpiPlan {
+    Plan p;
+    int path, kind, out;
+    int es;                // operand element size in bytes
+    Operand a, b;
+    int64_t kp;            // K as the kernel sees it, elements (a multiple of 16 bytes if an operand is kmaj)
+    WorkspaceLayout sk;
+    int64_t off_a, off_b, total;   // workspace offsets of the packed operands, and its size
+};
+
+bool known_type(int32_t t) { return t == TS_F16 || t == TS_BF16 || t == TS_F32 || t == TS_E4M3; }
+
+// Layout of an operand with `rows` x K (A) or K x `rows` (B) logical elements: s_r and
+// s_k are the strides along its rows (M or N) and along K.
+ts_status operand_layout(int64_t rows, int64_t K, int64_t s_r, int64_t s_k, bool kmaj_only, Operand* o) {
+    if (s_r < 0 || s_k < 0) return TS_ERR_INVALID_ARG;
+    const bool k_ok = K <= 1 || s_k == 1;
+    const bool r_ok = rows <= 1 || s_r == 1;
+    if (!k_ok && !r_ok) return TS_ERR_UNSUPPORTED;
+    // a single row along M or N, or a single k: whichever reading its unit stride allows
+    o->kmaj = kmaj_only ? true : (k_ok && r_ok) ? (rows <= 1 ? s_k == 1 : s_r != 1) : k_ok;
+    if (kmaj_only && !k_ok) return TS_ERR_UNSUPPORTED;
+    o->rows = o->kmaj ? rows : K;
+    o->cols = o->kmaj ? K : rows;
+    o->ld = o->kmaj ? s_r : s_k;
+    if (o->rows <= 1) o->ld = o->cols;
+    if (o->ld < o->cols) return TS_ERR_INVALID_ARG;
+    if (o->ld > INT_MAX) return TS_ERR_UNSUPPORTED;
+    o->pack = false;
+    o->packed_bytes = 0;
+    return TS_OK;
+}
+
+// Whether the loads take the operand as it lies; else it is packed.  `tile` is its extent
+// of a tile along the stored rows (rows of M / N, or of K).
+ts_status operand_pack(Operand* o, uintptr_t base, int es, int tile) {
+    if (o->kmaj) {
+        o->pack = base % 16 != 0 || (o->ld * es) % 16 != 0 || (o->cols * es) % 16 != 0 ||
+                  tile * o->ld * es >= kOffsetLimit;
+    } else {
+        o->pack = base % 4 != 0 || o->ld % 2 != 0 || o->cols % 2 != 0 || tile * o->ld * es >= kOffsetLimit;
+    }
+    if (o->pack) {
+        const int64_t pitch = round_up(o->cols * es, 16);
+        if (tile * pitch >= kOffsetLimit) return TS_ERR_UNSUPPORTED;
+        o->packed_bytes = round_up(pitch * o->rows, 256);
+    }
+    return TS_OK;
+}
+
+const void* epi_kernel_of(const EpiPlan& e, int32_t ab) {
+    const int f32 = e.out == TS_F32;
+    if (e.p.cfg == CFG_128) {
+        if (ab == TS_F16) return epi_kernels_cfg128_f16(f32, e.path, e.kind);
+        if (ab == TS_BF16) return epi_kernels_cfg128_bf16(f32, e.path, e.kind);
+        return epi_kernels_cfg128_e4m3(e.out, e.path, e.kind);
+    }
+    if (ab == TS_F16) return epi_kernels_cfg256w8_f16(f32, e.path, e.kind);
+    if (ab == TS_BF16) return epi_kernels_cfg256w8_bf16(f32, e.path, e.kind);
+    return epi_kernels_cfg256w8_e4m3(e.out, e.path, e.kind);
+}
+
+// What planning asks the runtime or computes at length, kept per kernel and per tile grid:
+// workgroups a CU holds, and the order the locality model chooses.
+std::mutex g_cache_mutex;
+std::map<std::pair<int, const void*>, int> g_occupancy;
+struct OrderChoice {
+    int order, group_m, remap, reuse;
+};
+std::map<std::tuple<int, int, int, int, int>, OrderChoice> g_orders;
+constexpr size_t kMaxOrders = 4096;
+
+int occupancy_of(int dev, const void* fn, int threads) {
+    std::lock_guard<std::mutex> lock(g_cache_mutex);
+    auto it = g_occupancy.find({dev, fn});
+    if (it != g_occupancy.end()) return it->second;
+    int n = 0;
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, 0) != hipSuccess || n < 1) {
+        (void)hipGetLastError();
+        n = 1;
+    }
+    g_occupancy[{dev, fn}] = n;
+    return n;
+}
+
+// resolve_grid with the chosen order kept by tile grid.
+ts_status resolve(Plan* p, int cu_count, int ppc, int xcds) {
+    if (!p->auto_order || p->s.num_tiles == 0) return resolve_grid(p, cu_count, ppc, xcds);
+    Plan q = *p;   // the grid does not depend on the order
+    q.auto_order = false;
+    q.s.num_tiles = p->s.num_tiles;
+    const int64_t want = p->mode == TS_MODE_TILED ? p->s.num_tiles
+                                                  : (p->requested_programs ? p->requested_programs : cu_count * ppc);
+    const auto key = std::make_tuple(p->s.nm, p->s.nn, (int)(want < INT_MAX ? want : INT_MAX), cu_count * ppc,
+                                     xcds * 8 + p->mode);
+    OrderChoice c;
+    bool found = false;
+    {
+        std::lock_guard<std::mutex> lock(g_cache_mutex);
+        auto it = g_orders.find(key);
+        if (it != g_orders.end()) {
+            c = it->second;
+            found = true;
+        }
+    }
+    if (!found) {
+        ts_status st = resolve_grid(p, cu_count, ppc, xcds);
+        if (st != TS_OK) return st;
+        c = OrderChoice{p->s.order, p->s.group_m, p->s.remap, p->l2_reuse_pm};
+        std::lock_guard<std::mutex> lock(g_cache_mutex);
+        if (g_orders.size() >= kMaxOrders) g_orders.clear();
+        g_orders[key] = c;
+        return TS_OK;
+    }
+    p->auto_order = false;
+    p->s.order = c.order;
+    p->s.group_m = c.group_m;
+    p->s.remap = c.remap;
+    return resolve_grid(p, cu_count, ppc, xcds);
+}
+
+// Everything but the device: types, layouts, tile, schedule, packing.
+ts_status epi_plan(const void* A, const void* B, int64_t M, int64_t N, int64_t K, int64_t sam, int64_t sak,
+                   int64_t sbk, int64_t sbn, int32_t ab, int32_t c, const ts_schedule* sp, EpiPlan* e) {
+    if (M < 0 || N < 0 || K < 0) return TS_ERR_INVALID_ARG;
+    if (M > INT_MAX || N > INT_MAX || K > INT_MAX) return TS_ERR_UNSUPPORTED;
+    if (!known_type(ab) || !known_type(c)) return TS_ERR_INVALID_ARG;
+    if (ab == TS_F32 || c == TS_E4M3 || (ab == TS_F16 && c == TS_BF16) || (ab == TS_BF16 && c == TS_F16))
+        return TS_ERR_UNSUPPORTED;
+    ts_schedule s = {TS_ORDER_AUTO, 1, TS_MODE_AUTO, 0, 0, TS_TILE_AUTO, TS_INDEX_DIVIDE};
+    if (sp) s = *sp;
+    if (s.order != TS_ORDER_ROW_MAJOR && s.order != TS_ORDER_GROUPED && s.order != TS_ORDER_AUTO)
+        return TS_ERR_INVALID_ARG;
+    if (s.order == TS_ORDER_GROUPED && s.group_m < 1) return TS_ERR_INVALID_ARG;
+    if (s.mode != TS_MODE_TILED && s.mode != TS_MODE_PERSISTENT && s.mode != TS_MODE_CROSSTILE &&
+        s.mode != TS_MODE_STREAMK && s.mode != TS_MODE_AUTO)
+        return TS_ERR_INVALID_ARG;
+    if (s.index_math != TS_INDEX_DIVIDE && s.index_math != TS_INDEX_MULSHIFT) return TS_ERR_INVALID_ARG;
+    if (s.num_programs < 0 || (s.xcd_remap != 0 && s.xcd_remap != 1)) return TS_ERR_INVALID_ARG;
+    if (s.tile_config < TS_TILE_AUTO || s.tile_config > TS_TILE_256x256x64_PP) return TS_ERR_INVALID_ARG;
+    if (s.tile_config != TS_TILE_AUTO && s.tile_config != TS_TILE_128x128x64 && s.tile_config != TS_TILE_256x256x64_W8)
+        return TS_ERR_UNSUPPORTED;
+
+    e->es = ab == TS_E4M3 ? 1 : 2;
+    e->out = c;
+    ts_status st = operand_layout(M, K, sam, sak, ab == TS_E4M3, &e->a);
+    if (st != TS_OK) return st;
+    st = operand_layout(N, K, sbn, sbk, ab == TS_E4M3, &e->b);
+    if (st != TS_OK) return st;
+    e->path = e->a.kmaj ? (e->b.kmaj ? PATH_EDGE_BT : PATH_EDGE) : (e->b.kmaj ? PATH_EDGE_ATBT : PATH_EDGE_AT);
+
+    Plan& p = e->p;
+    p.cfg = s.tile_config != TS_TILE_AUTO ? s.tile_config
+            : cdiv64(M, 256) * cdiv64(N, 256) >= 128 ? CFG_256W8 : CFG_128;
+    p.bm = p.bn = p.cfg == CFG_128 ? 128 : 256;
+    p.bk = 128 / e->es;   // one slice row is 128 bytes
+    st = operand_pack(&e->a, (uintptr_t)A, e->es, e->a.kmaj ? p.bm : p.bk);
+    if (st != TS_OK) return st;
+    st = operand_pack(&e->b, (uintptr_t)B, e->es, e->b.kmaj ? p.bn : p.bk);
+    if (st != TS_OK) return st;
+    e->kp = e->a.kmaj || e->b.kmaj ? round_up(K, 16 / e->es) : K;
+    // the kernels run at least two K steps a tile; slices past K read as zero
+    const int64_t nm = cdiv64(M, p.bm), nn = cdiv64(N, p.bn), ks = std::max<int64_t>(2, cdiv64(e->kp, p.bk));
+    if (nm * nn > INT_MAX / 2) return TS_ERR_UNSUPPORTED;
+    if (s.mode == TS_MODE_AUTO) s.mode = TS_MODE_CROSSTILE;
+    p.mode = s.mode;
+    p.io = 0;
+    p.masked = true;
+    p.path = e->path;
+    p.vec_a = p.vec_b = p.vec_c = 0;
+    p.requested_programs = s.num_programs;
+    p.s.nm = (int)nm;
+    p.s.nn = (int)nn;
+    p.s.ks = (int)ks;
+    p.s.num_tiles = (int)(nm * nn);
+    p.auto_order = s.order == TS_ORDER_AUTO;
+    p.l2_reuse_pm = -1;
+    p.s.order = p.auto_order ? TS_ORDER_ROW_MAJOR : s.order;
+    p.s.group_m = s.order == TS_ORDER_GROUPED ? (int)std::min<int64_t>(s.group_m, std::max<int64_t>(nm, 1)) : 1;
+    p.s.remap = p.auto_order ? 0 : s.xcd_remap;
+    p.s.xcds = 8;
+    p.s.grid = 0;
+    p.s.fastdiv = s.index_math == TS_INDEX_MULSHIFT;
+    p.max_items = 0;
+    e->kind = p.mode == TS_MODE_STREAMK ? EPI_STREAMK : EPI_XTILE;
+    return TS_OK;
+}
+
+// The grid and the workspace; needs the device where the grid does.
+ts_status epi_resolve(EpiPlan* e, int32_t ab, int dev, const DeviceInfo* di) {
+    Plan& p = e->p;
+    int ppc = 0;
+    if (di) ppc = occupancy_of(dev, epi_kernel_of(*e, ab), p.cfg == CFG_128 ? Cfg128::NT : Cfg256w8::NT);
+    ts_status st = di ? resolve(&p, di->cu_count, ppc, di->xcds) : resolve_grid(&p, 0, 0, 8);
+    if (st != TS_OK) return st;
+    e->sk = workspace_layout(p);
+    e->off_a = round_up(e->sk.total, 256);
+    e->off_b = e->off_a + e->a.packed_bytes;
+    e->total = e->off_b + e->b.packed_bytes;
+    return TS_OK;
+}
+
+bool grid_needs_device(const EpiPlan& e) { return e.p.mode != TS_MODE_TILED && e.p.requested_programs == 0; }
+
+ts_status check_epilogue(const ts_epilogue* x, int64_t M, int64_t N, int32_t ab, int32_t c) {
+    if (!x) return TS_OK;
+    const int ce = c == TS_F32 ? 4 : 2;
+    if (x->activation < TS_ACT_NONE || x->activation > TS_ACT_SILU || (x->grad != 0 && x->grad != 1))
+        return TS_ERR_INVALID_ARG;
+    if (x->bias && x->bias_dtype != TS_F16 && x->bias_dtype != TS_BF16 && x->bias_dtype != TS_F32)
+        return TS_ERR_INVALID_ARG;
+    if (x->grad && (!x->preact || x->bias || x->residual)) return TS_ERR_INVALID_ARG;
+    if ((x->scale_a || x->scale_b) && ab != TS_E4M3) return TS_ERR_INVALID_ARG;
+    if (x->residual && M > 1 && x->stride_rm < N) return TS_ERR_INVALID_ARG;
+    if (x->preact && M > 1 && x->stride_pm < N) return TS_ERR_INVALID_ARG;
+    if ((uintptr_t)x->bias % (x->bias_dtype == TS_F32 ? 4 : 2) || (uintptr_t)x->residual % ce ||
+        (uintptr_t)x->preact % ce || (uintptr_t)x->scale_a % 4 || (uintptr_t)x->scale_b % 4)
+        return TS_ERR_ALIGNMENT;
+    return TS_OK;
+}
+
+ts_status launch_pack(const Operand& o, const void* src, int es, char* dst, hipStream_t stream) {
+    const int64_t pitch = round_up(o.cols * es, 16);
+    const int64_t chunks = pitch / 16 * o.rows;
+    const int64_t blocks = std::min<int64_t>((chunks + 255) / 256, 8192);
+    if (blocks == 0) return TS_OK;
+    hipLaunchKernelGGL(pack_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, stream,
+                       static_cast<const uint8_t*>(src), (long long)(o.ld * es), reinterpret_cast<uint8_t*>(dst),
+                       (long long)pitch, (int)o.rows, (long long)(o.cols * es));
+    return hipGetLastError() == hipSuccess ? TS_OK : TS_ERR_HIP;
+}
+
+}  // namespace
+}  // namespace ts
+
+using namespace ts;
+
+extern "C" int64_t ts_gemm_epilogue_workspace(const void* A, const void* B, int64_t M, int64_t N, int64_t K,
+                                              int64_t stride_am, int64_t stride_ak, int64_t stride_bk,
+                                              int64_t stride_bn, int32_t ab_dtype, int32_t c_dtype,
+                                              const ts_schedule* sched) {
+    EpiPlan e;
+    ts_status st = epi_plan(A, B, M, N, K, stride_am, stride_ak, stride_bk, stride_bn, ab_dtype, c_dtype, sched, &e);
+    if (st != TS_OK) return st;
+    if (M == 0 || N == 0) return 0;
+    if (e.kind != EPI_STREAMK) return e.a.packed_bytes + e.b.packed_bytes;
+    int dev = 0;
+    DeviceInfo di;
+    const bool need = grid_needs_device(e);
+    if (need) {
+        st = current_device(&dev, &di);
+        if (st != TS_OK) return st;
+    }
+    st = epi_resolve(&e, ab_dtype, dev, need ? &di : nullptr);
+    return st != TS_OK ? st : e.total;
+}
+
+extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K,
+                                      int64_t stride_am, int64_t stride_ak, int64_t stride_bk, int64_t stride_bn,
+                                      int64_t stride_cm, int64_t stride_cn, int32_t ab_dtype, int32_t c_dtype,
+                                      const ts_epilogue* epi, const ts_schedule* sched, void* stream,
+                                      void* workspace, int64_t workspace_bytes) {
+    EpiPlan e;
+    ts_status st = epi_plan(A, B, M, N, K, stride_am, stride_ak, stride_bk, stride_bn, ab_dtype, c_dtype, sched, &e);
+    if (st != TS_OK) return st;
+    st = check_epilogue(epi, M, N, ab_dtype, c_dtype);
+    if (st != TS_OK) return st;
+    if (workspace_bytes < 0) return TS_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return TS_OK;
+    if (!C || (K > 0 && (!A || !B))) return TS_ERR_INVALID_ARG;
+    if (N > 1 && stride_cn != 1) return TS_ERR_UNSUPPORTED;
+    if (M <= 1) stride_cm = N;
+    if (stride_cm < N) return TS_ERR_INVALID_ARG;
+    if (stride_cm > INT_MAX || (epi && (epi->stride_rm > INT_MAX || epi->stride_pm > INT_MAX)))
+        return TS_ERR_UNSUPPORTED;
+    const int ce = c_dtype == TS_F32 ? 4 : 2;
+    if ((uintptr_t)A % e.es || (uintptr_t)B % e.es || (uintptr_t)C % ce) return TS_ERR_ALIGNMENT;
+
+    auto workspace_ok = [&](int64_t need) {
+        return need == 0 || (workspace && workspace_bytes >= need && (uintptr_t)workspace % 256 == 0);
+    };
+    if (e.kind != EPI_STREAMK && !workspace_ok(e.a.packed_bytes + e.b.packed_bytes)) return TS_ERR_INVALID_ARG;
+    if (e.kind == EPI_STREAMK && !grid_needs_device(e)) {
+        EpiPlan q = e;
+        st = epi_resolve(&q, ab_dtype, 0, nullptr);
+        if (st != TS_OK) return st;
+        if (!workspace_ok(q.total)) return TS_ERR_INVALID_ARG;
+    }
+    int dev;
+    DeviceInfo di;
+    st = current_device(&dev, &di);
+    if (st != TS_OK) return st;
+    st = epi_resolve(&e, ab_dtype, dev, &di);
+    if (st != TS_OK) return st;
+    if (!workspace_ok(e.total)) return TS_ERR_INVALID_ARG;
+
+    const hipStream_t hs = static_cast<hipStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    if (e.sk.total > 0) {
+        const int words = (int)(e.sk.header / 4);
+        hipLaunchKernelGGL(clear_flags_kernel, dim3((words + 255) / 256), dim3(256), 0, hs, reinterpret_cast<int*>(ws),
+                           words);
+        if (hipGetLastError() != hipSuccess) return TS_ERR_HIP;
+    }
+    if (e.a.pack && (st = launch_pack(e.a, A, e.es, ws + e.off_a, hs)) != TS_OK) return st;
+    if (e.b.pack && (st = launch_pack(e.b, B, e.es, ws + e.off_b, hs)) != TS_OK) return st;
+
+    // Sizes along K count 16-bit units (pairs of 8-bit elements).
+    const int unit = 2 / e.es;
+    const int64_t kk = e.kp / unit;
+    EpiArgs g;
+    memset(&g, 0, sizeof g);
+    auto pitch = [&](const Operand& o) {
+        return (o.pack ? round_up(o.cols * e.es, 16) / e.es : o.ld) / unit;
+    };
+    g.A = reinterpret_cast<const uint16_t*>(e.a.pack ? ws + e.off_a : A);
+    g.B = reinterpret_cast<const uint16_t*>(e.b.pack ? ws + e.off_b : B);
+    g.C = C;
+    g.M = (int)M;
+    g.N = (int)N;
+    g.K = (int)kk;
+    // a single row needs no pitch, but the loads of a tile's other rows (past the end,
+    // reading zero) form their offsets with it
+    g.lda = e.a.kmaj && e.a.rows <= 1 ? kk : pitch(e.a);
+    g.ldb = e.b.kmaj && e.b.rows <= 1 ? kk : pitch(e.b);
+    g.ldc = stride_cm;
+    // bytes to the end of the last row, its padding included where it was packed (an odd row
+    // length would cut the last element's dword)
+    auto extent = [&](const Operand& o, int64_t ld) {
+        const int64_t cols = (o.pack ? round_up(o.cols * e.es, 16) / e.es : o.cols) / unit;
+        return K == 0 ? 0 : ((o.rows - 1) * ld + cols) * 2;
+    };
+    g.a_bytes = extent(e.a, g.lda);
+    g.b_bytes = extent(e.b, g.ldb);
+    g.s = e.p.s;
+    if (e.sk.total > 0) {
+        g.sk_flags = reinterpret_cast<int*>(ws);
+        g.sk_err = reinterpret_cast<int*>(ws) + e.p.s.grid;
+        g.sk_part = reinterpret_cast<float*>(ws + e.sk.header);
+    }
+    g.sk_spin = kSpin;
+    if (epi) {
+        g.act = epi->activation;
+        g.grad = epi->grad;
+        g.bias = epi->bias;
+        g.bias_type = epi->bias_dtype;
+        g.aux_in = epi->grad ? epi->preact : epi->residual;
+        g.ld_in = M > 1 ? (epi->grad ? epi->stride_pm : epi->stride_rm) : N;
+        g.aux_out = epi->grad ? nullptr : epi->preact;
+        g.ld_out = M > 1 ? epi->stride_pm : N;
+        g.scale_a = epi->scale_a;
+        g.scale_b = epi->scale_b;
+    }
+    const int threads = e.p.cfg == CFG_128 ? Cfg128::NT : Cfg256w8::NT;
+    void* args[] = {&g};
+    if (hipLaunchKernel(epi_kernel_of(e, ab_dtype), dim3(e.p.s.grid), dim3(threads), args, 0, hs) != hipSuccess) {
+        (void)hipGetLastError();
+        return TS_ERR_HIP;
+    }
+    return TS_OK;
+}

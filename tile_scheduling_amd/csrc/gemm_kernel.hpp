@@ -53,10 +53,12 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 struct InF16 {};
 struct InBF16 {};
+struct InE4M3 {};   // 8-bit operands, carried as 16-bit pairs (see Engine::PAIRS)
 struct OutF16 {};
 struct OutBF16 {};
 struct OutF32 {};
@@ -155,6 +157,30 @@ template <>
 __device__ __forceinline__ f32x16 mfma32<InBF16>(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// The 8-bit product of two 16-byte chunks of each operand: v_mfma_f32_32x32x64 with
+// both operands e4m3 (format code 0) and no block scales.  Each lane's 32 bytes are its
+// chunks of two consecutive sub-steps; A and B are cut alike, so every k meets itself.
+__device__ __forceinline__ f32x16 mfma32_e4m3(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1, f32x16 c) {
+    const i32x8 a = {(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3], (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]};
+    const i32x8 b = {(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3], (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+// The same product of one chunk of each operand, widened to fp16 (which holds every e4m3
+// value exactly) and multiplied by two v_mfma_f32_32x32x16_f16.  The 8-bit matrix
+// instructions align the 8 products of a group to the largest and keep 13 bits below it
+// (measured: 2^16 + 2^t is exact down to t = 3 in a group, and to 2^-7 across groups): a
+// relative error of 1.5e-5, 1 / 14 of an fp16 output's rounding but 250 times an fp32 one's,
+// so fp32 outputs take this form at half the rate.
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ f16x8 widen_e4m3(uint32_t lo, uint32_t hi) {
+    const f16x2 p0 = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false));
+    const f16x2 p1 = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true));
+    const f16x2 p2 = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false));
+    const f16x2 p3 = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true));
+    return f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
 __device__ __forceinline__ uint32_t pack_bits(uint16_t lo, uint16_t hi) { return (uint32_t)lo | ((uint32_t)hi << 16); }
@@ -296,14 +322,24 @@ __device__ __forceinline__ u32x2 lds_read_tr(const char* lds, uint32_t off) {
 // tiles with B stored [N][K] (K contiguous, as A), whose B slices are staged and read
 // exactly as A's; whole tiles with A stored [K][M] (M contiguous, as B), whose A
 // slices are staged and read exactly as B's (with B stored [K][N] or [N][K]).
-enum : int { PATH_FULL = 0, PATH_MASKED = 1, PATH_EDGE = 2, PATH_FULL_BT = 3, PATH_FULL_AT = 4, PATH_FULL_ATBT = 5 };
+// The PATH_EDGE_* paths are the zero-filled edges for the other operand layouts (the
+// kernels with a fused epilogue run on these four edge paths only).
+enum : int { PATH_FULL = 0, PATH_MASKED = 1, PATH_EDGE = 2, PATH_FULL_BT = 3, PATH_FULL_AT = 4, PATH_FULL_ATBT = 5,
+             PATH_EDGE_BT = 6, PATH_EDGE_AT = 7, PATH_EDGE_ATBT = 8 };
 
 template <class Cfg, class TI, class TO, int PATH>
 struct Engine {
     static constexpr bool MASKED = PATH == PATH_MASKED;
-    static constexpr bool EDGE = PATH == PATH_EDGE;
-    static constexpr bool BT = PATH == PATH_FULL_BT || PATH == PATH_FULL_ATBT;   // B stored [N][K]
-    static constexpr bool AT = PATH == PATH_FULL_AT || PATH == PATH_FULL_ATBT;   // A stored [K][M]
+    static constexpr bool EDGE = PATH == PATH_EDGE || PATH >= PATH_EDGE_BT;
+    static constexpr bool BT = PATH == PATH_FULL_BT || PATH == PATH_FULL_ATBT ||
+                               PATH == PATH_EDGE_BT || PATH == PATH_EDGE_ATBT;   // B stored [N][K]
+    static constexpr bool AT = PATH == PATH_FULL_AT || PATH == PATH_FULL_ATBT ||
+                               PATH == PATH_EDGE_AT || PATH == PATH_EDGE_ATBT;   // A stored [K][M]
+    // 8-bit operands: both k-contiguous, so a row of K bytes is a row of K / 2 16-bit
+    // pairs and everything but the product (addresses, slots, fragments) is the 16-bit
+    // engine's.  Sizes along K (g.K, lda, ldb, slices) count pairs.
+    static constexpr bool PAIRS = std::is_same<TI, InE4M3>::value;
+    static constexpr bool WIDE8 = !std::is_same<TO, OutF32>::value;   // 8-bit products; else widened
     static constexpr bool EDGES = PATH != PATH_FULL;   // C stores masked to M x N
     static constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK, NT = Cfg::NT;
     static constexpr int FM = Cfg::FM, FN = Cfg::FN, KCH = Cfg::KCH, SUB = Cfg::SUB;
@@ -321,6 +357,9 @@ struct Engine {
                                     (BK * (RBB / 256)) % NW == 0;
     static constexpr bool FAST = !MASKED && FAST_OK;
     static_assert(!EDGE || FAST, "the edge paths run the direct-to-LDS pipeline");
+    static_assert(!PAIRS || (FAST && BT && !AT && SUB == 4), "8-bit operands: direct-to-LDS, both k-contiguous");
+    typedef Cfg Config;
+    typedef TO OutType;
     static constexpr int BH = RBB / 256;                                // 256-byte pieces of a B row
     static constexpr int A_DMA_N = FAST ? BM * RB / 1024 / NW : 0;   // 1 KiB A loads per wave
     static constexpr int B_DMA_N = !FAST ? 0 : BT ? BN * RB / 1024 / NW   // 1 KiB B loads per wave
@@ -578,7 +617,10 @@ struct Engine {
         if constexpr (AT) {   // as B's [k][n] loads, over A's [k][m] rows
             const int grp = c * NW + wave;
             const int e = ((c * NW * RPD) >> 3) & 1;
-            dma16(r, a_dg[e], (int)((long long)grp * RPD * g.lda * 2), la[SLOT] + grp * 1024);
+            if constexpr (EDGE)
+                dma16(r, a_dg[e] + (uint32_t)(grp * RPD * (int)g.lda * 2), 0, la[SLOT] + grp * 1024);
+            else
+                dma16(r, a_dg[e], (int)((long long)grp * RPD * g.lda * 2), la[SLOT] + grp * 1024);
             return;
         }
         const int grp = c * NW + wave;                     // 8-row group (1 KiB)
@@ -616,7 +658,12 @@ struct Engine {
         if constexpr (BT) {   // as dma_a_one, over B's [n][k] rows
             const int grp = c * NW + wave;
             const int e = ((c * NW) >> 2) & 1;
-            dma16(r, bt_go[e], (int)((long long)grp * 8 * g.ldb * 2), lb[SLOT] + grp * 1024);
+            if constexpr (EDGE) {
+                const uint32_t voff = bt_go[e] + (uint32_t)(grp * 8 * (int)g.ldb * 2);
+                dma16(r, (int)a_kc[e] < klim ? voff : kOutOfRange, 0, lb[SLOT] + grp * 1024);
+            } else {
+                dma16(r, bt_go[e], (int)((long long)grp * 8 * g.ldb * 2), lb[SLOT] + grp * 1024);
+            }
             return;
         }
         const int grp = c * NW + wave;                 // RPD-row group (1 KiB)
@@ -629,6 +676,7 @@ struct Engine {
     template <int SLOT>
     __device__ __forceinline__ void dma_b(int n0, int k, int valid) {
         const __amdgpu_buffer_rsrc_t r = rsrc_b(b_slice(n0, k), valid);
+        if constexpr (EDGE && BT) klim = g.K - k * BK;
 #pragma unroll
         for (int c = 0; c < B_DMA_N; ++c) dma_b_one<SLOT>(c, r);
     }
@@ -790,6 +838,20 @@ struct Engine {
         acc[i][j] = mfma32<TI>(fb[buf][j], fa[buf][i], acc[i][j]);
     }
 
+    // 8-bit operands: block number t of the pair of sub-steps 2 p and 2 p + 1.
+    __device__ __forceinline__ void mfma_pair(int p, int t) {
+        const int i = t / FN, j = t % FN;
+        acc[i][j] = mfma32_e4m3(fb[2 * p][j], fb[2 * p + 1][j], fa[2 * p][i], fa[2 * p + 1][i], acc[i][j]);
+    }
+
+    // 8-bit operands with fp32 output: block number t of sub-step S.
+    __device__ __forceinline__ void mfma_widened(int s, int t) {
+        const int i = t / FN, j = t % FN;
+        const u32x4 a = fa[s][i], b = fb[s][j];
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_e4m3(b[0], b[1]), widen_e4m3(a[0], a[1]), acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_e4m3(b[2], b[3]), widen_e4m3(a[2], a[3]), acc[i][j], 0, 0, 0);
+    }
+
     // MFMAs number [first, last) of a sub-step, in (i, j) order.
     __device__ __forceinline__ void mfmas(int buf, int first, int last) {
 #pragma unroll
@@ -926,7 +988,15 @@ struct Engine {
         constexpr int NT_ = NMF > F_NFR ? NMF : F_NFR;
 #pragma unroll
         for (int t = 0; t < NT_; ++t) {
-            if (t < NMF) mfma_one(S, t);
+            if constexpr (PAIRS && !WIDE8) {
+                if (t < NMF) mfma_widened(S, t);
+            } else if constexpr (PAIRS) {
+                // the blocks of sub-steps S and S ^ 1 in one product of twice the K: half
+                // of them in each of the two, every second slot
+                if (t < NMF && t % 2 == 0) mfma_pair(S >> 1, (S & 1) * (NMF / 2) + t / 2);
+            } else {
+                if (t < NMF) mfma_one(S, t);
+            }
             if (t < F_NFR) read_frag<RSLOT>(RS, t, RS);
             if (S >= 2) {
                 const int gt = (S - 2) * NMF + t;
@@ -1332,13 +1402,25 @@ __device__ __forceinline__ void streamk_wait(const GemmArgs& g, int r, int last)
     __syncthreads();
 }
 
+// What a kernel does with a finished tile: the plain store of the accumulators.  (The
+// fused epilogue, FusedStore, is in epilogue.hpp.)
+struct PlainStore {
+    typedef GemmArgs Args;
+    template <bool PARTS, class E>
+    static __device__ __forceinline__ void store(E& e, const Args&, int m0, int n0, const typename E::Parts& pt) {
+        e.template store_tile<PARTS>(m0, n0, pt);
+    }
+    template <class E>
+    static __device__ __forceinline__ typename E::Parts none() { return typename E::Parts{nullptr, 0, -1}; }
+};
+
 // Tiled, persistent and stream-K modes: for each of the program's work pieces, a
 // full pipeline (prologue loads, K loop with two slices in flight, epilogue).  A
 // piece is a whole tile, or in stream-K mode first the (at most two) pieces of
 // the program's range of split tiles.  One loop runs every kind of piece, so the
 // K loop is instantiated once.
-template <class Cfg, class TI, class TO, int PATH, int MODE>
-__global__ void __launch_bounds__(Cfg::NT) gemm_tiles_kernel(GemmArgs g) {
+template <class Cfg, class TI, class TO, int PATH, int MODE, class EPI = PlainStore>
+__global__ void __launch_bounds__(Cfg::NT) gemm_tiles_kernel(typename EPI::Args g) {
     __shared__ __attribute__((aligned(16))) char lds_a0[Cfg::A_SLOT], lds_a1[Cfg::A_SLOT];
     __shared__ __attribute__((aligned(16))) char lds_b0[Cfg::B_SLOT], lds_b1[Cfg::B_SLOT];
     __shared__ __attribute__((aligned(16))) char lds_c[Cfg::C_BYTES > 0 ? Cfg::C_BYTES : 16];
@@ -1388,9 +1470,9 @@ __global__ void __launch_bounds__(Cfg::NT) gemm_tiles_kernel(GemmArgs g) {
                 pt.last = sk.range_of((tile - sk.dp_tiles + 1) * ks - 1);
                 streamk_wait(g, r, pt.last);
             }
-            e.template store_tile<true>(m0, n0, pt);
+            EPI::template store<true>(e, g, m0, n0, pt);
         } else {
-            e.store_tile(m0, n0);
+            EPI::template store<false>(e, g, m0, n0, PlainStore::none<E>());
         }
     }
     e.drain();
@@ -1508,8 +1590,8 @@ __global__ void __launch_bounds__(Cfg::NT) gemm_flat_kernel(GemmArgs g) {
 // barriers a tile instead of three, and with the fragments read after the epilogue
 // nothing but the accumulators is live through it, so the loop needs no spills (the
 // flattened loop spills).
-template <class Cfg, class TI, class TO, int PATH, bool DEFER = true>
-__global__ void __launch_bounds__(Cfg::NT) gemm_xtile_kernel(GemmArgs g) {
+template <class Cfg, class TI, class TO, int PATH, bool DEFER = true, class EPI = PlainStore>
+__global__ void __launch_bounds__(Cfg::NT) gemm_xtile_kernel(typename EPI::Args g) {
     __shared__ __attribute__((aligned(16))) char lds_a0[Cfg::A_SLOT], lds_a1[Cfg::A_SLOT];
     __shared__ __attribute__((aligned(16))) char lds_b0[Cfg::B_SLOT], lds_b1[Cfg::B_SLOT];
     __shared__ __attribute__((aligned(16))) char lds_c[Cfg::C_BYTES > 0 ? Cfg::C_BYTES : 16];
@@ -1595,7 +1677,7 @@ __global__ void __launch_bounds__(Cfg::NT) gemm_xtile_kernel(GemmArgs g) {
         } else {
             e.template kstep_at<S0 ^ 1, DEFER>(a_ld, b_ld, kl, vl, false, 0);
         }
-        e.store_tile(m0, n0);
+        EPI::template store<false>(e, g, m0, n0, PlainStore::none<E>());
         sc = e.store_class(m0, n0);
         m0 = m1;
         n0 = n1;
