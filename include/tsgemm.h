@@ -424,8 +424,9 @@ typedef struct {
  *   256-byte aligned, contents arbitrary (a stream-K launch clears its own flags);
  *   calls that share one must not overlap in time.  NULL where none is needed.
  *   The current device must be the stream's.
- *   Errors: as ts_gemm; TS_ERR_INVALID_ARG for a bad epilogue; rows of 2^30 bytes per
- *   tile or more (K of 2^21 16-bit elements on the 256 tile): TS_ERR_UNSUPPORTED.
+ *   Errors: as ts_gemm; TS_ERR_INVALID_ARG for a bad epilogue.  TS_ERR_UNSUPPORTED: rows
+ *   of 2^30 bytes per tile or more (K of 2^21 16-bit elements on the 256 tile), row
+ *   strides of C, residual or preact of 2^26 elements or more.
  */
 ts_status ts_gemm_epilogue(const void* A, const void* B, void* C,
                            int64_t M, int64_t N, int64_t K,

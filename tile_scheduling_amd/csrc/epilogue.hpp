@@ -47,84 +47,61 @@ constexpr float kTanhW0 = 1.59576912160573071176f;             // sqrt(8 / pi)
 constexpr float kTanhW1 = 1.59576912160573071176f * 0.044715f;
 constexpr float kInvSqrt2Pi = 0.39894228040143267794f;
 
-template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-    if constexpr (ACT == ACT_RELU) return z < 0.0f ? 0.0f : z;   // NaN stays NaN
-    if constexpr (ACT == ACT_GELU) {
-        const float x = __builtin_fabsf(z);
-        const float q = tail_scaled(x) * __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z);
+// The activation is one wave-uniform number; silu and gelu_tanh are one function with
+// different coefficients: z sigmoid(z (w0 + w1 z^2)).  Calls f(tag) with the family's tag.
+enum : int { FAM_NONE = 0, FAM_RELU = 1, FAM_ERF = 2, FAM_SIGMOID = 3 };
+struct Sigmoid {
+    float w0, w1;
+};
+__device__ __forceinline__ Sigmoid sigmoid_of(int act) {
+    return act == ACT_SILU ? Sigmoid{1.0f, 0.0f} : Sigmoid{kTanhW0, kTanhW1};
+}
+template <int FAM>
+__device__ __forceinline__ float fam_value(float z, Sigmoid c) {
+    if constexpr (FAM == FAM_RELU) return z < 0.0f ? 0.0f : z;   // NaN stays NaN
+    if constexpr (FAM == FAM_ERF) {
+        const float q = tail_scaled(__builtin_fabsf(z)) * __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z);
         return z * (z < 0.0f ? q : 1.0f - q);
     }
-    if constexpr (ACT == ACT_GELU_TANH) return z * sigmoid(z * __builtin_fmaf(kTanhW1 * z, z, kTanhW0));
-    if constexpr (ACT == ACT_SILU) return z * sigmoid(z);
+    if constexpr (FAM == FAM_SIGMOID) return z * sigmoid(z * __builtin_fmaf(c.w1 * z, z, c.w0));
     return z;
 }
-
-template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
-    if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
-    if constexpr (ACT == ACT_GELU) {
-        const float x = __builtin_fabsf(z);
+template <int FAM>
+__device__ __forceinline__ float fam_slope(float z, Sigmoid c) {
+    if constexpr (FAM == FAM_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+    if constexpr (FAM == FAM_ERF) {
         const float e = __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z);
-        const float q = tail_scaled(x) * e;
+        const float q = tail_scaled(__builtin_fabsf(z)) * e;
         return __builtin_fmaf(z * kInvSqrt2Pi, e, z < 0.0f ? q : 1.0f - q);
     }
-    if constexpr (ACT == ACT_GELU_TANH) {
-        const float g = sigmoid(z * __builtin_fmaf(kTanhW1 * z, z, kTanhW0));
-        return __builtin_fmaf(z * (g * (1.0f - g)), __builtin_fmaf(3.0f * kTanhW1 * z, z, kTanhW0), g);
-    }
-    if constexpr (ACT == ACT_SILU) {
-        const float g = sigmoid(z);
-        return g * __builtin_fmaf(z, 1.0f - g, 1.0f);
+    if constexpr (FAM == FAM_SIGMOID) {
+        const float g = sigmoid(z * __builtin_fmaf(c.w1 * z, z, c.w0));
+        return __builtin_fmaf(z * (g * (1.0f - g)), __builtin_fmaf(3.0f * c.w1 * z, z, c.w0), g);
     }
     return 1.0f;
 }
-
-// The activation is one wave-uniform number: a scalar branch per group of E values.
+template <class F>
+__device__ __forceinline__ void with_family(int act, F&& f) {
+    if (act == ACT_RELU) f(std::integral_constant<int, FAM_RELU>{});
+    else if (act == ACT_GELU) f(std::integral_constant<int, FAM_ERF>{});
+    else if (act != ACT_NONE) f(std::integral_constant<int, FAM_SIGMOID>{});
+}
 template <int E>
 __device__ __forceinline__ void act_values(int act, float* v) {
-    switch (act) {
-        case ACT_RELU:
+    const Sigmoid c = sigmoid_of(act);
+    with_family(act, [&](auto fam) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = act_value<ACT_RELU>(v[e]);
-            break;
-        case ACT_GELU:
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = act_value<ACT_GELU>(v[e]);
-            break;
-        case ACT_GELU_TANH:
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = act_value<ACT_GELU_TANH>(v[e]);
-            break;
-        case ACT_SILU:
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = act_value<ACT_SILU>(v[e]);
-            break;
-        default: break;
-    }
+        for (int e = 0; e < E; ++e) v[e] = fam_value<decltype(fam)::value>(v[e], c);
+    });
 }
 // v[e] *= act'(z[e])
 template <int E>
 __device__ __forceinline__ void act_slopes(int act, float* v, const float* z) {
-    switch (act) {
-        case ACT_RELU:
+    const Sigmoid c = sigmoid_of(act);
+    with_family(act, [&](auto fam) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] *= act_slope<ACT_RELU>(z[e]);
-            break;
-        case ACT_GELU:
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[e] *= act_slope<ACT_GELU>(z[e]);
-            break;
-        case ACT_GELU_TANH:
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[e] *= act_slope<ACT_GELU_TANH>(z[e]);
-            break;
-        case ACT_SILU:
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[e] *= act_slope<ACT_SILU>(z[e]);
-            break;
-        default: break;
-    }
+        for (int e = 0; e < E; ++e) v[e] *= fam_slope<decltype(fam)::value>(z[e], c);
+    });
 }
 
 // ---- rows of C's type, any alignment -----------------------------------------------------
@@ -230,6 +207,36 @@ __device__ __forceinline__ float load_any(const void* p, int type, long long i) 
     return __builtin_bit_cast(float, (uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
 }
 
+// E (4 or 8) consecutive elements of a vector of any type; those at or past `valid` keep v.
+template <int E, class TO>
+__device__ __forceinline__ void load_columns_of(const void* p, long long n, int valid, float* v) {
+    constexpr int STEP = Elt<TO>::E < E ? Elt<TO>::E : E;   // 4 or 8 elements an access
+    const typename Elt<TO>::T* q = static_cast<const typename Elt<TO>::T*>(p) + n;
+    float t[8];
+    if (valid >= E) {
+        if constexpr (Elt<TO>::E == 8 && E == 4) {   // 8 bytes
+            typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+            const u32x2 w = *reinterpret_cast<const u32x2_a2*>(q);
+            unpack_row<TO>(u32x4{w[0], w[1], 0, 0}, t);
+        } else {
+#pragma unroll
+            for (int c = 0; c < E; c += STEP) unpack_row<TO>(load_row<TO>(q + c, STEP), t + c);
+        }
+#pragma unroll
+        for (int c = 0; c < E; ++c) v[c] = t[c];
+    } else {
+#pragma unroll
+        for (int c = 0; c < E; ++c)
+            if (c < valid) v[c] = (float)q[c];
+    }
+}
+template <int E>
+__device__ __forceinline__ void load_columns(const void* p, int type, long long n, int valid, float* v) {
+    if (type == ELT_F32) load_columns_of<E, OutF32>(p, n, valid, v);
+    else if (type == ELT_F16) load_columns_of<E, OutF16>(p, n, valid, v);
+    else load_columns_of<E, OutBF16>(p, n, valid, v);
+}
+
 // ---- the tile epilogue -------------------------------------------------------------------
 
 struct EpiArgs : GemmArgs {
@@ -239,172 +246,380 @@ struct EpiArgs : GemmArgs {
     long long ld_in, ld_out;
     const float *scale_a, *scale_b;   // 8-bit operands: M and N fp32 (null: 1)
     int bias_type, act, grad;
+    int stagger;            // sleeps (320 clocks) between the starts of consecutive groups of programs
 };
 
-// E consecutive columns of one row: v holds z (see the top), `in` the row's aux_in
-// elements.  Returns C's elements and, in *pre, preact's.
-template <class TO>
-__device__ __forceinline__ u32x4 epilogue_row(const EpiArgs& g, float* v, u32x4 in, u32x4* pre) {
-    constexpr int E = Elt<TO>::E;
-    if (g.grad) {
-        float z[E];
-        unpack_row<TO>(in, z);
-        act_slopes<E>(g.act, v, z);
-    } else {
-        if (g.aux_out) *pre = pack_row<TO>(v);
-        act_values<E>(g.act, v);
-        if (g.aux_in) {
-            float r[E];
-            unpack_row<TO>(in, r);
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[e] += r[e];
-        }
-    }
-    return pack_row<TO>(v);
+// The launch's arguments, read anew from the kernel argument segment: scalars that only the
+// epilogue needs are then not held (spilled to vector registers) through the K loop.
+__device__ __forceinline__ const EpiArgs& fresh_args() {
+    typedef const __attribute__((address_space(4))) EpiArgs* P;
+    P p = (P)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const EpiArgs*)p;
+}
+// A constant in a register that is not held between its uses.
+__device__ __forceinline__ float fresh(float c) {
+    asm volatile("" : "+v"(c));
+    return c;
 }
 
-// Store of one tile.  Each wave stages 16 rows x 64 columns of fp32 at a time through its
-// own 4 KiB of LDS (the plain store's staging area, 16-byte chunks XOR-swizzled by row)
-// and reads them back row-major, 16 bytes of C's type per lane, so that bias, residual,
-// preact and C all move as whole row segments of 128 or 256 bytes; staging fp32 rather than
-// C's type keeps the epilogue on unrounded sums.  aux_in's rows of a pass are loaded before
-// the pass is staged.  The passes are one rolled loop whose staging part alone is
-// instantiated per pass (its accumulators are fixed registers): with every activation
-// in every pass the code is too long to unroll, and the accumulators end up in memory.
+// Epilogue and store of one tile, in the accumulators' own layout: a lane holds, in block
+// (i, j) of its wave's sub-tile, columns 32 j + 8 q + 4 hk .. + 3 (q = 0 .. 3) of row
+// 32 i + r32.  Scales and bias are applied in place; then a block is taken to 16 registers of
+// its own, worked on there, and staged, rounded, in the wave's 4 KiB of LDS: 32 rows of 128 bytes,
+// the 64 columns of a row of blocks in 16 bits, or 32 columns in fp32, 16-byte chunks
+// XOR-swizzled by row.  From there it leaves as whole 128-byte row segments, 16 bytes a lane;
+// a matrix that is read (residual, preact) comes the other way through the same bytes.
+// The blocks are one rolled loop, in which only the taking of accumulators (fixed registers)
+// has a copy per block: unrolled, with every activation in every copy, the code is too
+// long, and accumulators changed in place behind branches end up spilled.  (An earlier form
+// staged fp32 for all types and decided per row segment on the way out: a dozen branches and
+// twice the LDS traffic per segment, 5 us a 256 x 256 tile.)
 struct FusedStore {
     typedef EpiArgs Args;
-    static constexpr int RS = 16;   // rows a pass
-
-    // Accumulators of pass P (rows 16 P .. 16 P + 15 of the wave's sub-tile) into staging.
-    template <int P, bool PARTS, class E>
-    static __device__ __forceinline__ void stage(E& e, char* st, int r32, int hk, int tt, const typename E::Parts& pt) {
-        typedef typename E::Config Cfg;
-        constexpr int i = P / 2, h = P % 2;
-        const int r = r32 - h * RS;
-        // the empty asm statements keep the compiler from merging the passes' code, which
-        // would select their accumulators by address, in memory
-        asm volatile("" ::"n"(P));
-        if (r >= 0 && r < RS) {
-#pragma unroll
-        for (int j = 0; j < Cfg::FN; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int ch = (8 * j + 2 * q + hk) ^ r;   // columns 32 j + 8 q + 4 hk .. + 3
-                float v[4] = {e.acc[i][j][4 * q], e.acc[i][j][4 * q + 1], e.acc[i][j][4 * q + 2],
-                              e.acc[i][j][4 * q + 3]};
-                if (PARTS) e.add_parts(v, pt, (i * Cfg::FN + j) * 4 + q, tt);
-                *reinterpret_cast<f32x4*>(st + r * 256 + ch * 16) = f32x4{v[0], v[1], v[2], v[3]};
-            }
-        }
-        asm volatile("" ::"n"(P));
+    static constexpr int MIN_WAVES = 2;   // two workgroups of the 128 tile, or one of the 256 tile, on a CU
+    static constexpr bool RENEW = true;
+    // Programs start in eight groups, g.stagger sleeps apart (see stagger_sleeps).
+    static __device__ __forceinline__ void start(const EpiArgs& g) {
+        const int n = ((blockIdx.x >> 3) & 7) * g.stagger;
+        for (int i = 0; i < n; ++i) __builtin_amdgcn_s_sleep(5);
     }
-    template <bool PARTS, class E, int... P>
-    static __device__ __forceinline__ void stage_any(E& e, int p, char* st, int r32, int hk, int tt,
-                                                     const typename E::Parts& pt, std::integer_sequence<int, P...>) {
-        ((p == P ? stage<P, PARTS>(e, st, r32, hk, tt, pt) : (void)0), ...);
-    }
+    static constexpr int NQ = 4;   // quads of a lane in a block
+    static constexpr int NU = 4;   // 16-byte accesses of a lane to the staged 4 KiB
 
-    // What a lane holds for its E columns (n .. n + E - 1 of the tile, `valid` of them
-    // before N) over the passes of a tile.
-    template <class E>
-    struct Columns {
-        typedef Elt<typename E::OutType> L;
-        typedef typename L::T T;
-        static constexpr int LPR = 64 / L::E, RPU = 64 / LPR;   // lanes a row, rows a store instruction
-        static constexpr int NU = RS / RPU;                     // store instructions a pass
-        int row, col, n, valid;
-        float bias[L::E], sb[L::E];
-        const T* in;
-        T *out, *C;
-        u32x4 rows[NU];                                         // aux_in's rows of the pass
+    // What the blocks of a tile share.
+    struct Tile {
+        char* st;         // the wave's staging area
+        int ln, r32, hk;
+        int m, n;         // first row and column of the wave's sub-tile
+        int M, N;
+        bool whole;       // its 64 columns are all before N (wave-uniform)
     };
+    static __device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
+    // Staged bytes: unit u of this lane (row 8 u + ln / 8, chunk ln mod 8), and `bytes` at
+    // byte `at` of row r32.
+    static __device__ __forceinline__ char* unit_lds(const Tile& t, int u) {
+        const int row = 8 * u + (t.ln >> 3);
+        return t.st + row * 128 + (((t.ln & 7) ^ swz(row)) << 4);
+    }
+    static __device__ __forceinline__ char* quad_lds(const Tile& t, int at) {
+        return t.st + t.r32 * 128 + (((at >> 4) ^ swz(t.r32)) << 4) + (at & 15);
+    }
+    // Unit u in a matrix of C's type whose staged part begins at row m, column n: that address
+    // is scalar, the lane's offset 32 bits wide (the host keeps row strides below 2^26).
+    template <class T>
+    static __device__ __forceinline__ T* unit_at(const Tile& t, const void* base, long long ld, int m, int n, int u) {
+        char* p = static_cast<char*>(const_cast<void*>(base)) + ((m + 8 * u) * ld + n) * (long long)sizeof(T);
+        return reinterpret_cast<T*>(p + ((uint32_t)(t.ln >> 3) * (uint32_t)ld * (uint32_t)sizeof(T) + (uint32_t)(t.ln & 7) * 16u));
+    }
 
-    // Store instruction U of a pass: row m of C, staged row rp.
-    template <int U, class E>
-    static __device__ __forceinline__ void row_step(const EpiArgs& g, const Columns<E>& k, const char* st, int mp) {
-        typedef Columns<E> K;
-        typedef typename K::L L;
-        typedef typename E::OutType TO;
-        const int rp = U * K::RPU + k.row;
-        const long long m = mp + U * K::RPU;
-        if (m >= g.M) return;
-        const float sa = E::PAIRS && g.scale_a ? g.scale_a[m] : 1.0f;
-        if (k.valid >= L::E) {
-            float v[L::E];
+    template <class E>
+    static __device__ __forceinline__ Tile tile_of(const E& e, const EpiArgs& g, int m0, int n0) {
+        Tile t;
+        t.ln = E::fresh_lane();   // addresses are formed here, not hoisted over the K loop
+        t.st = e.ldsc + e.wave * E::Config::STAGE_W;
+        t.r32 = t.ln & 31;
+        t.hk = t.ln >> 5;
+        t.m = m0 + e.wm * E::Config::TM;
+        t.n = n0 + e.wn * E::Config::TN;
+        t.M = g.M;
+        t.N = g.N;
+        t.whole = t.n + E::Config::TN <= g.N;
+        return t;
+    }
+
+    // Block B (i = B / FN, j = B mod FN) of the accumulators.  The empty asm statements keep
+    // the compiler from merging the copies for different B, which would select the
+    // accumulators by address, in memory.
+    template <int B, class E>
+    static __device__ __forceinline__ void take(const E& e, float (*v)[4]) {
+        constexpr int i = B / E::FN, j = B % E::FN;
+        asm volatile("" ::"n"(B));
 #pragma unroll
-            for (int c = 0; c < L::E / 4; ++c) {
-                const f32x4 f = *reinterpret_cast<const f32x4*>(st + rp * 256 + ((k.col / 4 + c) ^ rp) * 16);
+        for (int q = 0; q < NQ; ++q)
 #pragma unroll
-                for (int w = 0; w < 4; ++w) v[4 * c + w] = f[w];
+            for (int c = 0; c < 4; ++c) v[q][c] = e.acc[i][j][4 * q + c];
+        asm volatile("" ::"n"(B));
+    }
+    template <class E, int... B>
+    static __device__ __forceinline__ void take_any(int b, const E& e, float (*v)[4], std::integer_sequence<int, B...>) {
+        ((b == B ? take<B>(e, v) : (void)0), ...);
+    }
+    // Scales and bias of this lane's columns in block column j.
+    template <class E>
+    static __device__ __forceinline__ void columns(const EpiArgs& g, const Tile& t, int j, float (*sb)[4], float (*bias)[4]) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            const int n = t.n + 4 * t.hk + 32 * j + 8 * q;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                sb[q][c] = E::PAIRS ? fresh(1.0f) : 1.0f;
+                bias[q][c] = fresh(0.0f);
             }
-#pragma unroll
-            for (int c = 0; c < L::E; ++c) v[c] = (E::PAIRS ? v[c] * (sa * k.sb[c]) : v[c]) + k.bias[c];
-            u32x4 pre;
-            const u32x4 w = epilogue_row<TO>(g, v, k.rows[U], &pre);
-            if (g.aux_out) *reinterpret_cast<typename L::V*>(k.out + m * g.ld_out) = pre;
-            *reinterpret_cast<typename L::V*>(k.C + m * g.ldc) = w;
-        } else {   // the columns before N of a chunk that crosses it, one by one
-#pragma unroll 1
-            for (int c = 0; c < k.valid; ++c) {
-                float v = *reinterpret_cast<const float*>(st + rp * 256 + (((k.col + c) / 4) ^ rp) * 16 +
-                                                          ((k.col + c) & 3) * 4);
-                if (E::PAIRS) v *= sa * (g.scale_b ? g.scale_b[k.n + c] : 1.0f);
-                if (g.bias) v += load_any(g.bias, g.bias_type, k.n + c);
-                const float a = g.aux_in ? (float)k.in[m * g.ld_in + c] : 0.0f;
-                if (g.grad) {
-                    act_slopes<1>(g.act, &v, &a);
-                } else {
-                    if (g.aux_out) k.out[m * g.ld_out + c] = (typename K::T)v;
-                    act_values<1>(g.act, &v);
-                    v += a;
-                }
-                k.C[m * g.ldc + c] = (typename K::T)v;
-            }
+            if (E::PAIRS && g.scale_b) load_columns<4>(g.scale_b, ELT_F32, n, t.whole ? 4 : g.N - n, sb[q]);
+            if (g.bias) load_columns<4>(g.bias, g.bias_type, n, t.whole ? 4 : g.N - n, bias[q]);
         }
     }
-    template <class E, int... U>
-    static __device__ __forceinline__ void pass_steps(const EpiArgs& g, const Columns<E>& k, const char* st, int mp,
-                                                      std::integer_sequence<int, U...>) {
-        (row_step<U, E>(g, k, st, mp), ...);
+    // z in place of the sums, in straight runs (no branch around them): partial sums of a
+    // split tile, scales, bias.
+    template <bool PARTS, class E>
+    static __device__ __forceinline__ void finish_sums(E& e, const EpiArgs& g, const Tile& t, const typename E::Parts& pt) {
+        float sa[E::FM];
+#pragma unroll
+        for (int i = 0; i < E::FM; ++i) {
+            const int m = t.m + 32 * i + t.r32;
+            sa[i] = E::PAIRS && g.scale_a && m < g.M ? g.scale_a[m] : 1.0f;
+        }
+        const int tt = e.wave * 64 + t.ln;
+#pragma unroll
+        for (int j = 0; j < E::FN; ++j) {
+            float sb[NQ][4], bias[NQ][4];
+            columns<E>(g, t, j, sb, bias);
+#pragma unroll
+            for (int i = 0; i < E::FM; ++i)
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    float a[4] = {e.acc[i][j][4 * q], e.acc[i][j][4 * q + 1], e.acc[i][j][4 * q + 2], e.acc[i][j][4 * q + 3]};
+                    if (PARTS) e.add_parts(a, pt, (i * E::FN + j) * 4 + q, tt);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        e.acc[i][j][4 * q + c] = E::PAIRS ? __builtin_fmaf(a[c], sa[i] * sb[q][c], bias[q][c]) : a[c] + bias[q][c];
+                }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    // The staged part of a matrix that begins at (m, n), one unit per u.
+    template <class TO>
+    static __device__ __forceinline__ void fetch(const Tile& t, const void* base, long long ld, int m, int n, u32x4* rows) {
+        typedef typename Elt<TO>::T T;
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            const T* s = unit_at<T>(t, base, ld, m, n, u);
+            rows[u] = u32x4{0, 0, 0, 0};
+            if (m + 8 * u + (t.ln >> 3) < t.M)
+                rows[u] = t.whole ? *reinterpret_cast<const typename Elt<TO>::V*>(s)
+                                  : load_row<TO>(s, t.N - (n + (t.ln & 7) * Elt<TO>::E));
+        }
+    }
+    template <class TO>
+    static __device__ __forceinline__ void flush(const Tile& t, void* base, long long ld, int m, int n) {
+        typedef typename Elt<TO>::T T;
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            const u32x4 w = *reinterpret_cast<const u32x4*>(unit_lds(t, u));
+            if (m + 8 * u + (t.ln >> 3) < t.M) {
+                T* p = unit_at<T>(t, base, ld, m, n, u);
+                if (t.whole)
+                    *reinterpret_cast<typename Elt<TO>::V*>(p) = w;
+                else
+                    store_row<TO>(p, w, t.N - (n + (t.ln & 7) * Elt<TO>::E));
+            }
+        }
     }
 
     template <bool PARTS, class E>
-    static __device__ __forceinline__ void store(E& e, const EpiArgs& g, int m0, int n0,
-                                                 const typename E::Parts& pt) {
+    static __device__ __forceinline__ void store(E& e, const EpiArgs&, int m0, int n0, const typename E::Parts& pt) {
+        const EpiArgs& g = fresh_args();
         typedef typename E::Config Cfg;
-        typedef Columns<E> K;
-        typedef typename K::L L;
-        static_assert(Cfg::TN == 64 && Cfg::STAGE_W == RS * 256, "staging shape");
-        int ln = e.lane, tt = e.tid;   // opaque: addresses are formed here, not hoisted over the K loop
-        asm volatile("" : "+v"(ln));
-        if (PARTS) asm volatile("" : "+v"(tt));
-        char* st = e.ldsc + e.wave * Cfg::STAGE_W;
-        K k;
-        k.row = ln / K::LPR;
-        k.col = (ln % K::LPR) * L::E;
-        k.n = n0 + e.wn * Cfg::TN + k.col;
-        k.valid = g.N - k.n;
-        k.in = static_cast<const typename K::T*>(g.aux_in) + k.n;
-        k.out = static_cast<typename K::T*>(g.aux_out) + k.n;
-        k.C = static_cast<typename K::T*>(g.C) + k.n;
-#pragma unroll
-        for (int c = 0; c < L::E; ++c) {
-            k.bias[c] = g.bias && c < k.valid ? load_any(g.bias, g.bias_type, k.n + c) : 0.0f;
-            k.sb[c] = E::PAIRS && g.scale_b && c < k.valid ? g.scale_b[k.n + c] : 1.0f;
-        }
-        const int mw = m0 + e.wm * Cfg::TM + k.row;
+        typedef typename E::OutType TO;
+        typedef typename Elt<TO>::T T;
+        static_assert(Cfg::TN == 64 && Cfg::STAGE_W == 4096 && Cfg::FN == 2, "staging shape");
+        constexpr int OSZ = sizeof(T);
+        constexpr int JB = OSZ == 2 ? 2 : 1;               // blocks staged together
+        const Tile t = tile_of(e, g, m0, n0);
+        finish_sums<PARTS>(e, g, t, pt);
+        const Sigmoid coeff = sigmoid_of(g.act);
+        // preact first (where it is wanted), then C
 #pragma unroll 1
-        for (int p = 0; p < 2 * Cfg::FM; ++p) {
-            const int mp = mw + p * RS;
+        for (int out = g.aux_out ? 0 : 1; out < 2; ++out) {
+            void* base = out ? g.C : g.aux_out;
+            const long long ld = out ? g.ldc : g.ld_out;
+            const bool read = out && g.aux_in;
+#pragma unroll 1
+            for (int b = 0; b < Cfg::FM * Cfg::FN; ++b) {
+                const int j = b % Cfg::FN;
+                const int m = t.m + 32 * (b / Cfg::FN), n = JB == 2 ? t.n : t.n + 32 * j;   // of the staged part
+                if (read && b % JB == 0) {
+                    u32x4 rows[NU];
+                    fetch<TO>(t, g.aux_in, g.ld_in, m, n, rows);
 #pragma unroll
-            for (int u = 0; u < K::NU; ++u) {
-                const long long m = mp + u * K::RPU;
-                k.rows[u] = u32x4{0, 0, 0, 0};
-                if (g.aux_in && m < g.M && k.valid >= L::E)
-                    k.rows[u] = *reinterpret_cast<const typename L::V*>(k.in + m * g.ld_in);
+                    for (int u = 0; u < NU; ++u) *reinterpret_cast<u32x4*>(unit_lds(t, u)) = rows[u];
+                }
+                float v[NQ][4];
+                take_any(b, e, v, std::make_integer_sequence<int, Cfg::FM * Cfg::FN>{});
+                const int at0 = 4 * t.hk * OSZ + (JB == 2 ? 32 * j * OSZ : 0);
+                if (out && !g.grad)
+                    with_family(g.act, [&](auto fam) {
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) v[q][c] = fam_value<decltype(fam)::value>(v[q][c], coeff);
+                    });
+                if (read) {
+                    float w[NQ][4];
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        float f[8];
+                        if constexpr (OSZ == 4) {
+                            unpack_row<TO>(*reinterpret_cast<const u32x4*>(quad_lds(t, at0 + 8 * q * OSZ)), f);
+                        } else {
+                            const u32x2 h = *reinterpret_cast<const u32x2*>(quad_lds(t, at0 + 8 * q * OSZ));
+                            unpack_row<TO>(u32x4{h[0], h[1], 0, 0}, f);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) w[q][c] = f[c];
+                    }
+                    if (g.grad) {
+                        with_family(g.act, [&](auto fam) {
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) v[q][c] *= fam_slope<decltype(fam)::value>(w[q][c], coeff);
+                        });
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) v[q][c] += w[q][c];
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < NQ; ++q)
+                    Out<TO>::store4(reinterpret_cast<T*>(quad_lds(t, at0 + 8 * q * OSZ)), v[q], 4, true);
+                if (b % JB == JB - 1) flush<TO>(t, base, ld, m, n);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            stage_any<PARTS>(e, p, st, ln & 31, ln >> 5, tt, pt, std::make_integer_sequence<int, 2 * Cfg::FM>{});
-            pass_steps<E>(g, k, st, mp, std::make_integer_sequence<int, K::NU>{});
+        }
+    }
+};
+
+// The same for one activation family and one use of aux_in, for the 256 tile: a tile inside
+// M x N runs as one straight piece of code in which every accumulator, wait and store is fixed
+// at compile time.  A load's wait then leaves the stores issued after it in flight (loads
+// and stores retire in order on one counter; behind a branch the compiler has to wait for
+// all of them), so the rows of aux_in are fetched one staged part ahead.  Tiles on the edge
+// take FusedStore.  Against it, 4096 x 16384, bf16 C: K = 1024 none 124 / 133 us, gelu 156 / 169,
+// residual 143 / 165, gelu with preact 163 / 187; K = 4096 3 to 7 us in 420 to 470 less; fp32 C
+// level without aux_in, 12 % (1024) and 2 % (4096) less with.
+enum : int { AUX_NONE = 0, AUX_RESIDUAL = 1, AUX_GRAD = 2, AUX_PREACT = 3 };
+template <int FAM, int AUX>
+struct SpecialStore {
+    typedef EpiArgs Args;
+    static constexpr int MIN_WAVES = 2;
+    static constexpr bool RENEW = true;
+    typedef FusedStore G;
+    static __device__ __forceinline__ void start(const EpiArgs& g) { G::start(g); }
+    static constexpr int NQ = G::NQ, NU = G::NU;
+    static constexpr bool IN = AUX == AUX_RESIDUAL || AUX == AUX_GRAD;   // aux_in is read
+
+    // A walk over the staged parts of a matrix of C's type: the address of the part's first
+    // row is scalar and moves on from part to part (opaque, or the addresses of all parts are
+    // formed at once and spilled), the lane's offset 32 bits wide.
+    template <class E>
+    struct Walk {
+        typedef typename E::OutType TO;
+        typedef typename Elt<TO>::T T;
+        static constexpr int OSZ = sizeof(T), JB = OSZ == 2 ? 2 : 1;   // blocks in a part
+        static constexpr int NP = E::FM * E::FN / JB;                  // parts of a tile
+        char* p;
+        long long row8;
+        uint32_t lane;
+        __device__ __forceinline__ Walk(const G::Tile& t, const void* base, long long ld)
+            : p(static_cast<char*>(const_cast<void*>(base)) + (t.m * ld + t.n) * (long long)OSZ), row8(8 * ld * OSZ),
+              lane((uint32_t)(t.ln >> 3) * (uint32_t)ld * (uint32_t)OSZ + (uint32_t)(t.ln & 7) * 16u) {}
+        __device__ __forceinline__ typename Elt<TO>::V* unit(int u) const {
+            return reinterpret_cast<typename Elt<TO>::V*>(p + u * row8 + lane);
+        }
+        // to part q + 1 from part q
+        __device__ __forceinline__ void next(int q) {
+            if (JB == 2 || q % E::FN == E::FN - 1)
+                p += 4 * row8 - (JB == 1 ? 128 * (E::FN - 1) : 0);
+            else
+                p += 128;   // 32 fp32 columns on
+            asm volatile("" : "+s"(p));
+        }
+        __device__ __forceinline__ void fetch(u32x4* rows) const {
+#pragma unroll
+            for (int u = 0; u < NU; ++u) rows[u] = *unit(u);
+        }
+    };
+    // z of quad q of block (i, j).
+    template <class E>
+    static __device__ __forceinline__ void z_of(const E& e, int i, int j, int q, const float (*bias)[4], float* v) {
+        static_assert(!E::PAIRS, "16-bit operands (the scales of 8-bit ones cost the registers this form needs)");
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = e.acc[i][j][4 * q + c] + bias[j * NQ + q][c];
+    }
+    template <bool PARTS, class E>
+    static __device__ __forceinline__ void store(E& e, const EpiArgs&, int m0, int n0, const typename E::Parts& pt) {
+        const EpiArgs& g = fresh_args();
+        typedef typename E::OutType TO;
+        typedef typename Elt<TO>::T T;
+        typedef Walk<E> K;
+        if (m0 + E::BM > g.M || n0 + E::BN > g.N) {
+            G::store<PARTS>(e, g, m0, n0, pt);
+            return;
+        }
+        const G::Tile t = G::tile_of(e, g, m0, n0);
+        K in(t, g.aux_in, g.ld_in), pre(t, g.aux_out, g.ld_out), w(t, g.C, g.ldc);
+        u32x4 rows[NU];
+        if constexpr (IN) {
+            in.fetch(rows);
+            in.next(0);
+        }
+        float bias[E::FN * NQ][4], one[NQ][4];
+#pragma unroll
+        for (int j = 0; j < E::FN; ++j) G::template columns<E>(g, t, j, one, bias + j * NQ);
+        const Sigmoid coeff = sigmoid_of(g.act);
+#pragma unroll
+        for (int p = 0; p < K::NP; ++p) {
+            const int i = p * K::JB / E::FN, j0 = (p * K::JB) % E::FN;
+            if constexpr (IN) {
+#pragma unroll
+                for (int u = 0; u < NU; ++u) *reinterpret_cast<u32x4*>(G::unit_lds(t, u)) = rows[u];
+                if (p + 1 < K::NP) {
+                    in.fetch(rows);
+                    in.next(p + 1);
+                }
+            }
+            if constexpr (AUX == AUX_PREACT) {
+#pragma unroll
+                for (int x = 0; x < K::JB * NQ; ++x) {
+                    float v[4];
+                    z_of(e, i, j0 + x / NQ, x % NQ, bias, v);
+                    Out<TO>::store4(reinterpret_cast<T*>(G::quad_lds(t, (4 * t.hk + 32 * (x / NQ) + 8 * (x % NQ)) * K::OSZ)), v, 4, true);
+                }
+#pragma unroll
+                for (int u = 0; u < NU; ++u) *pre.unit(u) = *reinterpret_cast<const u32x4*>(G::unit_lds(t, u));
+                pre.next(p);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int x = 0; x < K::JB * NQ; ++x) {
+                float v[4];
+                z_of(e, i, j0 + x / NQ, x % NQ, bias, v);
+                char* at = G::quad_lds(t, (4 * t.hk + 32 * (x / NQ) + 8 * (x % NQ)) * K::OSZ);
+                if constexpr (AUX != AUX_GRAD) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[c] = fam_value<FAM>(v[c], coeff);
+                }
+                if constexpr (IN) {
+                    float f[8];
+                    if constexpr (K::OSZ == 4) {
+                        unpack_row<TO>(*reinterpret_cast<const u32x4*>(at), f);
+                    } else {
+                        const u32x2 h = *reinterpret_cast<const u32x2*>(at);
+                        unpack_row<TO>(u32x4{h[0], h[1], 0, 0}, f);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[c] = AUX == AUX_GRAD ? v[c] * fam_slope<FAM>(f[c], coeff) : v[c] + f[c];
+                }
+                Out<TO>::store4(reinterpret_cast<T*>(at), v, 4, true);
+            }
+#pragma unroll
+            for (int u = 0; u < NU; ++u) *w.unit(u) = *reinterpret_cast<const u32x4*>(G::unit_lds(t, u));
+            w.next(p);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -413,7 +628,35 @@ struct FusedStore {
 // Kernel instances with the fused epilogue.  The edge paths only (they differ from the
 // whole-tile paths by a compare and a select per load), and two loops: stream-K, and the
 // nested cross-tile loop for every other mode (a program of one tile is its tiled form).
-enum : int { EPI_STREAMK = 1, EPI_XTILE = 2 };   // kernel kinds
+// The special forms of the epilogue are kinds of the second.
+enum : int { EPI_STREAMK = 1, EPI_XTILE = 2, EPI_SPECIAL = 8 };   // EPI_SPECIAL + 4 * AUX_* + FAM_*
+
+template <class Cfg, class TI, class TO, int PATH, int FAM, int AUX>
+const void* epi_special() {
+    return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg, TI, TO, PATH, false, SpecialStore<FAM, AUX>>);
+}
+// The special instances of one type and layout (null: none for this kind).
+template <class Cfg, class TI, class TO, int PATH>
+const void* epi_special_by_kind(int kind) {
+    switch (kind) {
+        case EPI_SPECIAL + 4 * AUX_NONE + FAM_NONE: return epi_special<Cfg, TI, TO, PATH, FAM_NONE, AUX_NONE>();
+        case EPI_SPECIAL + 4 * AUX_NONE + FAM_RELU: return epi_special<Cfg, TI, TO, PATH, FAM_RELU, AUX_NONE>();
+        case EPI_SPECIAL + 4 * AUX_NONE + FAM_ERF: return epi_special<Cfg, TI, TO, PATH, FAM_ERF, AUX_NONE>();
+        case EPI_SPECIAL + 4 * AUX_NONE + FAM_SIGMOID: return epi_special<Cfg, TI, TO, PATH, FAM_SIGMOID, AUX_NONE>();
+        case EPI_SPECIAL + 4 * AUX_RESIDUAL + FAM_NONE: return epi_special<Cfg, TI, TO, PATH, FAM_NONE, AUX_RESIDUAL>();
+        case EPI_SPECIAL + 4 * AUX_RESIDUAL + FAM_SIGMOID: return epi_special<Cfg, TI, TO, PATH, FAM_SIGMOID, AUX_RESIDUAL>();
+        case EPI_SPECIAL + 4 * AUX_PREACT + FAM_ERF: return epi_special<Cfg, TI, TO, PATH, FAM_ERF, AUX_PREACT>();
+        case EPI_SPECIAL + 4 * AUX_PREACT + FAM_SIGMOID: return epi_special<Cfg, TI, TO, PATH, FAM_SIGMOID, AUX_PREACT>();
+        case EPI_SPECIAL + 4 * AUX_GRAD + FAM_ERF: return epi_special<Cfg, TI, TO, PATH, FAM_ERF, AUX_GRAD>();
+        case EPI_SPECIAL + 4 * AUX_GRAD + FAM_SIGMOID: return epi_special<Cfg, TI, TO, PATH, FAM_SIGMOID, AUX_GRAD>();
+        default: return nullptr;
+    }
+}
+// Each in its own translation unit: the 8-wave 256 tile, A [M][K] and B [K][N] or [N][K].
+const void* epi_special_f16_nn(int out_f32, int kind);
+const void* epi_special_f16_nt(int out_f32, int kind);
+const void* epi_special_bf16_nn(int out_f32, int kind);
+const void* epi_special_bf16_nt(int out_f32, int kind);
 
 template <class Cfg, class TI, class TO, int PATH>
 const void* epi_kernel_by_kind(int kind) {
@@ -439,7 +682,7 @@ const void* epi_kernel(int path, int kind) {
             case PATH_EDGE_BT: return epi_kernel_by_kind<Cfg, TI, TO, PATH_EDGE_BT>(kind);
             case PATH_EDGE_AT: return epi_kernel_by_kind<Cfg, TI, TO, PATH_EDGE_AT>(kind);
             case PATH_EDGE_ATBT: return epi_kernel_by_kind<Cfg, TI, TO, PATH_EDGE_ATBT>(kind);
-            default: return epi_kernel_by_kind<Cfg, TI, TO, PATH_EDGE>(kind);
+            default: return epi_kernel_by_kind<Cfg, TI, TO, PATH_EDGE_NN>(kind);
         }
     }
 }

@@ -49,6 +49,8 @@ __global__ void clear_flags_kernel(int* p, int n) {
 namespace {
 
 constexpr int64_t kOffsetLimit = 1LL << 30;   // in-tile byte offsets of the direct-to-LDS loads
+constexpr int64_t kMaxExtent = INT_MAX - 1024;    // rows and columns of the last tile stay ints
+constexpr int64_t kMaxStride = (1LL << 26) - 1;   // 32-bit lane offsets of the epilogue (16 rows of 4 bytes)
 constexpr int kSpin = 1 << 24;                // sleeps before a stream-K wait gives up (about a second)
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
@@ -66,6 +68,7 @@ struct Operand {
 struct EpiPlan {
     Plan p;
     int path, kind, out;
+    int special = 0;       // special form of the epilogue (EPI_SPECIAL + ...), 0: the general one
     int es;                // operand element size in bytes
     Operand a, b;
     int64_t kp;            // K as the kernel sees it, elements (a multiple of 16 bytes if an operand is kmaj)
@@ -113,8 +116,39 @@ ts_status operand_pack(Operand* o, uintptr_t base, int es, int tile) {
     return TS_OK;
 }
 
+// Sleeps (320 clocks, FusedStore::start) between the starts of the eight groups of programs.
+// With fp32 C and a matrix read beside it a 256 tile moves 512 KiB after its K loop, as long as
+// 18 K steps at the copy rate while all CUs do it at once; spread over most of a tile's
+// time, the groups' traffic overlaps the others' products.  Measured with 4 tiles a
+// program (4096 x 16384, residual): K = 512 176 -> 138 us, 1024 222 -> 184, 2048 320 -> 287, 4096
+// 511 -> 532, so up to 32 K steps; with 16-bit C, or without a read, 0 to 10 % slower at every K,
+// so not there.
+int stagger_sleeps(const EpiPlan& e, bool reads) {
+    const SchedArgs& s = e.p.s;
+    if (e.kind != EPI_XTILE || e.p.cfg != CFG_256W8 || e.out != TS_F32 || !reads) return 0;
+    return s.ks <= 32 && s.num_tiles >= 3 * (int64_t)s.grid ? 3 * s.ks / 4 : 0;
+}
+
+// The special form of an epilogue, 0 if it has none.  They exist where the 256 tile runs (see
+// SpecialStore): one use of aux_in or aux_out at most, 16-bit operands, A stored [M][K].
+int special_kind(const ts_epilogue& x) {
+    const int fam = x.activation == TS_ACT_NONE ? FAM_NONE : x.activation == TS_ACT_RELU ? FAM_RELU
+                    : x.activation == TS_ACT_GELU ? FAM_ERF : FAM_SIGMOID;
+    if (!x.grad && x.residual && x.preact) return 0;
+    const int aux = x.grad ? AUX_GRAD : x.residual ? AUX_RESIDUAL : x.preact ? AUX_PREACT : AUX_NONE;
+    return EPI_SPECIAL + 4 * aux + fam;
+}
+
 const void* epi_kernel_of(const EpiPlan& e, int32_t ab) {
     const int f32 = e.out == TS_F32;
+    if (e.special && e.kind == EPI_XTILE && e.p.cfg == CFG_256W8) {
+        const void* fn = nullptr;
+        if (e.path == PATH_EDGE_NN)
+            fn = ab == TS_F16 ? epi_special_f16_nn(f32, e.special) : ab == TS_BF16 ? epi_special_bf16_nn(f32, e.special) : nullptr;
+        if (e.path == PATH_EDGE_BT)
+            fn = ab == TS_F16 ? epi_special_f16_nt(f32, e.special) : ab == TS_BF16 ? epi_special_bf16_nt(f32, e.special) : nullptr;
+        if (fn) return fn;
+    }
     if (e.p.cfg == CFG_128) {
         if (ab == TS_F16) return epi_kernels_cfg128_f16(f32, e.path, e.kind);
         if (ab == TS_BF16) return epi_kernels_cfg128_bf16(f32, e.path, e.kind);
@@ -188,7 +222,7 @@ ts_status resolve(Plan* p, int cu_count, int ppc, int xcds) {
 ts_status epi_plan(const void* A, const void* B, int64_t M, int64_t N, int64_t K, int64_t sam, int64_t sak,
                    int64_t sbk, int64_t sbn, int32_t ab, int32_t c, const ts_schedule* sp, EpiPlan* e) {
     if (M < 0 || N < 0 || K < 0) return TS_ERR_INVALID_ARG;
-    if (M > INT_MAX || N > INT_MAX || K > INT_MAX) return TS_ERR_UNSUPPORTED;
+    if (M > kMaxExtent || N > kMaxExtent || K > kMaxExtent) return TS_ERR_UNSUPPORTED;
     if (!known_type(ab) || !known_type(c)) return TS_ERR_INVALID_ARG;
     if (ab == TS_F32 || c == TS_E4M3 || (ab == TS_F16 && c == TS_BF16) || (ab == TS_BF16 && c == TS_F16))
         return TS_ERR_UNSUPPORTED;
@@ -212,7 +246,7 @@ ts_status epi_plan(const void* A, const void* B, int64_t M, int64_t N, int64_t K
     if (st != TS_OK) return st;
     st = operand_layout(N, K, sbn, sbk, ab == TS_E4M3, &e->b);
     if (st != TS_OK) return st;
-    e->path = e->a.kmaj ? (e->b.kmaj ? PATH_EDGE_BT : PATH_EDGE) : (e->b.kmaj ? PATH_EDGE_ATBT : PATH_EDGE_AT);
+    e->path = e->a.kmaj ? (e->b.kmaj ? PATH_EDGE_BT : PATH_EDGE_NN) : (e->b.kmaj ? PATH_EDGE_ATBT : PATH_EDGE_AT);
 
     Plan& p = e->p;
     p.cfg = s.tile_config != TS_TILE_AUTO ? s.tile_config
@@ -330,13 +364,16 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
     if (st != TS_OK) return st;
     st = check_epilogue(epi, M, N, ab_dtype, c_dtype);
     if (st != TS_OK) return st;
+    const ts_epilogue plain = {};
+    e.special = special_kind(epi ? *epi : plain);
     if (workspace_bytes < 0) return TS_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return TS_OK;
     if (!C || (K > 0 && (!A || !B))) return TS_ERR_INVALID_ARG;
     if (N > 1 && stride_cn != 1) return TS_ERR_UNSUPPORTED;
     if (M <= 1) stride_cm = N;
     if (stride_cm < N) return TS_ERR_INVALID_ARG;
-    if (stride_cm > INT_MAX || (epi && (epi->stride_rm > INT_MAX || epi->stride_pm > INT_MAX)))
+    if (M > 1 && (stride_cm > kMaxStride || (epi && ((epi->residual && epi->stride_rm > kMaxStride) ||
+                                                     (epi->preact && epi->stride_pm > kMaxStride)))))
         return TS_ERR_UNSUPPORTED;
     const int ce = c_dtype == TS_F32 ? 4 : 2;
     if ((uintptr_t)A % e.es || (uintptr_t)B % e.es || (uintptr_t)C % ce) return TS_ERR_ALIGNMENT;
@@ -416,6 +453,7 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
         g.scale_a = epi->scale_a;
         g.scale_b = epi->scale_b;
     }
+    g.stagger = stagger_sleeps(e, g.aux_in != nullptr);
     const int threads = e.p.cfg == CFG_128 ? Cfg128::NT : Cfg256w8::NT;
     void* args[] = {&g};
     if (hipLaunchKernel(epi_kernel_of(e, ab_dtype), dim3(e.p.s.grid), dim3(threads), args, 0, hs) != hipSuccess) {

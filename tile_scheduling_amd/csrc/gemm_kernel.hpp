@@ -322,10 +322,10 @@ __device__ __forceinline__ u32x2 lds_read_tr(const char* lds, uint32_t off) {
 // tiles with B stored [N][K] (K contiguous, as A), whose B slices are staged and read
 // exactly as A's; whole tiles with A stored [K][M] (M contiguous, as B), whose A
 // slices are staged and read exactly as B's (with B stored [K][N] or [N][K]).
-// The PATH_EDGE_* paths are the zero-filled edges for the other operand layouts (the
-// kernels with a fused epilogue run on these four edge paths only).
+// The PATH_EDGE_* paths are the zero-filled edges for every operand layout, for the kernels
+// with a fused epilogue; PATH_EDGE_NN is PATH_EDGE with the load offsets of STEP_OFFS.
 enum : int { PATH_FULL = 0, PATH_MASKED = 1, PATH_EDGE = 2, PATH_FULL_BT = 3, PATH_FULL_AT = 4, PATH_FULL_ATBT = 5,
-             PATH_EDGE_BT = 6, PATH_EDGE_AT = 7, PATH_EDGE_ATBT = 8 };
+             PATH_EDGE_BT = 6, PATH_EDGE_AT = 7, PATH_EDGE_ATBT = 8, PATH_EDGE_NN = 9 };
 
 template <class Cfg, class TI, class TO, int PATH>
 struct Engine {
@@ -338,6 +338,18 @@ struct Engine {
     // 8-bit operands: both k-contiguous, so a row of K bytes is a row of K / 2 16-bit
     // pairs and everything but the product (addresses, slots, fragments) is the 16-bit
     // engine's.  Sizes along K (g.K, lda, ldb, slices) count pairs.
+    // Edge paths of the 8-wave tile: a K step forms the per-lane offset of its first A and
+    // first B load, with the out-of-range bit of chunks past K in it, and each further load
+    // adds the distance of a load group.  Held per load instead (PATH_EDGE), the eight
+    // offsets cost eight registers that the loop does not have: the 8-bit kernel then
+    // reloads spilled ones inside the K step, and every such reload waits for the loads in
+    // flight (4096 x 16384 x 4096: 356 us against the 128 tile's 274).
+    static constexpr bool STEP_OFFS = PATH >= PATH_EDGE_BT && Cfg::NT == 512;
+    // With them, the lane offsets of fragment reads carry the place of their operand's slots
+    // in LDS (the compiler lays out staging, A0, A1, B0, B1), so that both slots are reached
+    // by the 16-bit immediate of one register; only the cost depends on that layout.
+    static constexpr int A_BIAS = STEP_OFFS ? Cfg::C_BYTES : 0;
+    static constexpr int B_BIAS = STEP_OFFS ? Cfg::C_BYTES + Cfg::A_BYTES : 0;
     static constexpr bool PAIRS = std::is_same<TI, InE4M3>::value;
     static constexpr bool WIDE8 = !std::is_same<TO, OutF32>::value;   // 8-bit products; else widened
     static constexpr bool EDGES = PATH != PATH_FULL;   // C stores masked to M x N
@@ -397,6 +409,8 @@ struct Engine {
     uint32_t a_go[2], b_go;   // A: [c&1] of the load / chunk index c
     uint32_t bt_go[2];        // PATH_FULL_BT: B's load offsets, as a_go
     uint32_t a_kc[2];         // edge paths: first k (element) of the A chunk a_go[e] points at
+    uint32_t a_off = 0, b_off = 0;   // STEP_OFFS: offset of the next A and B load
+    uint32_t k_row = 0, k_chunk = 0; // STEP_OFFS: lane / 8, and the byte its loads take of a k-contiguous row
     int klim = 0;             // edge paths: k elements of the A slice being loaded that exist
     bool b_active;        // this thread owns a B loader block
 
@@ -412,6 +426,23 @@ struct Engine {
         wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         wm = wave / Cfg::WN;
         wn = wave % Cfg::WN;
+        lane_offsets();
+    }
+    // The lane's number within the wave, formed anew at each call (opaque): nothing of it is
+    // held in between.
+    static __device__ __forceinline__ int fresh_lane() {
+        int l = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+        asm volatile("" : "+v"(l));
+        return l;
+    }
+    // The per-lane offsets again: after an epilogue, so that they hold no registers through it
+    // (what is live there and does not fit would be spilled, and reloaded in every K step).
+    __device__ __forceinline__ void renew_lane_offsets() {
+        lane = fresh_lane();
+        tid = wave * 64 + lane;
+        lane_offsets();
+    }
+    __device__ __forceinline__ void lane_offsets() {
         const int r32 = lane & 31, hk = lane >> 5;
         // Rows of [m][k] (and, on the register path, [n][k]) slices are swizzled by
         // swz(r) = (r ^ (r >> 3)) mod KCH.  A fragment row is (32-aligned base) +
@@ -521,6 +552,23 @@ struct Engine {
                 }
             }
         }
+        if constexpr (STEP_OFFS) {
+            k_row = (uint32_t)(lane >> 3);
+            k_chunk = 2 * a_kc[0];
+            if (!AT || BT) {
+                asm volatile("" : "+v"(k_row));
+                asm volatile("" : "+v"(k_chunk));
+            }
+#pragma unroll
+            for (int s = 0; s < SUB; ++s) {
+                a_rd[s] += A_BIAS;
+                b_rd[s] += B_BIAS;
+            }
+#pragma unroll
+            for (int u = 0; u < NIA; ++u) at_rd[u] += A_BIAS;
+#pragma unroll
+            for (int u = 0; u < NJB; ++u) bt_rd[u] += B_BIAS;
+        }
         // Keep the lane offsets opaque: otherwise their compile-time parts (the B
         // region starts at 64 KiB or more) are folded into per-access constants too
         // large for the 16-bit LDS offset field, and every access needs its own
@@ -597,6 +645,13 @@ struct Engine {
     // The count is clamped to [0, 2^31 - 16], a multiple of 4; the in-tile offsets
     // of the edge path stay below 2^30.
     static __device__ __forceinline__ int clamp_records(long long left) {
+        if constexpr (STEP_OFFS) {
+            // with scalar shifts and masks: a compare and select takes vector registers for
+            // its constants, all through the loop
+            long long d = (left & ~(left >> 63)) - 0x7ffffff0LL;
+            asm("" : "+s"(d));
+            return 0x7ffffff0 + (int)(d & (d >> 63));
+        }
         return (int)(left < 0 ? 0 : left < 0x7ffffff0LL ? left : 0x7ffffff0LL);
     }
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_a(long long off, int valid) const {
@@ -610,10 +665,30 @@ struct Engine {
     // A per-lane offset no record count reaches: the load reads zero.
     static constexpr uint32_t kOutOfRange = 0x80000000u;
 
+    // STEP_OFFS: the offsets of a K step's first loads, for the slice klim was set for.  The
+    // load groups of the 8-wave tile all have bit 2 of the group (k-contiguous) or bit 3 of
+    // the row (else) of group 0, so one offset per operand serves them all.
+    __device__ __forceinline__ void step_offsets() {
+        const uint32_t past = (uint32_t)(2 * klim - 1 - (int)k_chunk) & kOutOfRange;   // the sign bit
+        uint32_t row = (uint32_t)wave;
+        asm volatile("" : "+s"(row));   // keeps the offsets from being formed once for all steps
+        // k-contiguous: stored row 8 wave + lane / 8 of the tile (row strides are below 2^21
+        // elements, so 24-bit factors), swizzled chunk lane mod 8
+        const uint32_t krow = k_row + 8 * row;
+        a_off = AT ? a_dg[0] + row * (uint32_t)(RPD * (int)g.lda * 2)
+                   : (__umul24(krow, (uint32_t)g.lda * 2) + k_chunk) | past;
+        b_off = BT ? (__umul24(krow, (uint32_t)g.ldb * 2) + k_chunk) | past
+                   : b_dg[0] + row * (uint32_t)(RPD * (int)g.ldb * 2);
+    }
     // Fast path: 1 KiB A load number c of this wave, into A slot `slot`.  Edge
     // paths: chunks at or past k = klim of the slice read as zero.
     template <int SLOT>
     __device__ __forceinline__ void dma_a_one(int c, const __amdgpu_buffer_rsrc_t& r) {
+        if constexpr (STEP_OFFS) {
+            dma16(r, a_off, 0, la[SLOT] + (c * NW + wave) * 1024);
+            if (c + 1 < A_DMA_N) a_off += (uint32_t)(NW * (AT ? RPD : 8) * (int)g.lda * 2);
+            return;
+        }
         if constexpr (AT) {   // as B's [k][n] loads, over A's [k][m] rows
             const int grp = c * NW + wave;
             const int e = ((c * NW * RPD) >> 3) & 1;
@@ -640,6 +715,7 @@ struct Engine {
     __device__ __forceinline__ void dma_a(int m0, int k, int valid) {
         const __amdgpu_buffer_rsrc_t r = rsrc_a(a_slice(m0, k), valid);
         if constexpr (EDGE) klim = g.K - k * BK;
+        if constexpr (STEP_OFFS) step_offsets();
 #pragma unroll
         for (int c = 0; c < A_DMA_N; ++c) dma_a_one<SLOT>(c, r);
     }
@@ -655,6 +731,11 @@ struct Engine {
     }
     template <int SLOT>
     __device__ __forceinline__ void dma_b_one(int c, const __amdgpu_buffer_rsrc_t& r) {
+        if constexpr (STEP_OFFS) {
+            dma16(r, b_off, 0, lb[SLOT] + (c * NW + wave) * 1024);
+            if (c + 1 < B_DMA_N) b_off += (uint32_t)(NW * (BT ? 8 : RPD) * (int)g.ldb * 2);
+            return;
+        }
         if constexpr (BT) {   // as dma_a_one, over B's [n][k] rows
             const int grp = c * NW + wave;
             const int e = ((c * NW) >> 2) & 1;
@@ -677,6 +758,7 @@ struct Engine {
     __device__ __forceinline__ void dma_b(int n0, int k, int valid) {
         const __amdgpu_buffer_rsrc_t r = rsrc_b(b_slice(n0, k), valid);
         if constexpr (EDGE && BT) klim = g.K - k * BK;
+        if constexpr (STEP_OFFS) step_offsets();
 #pragma unroll
         for (int c = 0; c < B_DMA_N; ++c) dma_b_one<SLOT>(c, r);
     }
@@ -791,12 +873,20 @@ struct Engine {
     template <int SLOT>
     __device__ __forceinline__ u32x4 read_a(int s, int i) const {
         if constexpr (AT) {   // two transpose reads, as read_b's
+            if constexpr (STEP_OFFS) {
+                const long long off = (long long)at_rd[i & 3] + ((i >> 2) * 256 + 16 * s * RBB - A_BIAS);
+                const u32x2 lo = lds_read_tr(la[SLOT] + off, 0);
+                const u32x2 hi = lds_read_tr(la[SLOT] + (off + 4 * RBB), 0);
+                return u32x4{lo[0], lo[1], hi[0], hi[1]};
+            }
             const char* tb = la[SLOT] + (i >> 2) * 256 + 16 * s * RBB;
             const u32x2 lo = lds_read_tr(tb, at_rd[i & 3]);
             const u32x2 hi = lds_read_tr(tb + 4 * RBB, at_rd[i & 3]);
             return u32x4{lo[0], lo[1], hi[0], hi[1]};
         }
         const char* base = la[SLOT];
+        if constexpr (STEP_OFFS)
+            return lds_read16(base + ((long long)a_rd[(i & 1) ? (s ^ 2) : s] + (i * 32 * RB - A_BIAS)), 0);
         return lds_read16(base, a_rd[(KCH == 8 && (i & 1)) ? (s ^ 2) : s] + i * 32 * RB);
     }
 
@@ -804,11 +894,19 @@ struct Engine {
     template <int SLOT>
     __device__ __forceinline__ u32x4 read_b(int s, int j) const {
         if (FAST && !BT) {   // two transpose reads: k offsets 0-3 and 4-7 of the lane's half
+            if constexpr (STEP_OFFS) {
+                const long long off = (long long)bt_rd[j & 3] + ((j >> 2) * 256 + 16 * s * RBB - B_BIAS);
+                const u32x2 lo = lds_read_tr(lb[SLOT] + off, 0);
+                const u32x2 hi = lds_read_tr(lb[SLOT] + (off + 4 * RBB), 0);
+                return u32x4{lo[0], lo[1], hi[0], hi[1]};
+            }
             const char* base = lb[SLOT] + (j >> 2) * 256 + 16 * s * RBB;
             const u32x2 lo = lds_read_tr(base, bt_rd[j & 3]);
             const u32x2 hi = lds_read_tr(base + 4 * RBB, bt_rd[j & 3]);
             return u32x4{lo[0], lo[1], hi[0], hi[1]};
         }
+        if constexpr (STEP_OFFS)
+            return lds_read16(lb[SLOT] + ((long long)b_rd[(j & 1) ? (s ^ 2) : s] + (j * 32 * RB - B_BIAS)), 0);
         return lds_read16(lb[SLOT], b_rd[(KCH == 8 && (j & 1)) ? (s ^ 2) : s] + j * 32 * RB);
     }
 
@@ -1053,6 +1151,7 @@ struct Engine {
             barrier_behind_stores<0>(sc);
         else
             barrier_after_loads<0>();
+        if constexpr (STEP_OFFS) step_offsets();
         fast_sub<SLOT, 2>(ra_, rb_);
         fast_sub<SLOT, 3>(ra_, rb_);
     }
@@ -1406,6 +1505,9 @@ __device__ __forceinline__ void streamk_wait(const GemmArgs& g, int r, int last)
 // fused epilogue, FusedStore, is in epilogue.hpp.)
 struct PlainStore {
     typedef GemmArgs Args;
+    static constexpr int MIN_WAVES = 0;   // waves per SIMD the registers must allow (0: no demand)
+    static __device__ __forceinline__ void start(const Args&) {}
+    static constexpr bool RENEW = false;  // form the engine's lane offsets again after the store
     template <bool PARTS, class E>
     static __device__ __forceinline__ void store(E& e, const Args&, int m0, int n0, const typename E::Parts& pt) {
         e.template store_tile<PARTS>(m0, n0, pt);
@@ -1420,7 +1522,8 @@ struct PlainStore {
 // the program's range of split tiles.  One loop runs every kind of piece, so the
 // K loop is instantiated once.
 template <class Cfg, class TI, class TO, int PATH, int MODE, class EPI = PlainStore>
-__global__ void __launch_bounds__(Cfg::NT) gemm_tiles_kernel(typename EPI::Args g) {
+__global__ void __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(EPI::MIN_WAVES)))
+gemm_tiles_kernel(typename EPI::Args g) {
     __shared__ __attribute__((aligned(16))) char lds_a0[Cfg::A_SLOT], lds_a1[Cfg::A_SLOT];
     __shared__ __attribute__((aligned(16))) char lds_b0[Cfg::B_SLOT], lds_b1[Cfg::B_SLOT];
     __shared__ __attribute__((aligned(16))) char lds_c[Cfg::C_BYTES > 0 ? Cfg::C_BYTES : 16];
@@ -1471,6 +1574,7 @@ __global__ void __launch_bounds__(Cfg::NT) gemm_tiles_kernel(typename EPI::Args 
                 streamk_wait(g, r, pt.last);
             }
             EPI::template store<true>(e, g, m0, n0, pt);
+            if constexpr (EPI::RENEW) e.renew_lane_offsets();
         } else {
             EPI::template store<false>(e, g, m0, n0, PlainStore::none<E>());
         }
@@ -1591,7 +1695,8 @@ __global__ void __launch_bounds__(Cfg::NT) gemm_flat_kernel(GemmArgs g) {
 // nothing but the accumulators is live through it, so the loop needs no spills (the
 // flattened loop spills).
 template <class Cfg, class TI, class TO, int PATH, bool DEFER = true, class EPI = PlainStore>
-__global__ void __launch_bounds__(Cfg::NT) gemm_xtile_kernel(typename EPI::Args g) {
+__global__ void __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(EPI::MIN_WAVES)))
+gemm_xtile_kernel(typename EPI::Args g) {
     __shared__ __attribute__((aligned(16))) char lds_a0[Cfg::A_SLOT], lds_a1[Cfg::A_SLOT];
     __shared__ __attribute__((aligned(16))) char lds_b0[Cfg::B_SLOT], lds_b1[Cfg::B_SLOT];
     __shared__ __attribute__((aligned(16))) char lds_c[Cfg::C_BYTES > 0 ? Cfg::C_BYTES : 16];
@@ -1626,6 +1731,7 @@ __global__ void __launch_bounds__(Cfg::NT) gemm_xtile_kernel(typename EPI::Args 
         const int grp = (blockIdx.x >> 3) & 7;
         for (int i = 0; i < grp; ++i) __builtin_amdgcn_s_sleep(32);
     }
+    EPI::start(g);
     e.prologue_loads(typename E::Next{m0, 0, -1, n0, 0, -1}, typename E::Next{m0, 1, -1, n0, 1, -1});
     if constexpr (!DEFER) e.template barrier_after_loads<E::NLD>();   // the first slice has landed
     const long long a_ks = e.a_kstride(), b_ks = e.b_kstride();
@@ -1678,6 +1784,7 @@ __global__ void __launch_bounds__(Cfg::NT) gemm_xtile_kernel(typename EPI::Args 
             e.template kstep_at<S0 ^ 1, DEFER>(a_ld, b_ld, kl, vl, false, 0);
         }
         EPI::template store<false>(e, g, m0, n0, PlainStore::none<E>());
+        if constexpr (EPI::RENEW) e.renew_lane_offsets();
         sc = e.store_class(m0, n0);
         m0 = m1;
         n0 = n1;
