@@ -54,6 +54,39 @@ def test_forward_shapes_and_layouts(M, N, K, layout):
         R.check(pre, z, zerr + R.rounded(z.abs() + zerr, out), "preact")
 
 
+@pytest.mark.parametrize("layout", ["nn", "nt"])
+@pytest.mark.parametrize("N,K", [(1, 1), (15, 31), (16, 64), (70, 33), (257, 1000), (1000, 4200), (33000, 96), (40, 9000)])
+def test_few_rows(N, K, layout):
+    # one token to 32 rows: the one-pass kernels, and the tile kernels on the same call
+    for i, M in enumerate((1, 2, 13, 16, 17, 32)):
+        dtype, out = [(H, H), (B, F), (B, B), (H, F)][i % 4]
+        name = R.ACTS[i % 5]
+        n = R.gen(M + N + K)
+        a, b, ad, bd = operands(M, N, K, dtype, layout, M * N + K, pad=i, offset=i)
+        bias, res = n(N), n(M, N).to(out)
+        rd, _ = R.padded(res, "cuda", 3, 1)
+        pd, pbuf = R.padded(torch.zeros(M, N).to(out), "cuda", 2, 1, fill=7.0)
+        cd, cbuf = R.padded(torch.zeros(M, N).to(out), "cuda", 5, 0, fill=7.0)
+        say(M, N, K, layout, dtype, out, name)
+        z, zerr = R.product(a, b, bias)
+        want, bound = R.forward(z, zerr, name, res, out)
+        for sched in (None, ts.Schedule(order="auto", mode="crosstile")):
+            cd.zero_()
+            pd.zero_()
+            ts.gemm_epilogue(ad, bd, bias=bias.cuda(), activation=name, residual=rd, preact=pd, out=cd, schedule=sched)
+            R.check(cd, want, bound, f"C {sched}")
+            R.check(pd, z, zerr + R.rounded(z.abs() + zerr, out), f"preact {sched}")
+        for buf, v in ((cbuf, cd), (pbuf, pd)):
+            v.fill_(7.0)
+            assert bool((buf == 7.0).all())
+        zz = n(M, N).to(out)
+        got = ts.gemm_dact(ad, bd, zz.cuda(), "gelu")
+        p, perr = R.product(a, b)
+        s = R.slope(zz.double(), "gelu")
+        err = 1.2 * perr + R.ACT_ERR * (zz.double().abs() + 1) * p.abs()
+        R.check(got, p * s, err + R.rounded((p * s).abs() + err, out), "dact")
+
+
 @pytest.mark.parametrize("pad,offset", [(0, 1), (1, 0), (3, 5), (8, 8), (2, 2)])
 @pytest.mark.parametrize("layout", ["nn", "nt", "tn", "tt"])
 def test_strides_and_alignment(layout, pad, offset):
@@ -205,7 +238,8 @@ def quantised(x):
 
 @pytest.mark.parametrize("out", [H, B, F])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 128, 256), (4, 96, 48), (17, 130, 1000), (129, 257, 144),
-                                   (300, 300, 33), (256, 512, 1024), (40, 64, 0)])
+                                   (300, 300, 33), (256, 512, 1024), (40, 64, 0), (16, 33000, 130), (32, 50, 9100),
+                                   (2, 17, 0)])
 def test_scaled(M, N, K, out):
     for name, pad in (("none", 0), ("silu", 16), ("gelu", 5)):
         n = R.gen(M + N + K)

@@ -12,6 +12,7 @@
 
 #include "../../include/tsgemm.h"
 #include "epilogue.hpp"
+#include "few_rows.hpp"
 #include "plan.hpp"
 
 namespace ts {
@@ -71,6 +72,7 @@ struct EpiPlan {
     int special = 0;       // special form of the epilogue (EPI_SPECIAL + ...), 0: the general one
     int es;                // operand element size in bytes
     Operand a, b;
+    bool few;              // few_rows.hip runs it: none of the rest is filled
     int64_t kp;            // K as the kernel sees it, elements (a multiple of 16 bytes if an operand is kmaj)
     WorkspaceLayout sk;
     int64_t off_a, off_b, total;   // workspace offsets of the packed operands, and its size
@@ -248,6 +250,14 @@ ts_status epi_plan(const void* A, const void* B, int64_t M, int64_t N, int64_t K
     if (st != TS_OK) return st;
     e->path = e->a.kmaj ? (e->b.kmaj ? PATH_EDGE_BT : PATH_EDGE_NN) : (e->b.kmaj ? PATH_EDGE_ATBT : PATH_EDGE_AT);
 
+    // few rows and a schedule that leaves everything to the library: one pass over B
+    e->few = M > 0 && M <= kFewRows && e->a.kmaj && s.order == TS_ORDER_AUTO && s.mode == TS_MODE_AUTO &&
+             s.tile_config == TS_TILE_AUTO && s.num_programs == 0;
+    if (e->few) {
+        e->kind = 0;
+        return TS_OK;
+    }
+
     Plan& p = e->p;
     p.cfg = s.tile_config != TS_TILE_AUTO ? s.tile_config
             : cdiv64(M, 256) * cdiv64(N, 256) >= 128 ? CFG_256W8 : CFG_128;
@@ -341,7 +351,7 @@ extern "C" int64_t ts_gemm_epilogue_workspace(const void* A, const void* B, int6
     EpiPlan e;
     ts_status st = epi_plan(A, B, M, N, K, stride_am, stride_ak, stride_bk, stride_bn, ab_dtype, c_dtype, sched, &e);
     if (st != TS_OK) return st;
-    if (M == 0 || N == 0) return 0;
+    if (M == 0 || N == 0 || e.few) return 0;
     if (e.kind != EPI_STREAMK) return e.a.packed_bytes + e.b.packed_bytes;
     int dev = 0;
     DeviceInfo di;
@@ -377,6 +387,42 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
         return TS_ERR_UNSUPPORTED;
     const int ce = c_dtype == TS_F32 ? 4 : 2;
     if ((uintptr_t)A % e.es || (uintptr_t)B % e.es || (uintptr_t)C % ce) return TS_ERR_ALIGNMENT;
+
+    if (e.few) {
+        int dev;
+        DeviceInfo di;
+        st = current_device(&dev, &di);
+        if (st != TS_OK) return st;
+        FewArgs f;
+        memset(&f, 0, sizeof f);
+        f.A = A;
+        f.B = B;
+        f.C = C;
+        f.M = (int)M;
+        f.N = (int)N;
+        f.K = (int)K;
+        f.lda = e.a.ld;
+        f.ldb = e.b.ld;
+        f.ldc = stride_cm;
+        f.xcds = di.xcds;
+        if (epi) {
+            f.act = epi->activation;
+            f.grad = epi->grad;
+            f.bias = epi->bias;
+            f.bias_type = epi->bias_dtype;
+            f.aux_in = epi->grad ? epi->preact : epi->residual;
+            f.ld_in = M > 1 ? (epi->grad ? epi->stride_pm : epi->stride_rm) : N;
+            f.aux_out = epi->grad ? nullptr : epi->preact;
+            f.ld_out = M > 1 ? epi->stride_pm : N;
+            f.scale_a = epi->scale_a;
+            f.scale_b = epi->scale_b;
+        }
+        if (launch_few_rows(f, ab_dtype, c_dtype, e.b.kmaj, static_cast<hipStream_t>(stream)) != hipSuccess) {
+            (void)hipGetLastError();
+            return TS_ERR_HIP;
+        }
+        return TS_OK;
+    }
 
     auto workspace_ok = [&](int64_t need) {
         return need == 0 || (workspace && workspace_bytes >= need && (uintptr_t)workspace % 256 == 0);
