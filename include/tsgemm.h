@@ -420,6 +420,9 @@ typedef struct {
  *   bit-identical results; TS_MODE_STREAMK as in ts_gemm.  Tiles: TS_TILE_AUTO,
  *   TS_TILE_128x128x64, TS_TILE_256x256x64_W8 (others: TS_ERR_UNSUPPORTED); with
  *   8-bit operands a K step holds 128 values.
+ *   Up to 32 rows, A stored [M][K], and a schedule that leaves order, mode, tile and
+ *   programs to the library: one pass over B with K split over the waves of a workgroup
+ *   (sums in another order than the tile kernels', the same on every run), no workspace.
  *   workspace: at least ts_gemm_epilogue_workspace bytes for the same arguments,
  *   256-byte aligned, contents arbitrary (a stream-K launch clears its own flags);
  *   calls that share one must not overlap in time.  NULL where none is needed.

@@ -30,6 +30,7 @@ _i32, _i64, _p = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 # status codes, element types and schedule enums (include/tsgemm.h)
 TS_OK, TS_ERR_INVALID_ARG, TS_ERR_UNSUPPORTED, TS_ERR_ALIGNMENT, TS_ERR_HIP, TS_ERR_NO_DEVICE = 0, -1, -2, -3, -4, -5
 TS_F16, TS_BF16, TS_F32, TS_E4M3 = 1, 2, 3, 4
+FEW_ROWS = 32   # products of up to this many rows need no workspace (ts_gemm_epilogue)
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 ORDERS = {"row_major": 0, "grouped": 1, "auto": 2}
 MODES = {"tiled": 0, "persistent": 1, "crosstile": 2, "streamk": 3, "auto": 4}
@@ -337,57 +338,55 @@ def schedule_trace_host(M: int, N: int, K: int, schedule: Schedule, cu_count: in
 _DTYPE = {**_TORCH_DTYPE, torch.float8_e4m3fn: TS_E4M3}
 
 
-def _device_of(*tensors) -> torch.device:
-    """The one GPU that every given tensor (None: absent) is on."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
+# Calls of a few microseconds of GPU time are bound by what surrounds them on the host, so the
+# checks below read each attribute once, and the stream comes as its raw handle.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _device_of(first: torch.Tensor, *others) -> int:
+    """Index of the one GPU that every given tensor (None: absent) is on."""
+    index = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != index:
             raise ValueError("all tensors must be on the same GPU")
-    if dev.type != "cuda":
+    if index < 0:
         raise ValueError("tensors must be on a GPU")
-    return dev
+    return index
 
 
-class _On:
-    """Makes `device` current for the launches inside (and back), and holds its stream."""
-
-    def __init__(self, device: torch.device):
-        self.index = device.index
-        self.stream = torch.cuda.current_stream(device).cuda_stream
-
-    def __enter__(self):
-        self.back = torch.cuda.current_device()
-        if self.back != self.index:
-            torch.cuda.set_device(self.index)
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.back != self.index:
-            torch.cuda.set_device(self.back)
-        return False
+def _launch(index: int, fn, *args) -> None:
+    """fn(*args) with GPU `index` current; raises on an error status."""
+    if torch.cuda.current_device() == index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args)
+    if st != TS_OK:
+        raise TsError(st)
 
 
-def _scratch(nbytes: int, device: torch.device):
+def _scratch(nbytes: int, like: torch.Tensor):
     """A workspace of the call's own, from torch's allocator: calls on other streams, and
     graphs captured one after the other, never share one."""
     if nbytes < 0:
         raise TsError(int(nbytes))
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None
 
 
 def _rows(t: torch.Tensor, shape, what: str, dtype=None) -> int:
     """Row stride of a matrix with unit column stride, after its checks."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
-    if shape[1] > 1 and t.stride(1) != 1:
+    row, col = t.stride()
+    if col != 1 and shape[1] > 1:
         raise ValueError(f"{what} must have unit stride along its rows")
-    return t.stride(0)
+    return row
 
 
 def _vector(t: torch.Tensor, n: int, what: str, dtype=None) -> None:
-    if tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{what} must be a contiguous vector of {n}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
@@ -401,39 +400,44 @@ def _activation(name) -> int:
     return ACTIVATIONS[name]
 
 
-def _product(a, b, out, out_dtype, epi: _Epilogue, schedule, matrices, bias=None, scales=(None, None)):
+def _product(a, b, out, out_dtype, epi: _Epilogue, schedule, residual=None, preact=None, bias=None, scale_a=None,
+             scale_b=None):
     if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[0]:
         raise ValueError(f"shapes {tuple(a.shape)} @ {tuple(b.shape)} do not multiply")
     if a.dtype != b.dtype:
         raise ValueError(f"A is {a.dtype}, B is {b.dtype}")
-    dev = _device_of(a, b, out, bias, *scales, *(t for t, _, _ in matrices))
+    dev = _device_of(a, b, out, bias, residual, preact, scale_a, scale_b)
     (M, K), N = a.shape, b.shape[1]
+    shape = (M, N)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
-    elif out.shape != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
+        out = torch.empty(shape, dtype=out_dtype, device=a.device)
+    elif out.shape != shape or out.dtype != out_dtype:
         raise ValueError("out has the wrong shape or type")
-    for t, what, put in matrices:
-        if t is not None:
-            put(t.data_ptr(), _rows(t, (M, N), what, out.dtype))
+    if residual is not None:
+        epi.residual, epi.stride_rm = residual.data_ptr(), _rows(residual, shape, "residual", out_dtype)
+    if preact is not None:
+        epi.preact, epi.stride_pm = preact.data_ptr(), _rows(preact, shape, "preact", out_dtype)
     if bias is not None:
         _vector(bias, N, "bias")
         epi.bias, epi.bias_dtype = bias.data_ptr(), _TORCH_DTYPE[bias.dtype]
-    if scales[0] is not None:
-        _vector(scales[0], M, "scale_a", torch.float32)
-        epi.scale_a = scales[0].data_ptr()
-    if scales[1] is not None:
-        _vector(scales[1], N, "scale_b", torch.float32)
-        epi.scale_b = scales[1].data_ptr()
+    if scale_a is not None:
+        _vector(scale_a, M, "scale_a", torch.float32)
+        epi.scale_a = scale_a.data_ptr()
+    if scale_b is not None:
+        _vector(scale_b, N, "scale_b", torch.float32)
+        epi.scale_b = scale_b.data_ptr()
     s = ctypes.byref(schedule._c()) if schedule is not None else None
-    ab_t, c_t = _DTYPE.get(a.dtype, 0), _DTYPE.get(out.dtype, 0)
+    ab_t, c_t = _DTYPE.get(a.dtype, 0), _DTYPE.get(out_dtype, 0)
     pa, pb = a.data_ptr(), b.data_ptr()
-    sizes = (M, N, K, a.stride(0), a.stride(1), b.stride(0), b.stride(1))
-    with _On(dev) as stream:
-        need = _lib.ts_gemm_epilogue_workspace(pa, pb, *sizes, ab_t, c_t, s)
-        ws = _scratch(need, dev)
-        _check(_lib.ts_gemm_epilogue(pa, pb, out.data_ptr(), *sizes, out.stride(0), out.stride(1), ab_t, c_t,
-                                     ctypes.byref(epi), s, stream, ws.data_ptr() if ws is not None else None,
-                                     max(need, 0)))
+    sam, sak = a.stride()
+    sbk, sbn = b.stride()
+    scm, scn = out.stride()
+    ws, need = None, 0
+    if M > FEW_ROWS or s is not None or sak != 1:
+        need = _lib.ts_gemm_epilogue_workspace(pa, pb, M, N, K, sam, sak, sbk, sbn, ab_t, c_t, s)
+        ws = _scratch(need, a)
+    _launch(dev, _lib.ts_gemm_epilogue, pa, pb, out.data_ptr(), M, N, K, sam, sak, sbk, sbn, scm, scn, ab_t, c_t,
+            ctypes.byref(epi), s, _raw_stream(dev), ws.data_ptr() if need else None, need)
     return out
 
 
@@ -450,16 +454,9 @@ def gemm_epilogue(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = 
     Enqueued on the current stream of A's device.  A 2-D product: batched or 1-D operands
     are reshaped by the caller.  The gradients: ``gemm_epilogue_backward``.
     """
-    epi = _Epilogue(activation=_activation(activation))
-
-    def put_r(p, ld):
-        epi.residual, epi.stride_rm = p, ld
-
-    def put_p(p, ld):
-        epi.preact, epi.stride_pm = p, ld
-
-    return _product(a, b, out, out_dtype or (out.dtype if out is not None else a.dtype), epi, schedule,
-                    [(residual, "residual", put_r), (preact, "preact", put_p)], bias)
+    epi = _Epilogue(_activation(activation))
+    return _product(a, b, out, out_dtype or (out.dtype if out is not None else a.dtype), epi, schedule, residual, preact,
+                    bias)
 
 
 def gemm_dact(a: torch.Tensor, b: torch.Tensor, preact: torch.Tensor, activation: str,
@@ -467,12 +464,7 @@ def gemm_dact(a: torch.Tensor, b: torch.Tensor, preact: torch.Tensor, activation
     """C = (A @ B) * act'(preact): the gradient that reaches the input of an activation whose
     output feeds a product, in that product's own backward launch (A the gradient of its
     output, B its weights transposed).  C has ``preact``'s type."""
-    epi = _Epilogue(activation=_activation(activation), grad=1)
-
-    def put_p(p, ld):
-        epi.preact, epi.stride_pm = p, ld
-
-    return _product(a, b, out, preact.dtype, epi, schedule, [(preact, "preact", put_p)])
+    return _product(a, b, out, preact.dtype, _Epilogue(_activation(activation), 1), schedule, preact=preact)
 
 
 def gemm_scaled(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor | None = None,
@@ -489,16 +481,9 @@ def gemm_scaled(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor | None =
     """
     if a.dtype != torch.float8_e4m3fn:
         raise ValueError(f"A is {a.dtype}, expected torch.float8_e4m3fn")
-    epi = _Epilogue(activation=_activation(activation))
-
-    def put_r(p, ld):
-        epi.residual, epi.stride_rm = p, ld
-
-    def put_p(p, ld):
-        epi.preact, epi.stride_pm = p, ld
-
-    return _product(a, b, out, out_dtype or (out.dtype if out is not None else torch.bfloat16), epi, schedule,
-                    [(residual, "residual", put_r), (preact, "preact", put_p)], bias, (scale_a, scale_b))
+    epi = _Epilogue(_activation(activation))
+    return _product(a, b, out, out_dtype or (out.dtype if out is not None else torch.bfloat16), epi, schedule, residual,
+                    preact, bias, scale_a, scale_b)
 
 
 def act_grad(dc: torch.Tensor, preact: torch.Tensor | None = None, activation: str = "none",
@@ -515,30 +500,27 @@ def act_grad(dc: torch.Tensor, preact: torch.Tensor | None = None, activation: s
     act = _activation(activation)
     if dc.dim() != 2:
         raise ValueError("dC must be a matrix")
-    M, N = dc.shape
+    M, N = shape = dc.shape
     if act and preact is None:
         raise ValueError("preact is needed for this activation")
     if not act:
         preact = None
-    ldc = _rows(dc, (M, N), "dC")
-    ldz = _rows(preact, (M, N), "preact", dc.dtype) if preact is not None else N
-    copy = act or out is not None or out_dtype not in (None, dc.dtype)
-    if out is None and copy:
-        out = torch.empty((M, N), dtype=out_dtype or dc.dtype, device=dc.device)
+    ldc = _rows(dc, shape, "dC")
+    ldz = _rows(preact, shape, "preact", dc.dtype) if preact is not None else N
+    if out is None and (act or out_dtype not in (None, dc.dtype)):
+        out = torch.empty(shape, dtype=out_dtype or dc.dtype, device=dc.device)
     dev = _device_of(dc, preact, out)
-    ldo = _rows(out, (M, N), "out", out_dtype) if out is not None else N
-    db = torch.empty(N, dtype=dbias_dtype, device=dev) if dbias else None
+    ldo = _rows(out, shape, "out", out_dtype) if out is not None else N
+    db = torch.empty(N, dtype=dbias_dtype, device=dc.device) if dbias else None
     if out is None and db is None:
         return dc, None
-    with _On(dev) as stream:
-        need = _lib.ts_act_grad_workspace(M, N) if dbias else 0
-        ws = _scratch(need, dev)
-        _check(_lib.ts_act_grad(dc.data_ptr(), preact.data_ptr() if preact is not None else None,
-                                out.data_ptr() if out is not None else None, db.data_ptr() if dbias else None,
-                                M, N, ldc, ldz, ldo, _DTYPE.get(dc.dtype, 0),
-                                _DTYPE.get(out.dtype if out is not None else dc.dtype, 0),
-                                _DTYPE.get(dbias_dtype, 0), act, stream,
-                                ws.data_ptr() if ws is not None else None, max(need, 0)))
+    need = _lib.ts_act_grad_workspace(M, N) if dbias else 0
+    ws = _scratch(need, dc)
+    in_t = _DTYPE.get(dc.dtype, 0)
+    _launch(dev, _lib.ts_act_grad, dc.data_ptr(), preact.data_ptr() if preact is not None else None,
+            out.data_ptr() if out is not None else None, db.data_ptr() if dbias else None, M, N, ldc, ldz, ldo, in_t,
+            _DTYPE.get(out.dtype, 0) if out is not None else in_t, _DTYPE.get(dbias_dtype, 0), act, _raw_stream(dev),
+            ws.data_ptr() if need else None, need)
     return (out if out is not None else dc), db
 
 
@@ -580,30 +562,30 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch
         raise ValueError("x must be a matrix of rows")
     if h is not None and residual is None:
         raise ValueError("h is written only with a residual")
-    M, N = x.shape
-    ldx = _rows(x, (M, N), "x")
-    out_dtype = out_dtype or (out.dtype if out is not None else x.dtype)
+    M, N = shape = x.shape
+    dtype = x.dtype
+    out_dtype = out_dtype or (out.dtype if out is not None else dtype)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        out = torch.empty(shape, dtype=out_dtype, device=x.device)
+    if residual is not None and h is None:
+        h = torch.empty(shape, dtype=dtype, device=x.device)
     dev = _device_of(x, weight, residual, out, h)
-    ldy = _rows(out, (M, N), "out", out_dtype)
+    ldx = _rows(x, shape, "x")
+    ldy = _rows(out, shape, "out", out_dtype)
     ldr = ldh = N
+    pr = ph = pw = ps = scale = None
     if residual is not None:
-        ldr = _rows(residual, (M, N), "residual", x.dtype)
-        if h is None:
-            h = torch.empty((M, N), dtype=x.dtype, device=dev)
-        ldh = _rows(h, (M, N), "h", x.dtype)
+        ldr, ldh = _rows(residual, shape, "residual", dtype), _rows(h, shape, "h", dtype)
+        pr, ph = residual.data_ptr(), h.data_ptr()
+    w_t = TS_F32
     if weight is not None:
         _vector(weight, N, "weight")
-    scale = torch.empty(M, dtype=torch.float32, device=dev) if out_dtype == torch.float8_e4m3fn else None
-    with _On(dev) as stream:
-        _check(_lib.ts_rmsnorm(x.data_ptr(), residual.data_ptr() if residual is not None else None,
-                               weight.data_ptr() if weight is not None else None, out.data_ptr(),
-                               h.data_ptr() if h is not None else None,
-                               scale.data_ptr() if scale is not None else None, M, N, ldx, ldr, ldy, ldh,
-                               _TORCH_DTYPE.get(x.dtype, 0),
-                               _TORCH_DTYPE[weight.dtype] if weight is not None else TS_F32,
-                               _DTYPE.get(out_dtype, 0), float(eps), stream))
+        pw, w_t = weight.data_ptr(), _TORCH_DTYPE[weight.dtype]
+    if out_dtype == torch.float8_e4m3fn:
+        scale = torch.empty(M, dtype=torch.float32, device=x.device)
+        ps = scale.data_ptr()
+    _launch(dev, _lib.ts_rmsnorm, x.data_ptr(), pr, pw, out.data_ptr(), ph, ps, M, N, ldx, ldr, ldy, ldh,
+            _TORCH_DTYPE.get(dtype, 0), w_t, _DTYPE.get(out_dtype, 0), eps, _raw_stream(dev))
     return out, scale, (h if h is not None else x)
 
 
@@ -619,26 +601,23 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | N
     """
     if dy.dim() != 2:
         raise ValueError("dy must be a matrix of rows")
-    M, N = dy.shape
-    ldy = _rows(dy, (M, N), "dy")
-    ldh = _rows(h, (M, N), "h", dy.dtype)
-    lds = _rows(dh, (M, N), "dh", dy.dtype) if dh is not None else N
+    M, N = shape = dy.shape
+    dtype = dy.dtype
     if out is None:
-        out = torch.empty((M, N), dtype=dy.dtype, device=dy.device)
+        out = torch.empty(shape, dtype=dtype, device=dy.device)
     dev = _device_of(dy, h, weight, dh, out)
-    ldx = _rows(out, (M, N), "out", dy.dtype)
-    dw = None
+    ldy, ldh, ldx = _rows(dy, shape, "dy"), _rows(h, shape, "h", dtype), _rows(out, shape, "out", dtype)
+    lds = _rows(dh, shape, "dh", dtype) if dh is not None else N
+    dw, w_t = None, TS_F32
     if weight is not None:
         _vector(weight, N, "weight")
+        w_t = _TORCH_DTYPE[weight.dtype]
         if dweight:
-            dw = torch.empty(N, dtype=weight.dtype, device=dev)
-    with _On(dev) as stream:
-        need = _lib.ts_rmsnorm_backward_workspace(M, N) if dw is not None or N > 32768 else 0
-        ws = _scratch(need, dev)
-        _check(_lib.ts_rmsnorm_backward(dy.data_ptr(), h.data_ptr(), weight.data_ptr() if weight is not None else None,
-                                        dh.data_ptr() if dh is not None else None, out.data_ptr(),
-                                        dw.data_ptr() if dw is not None else None, M, N, ldy, ldh, lds, ldx,
-                                        _TORCH_DTYPE.get(dy.dtype, 0),
-                                        _TORCH_DTYPE[weight.dtype] if weight is not None else TS_F32, float(eps),
-                                        stream, ws.data_ptr() if ws is not None else None, max(need, 0)))
+            dw = torch.empty(N, dtype=weight.dtype, device=dy.device)
+    need = _lib.ts_rmsnorm_backward_workspace(M, N) if dw is not None or N > 32768 else 0
+    ws = _scratch(need, dy)
+    _launch(dev, _lib.ts_rmsnorm_backward, dy.data_ptr(), h.data_ptr(), weight.data_ptr() if weight is not None else None,
+            dh.data_ptr() if dh is not None else None, out.data_ptr(), dw.data_ptr() if dw is not None else None, M, N,
+            ldy, ldh, lds, ldx, _TORCH_DTYPE.get(dtype, 0), w_t, eps, _raw_stream(dev),
+            ws.data_ptr() if need else None, need)
     return out, dw
