@@ -423,6 +423,8 @@ typedef struct {
  *   Up to 32 rows, A stored [M][K], and a schedule that leaves order, mode, tile and
  *   programs to the library: one pass over B with K split over the waves of a workgroup
  *   (sums in another order than the tile kernels', the same on every run), no workspace.
+ *   With such a schedule and few tiles, K is split among programs (whole fp32 tiles of sums in
+ *   the workspace) and a second kernel adds the parts, in order, and applies the epilogue.
  *   workspace: at least ts_gemm_epilogue_workspace bytes for the same arguments,
  *   256-byte aligned, contents arbitrary (a stream-K launch clears its own flags);
  *   calls that share one must not overlap in time.  NULL where none is needed.

@@ -87,6 +87,45 @@ def test_few_rows(N, K, layout):
         R.check(got, p * s, err + R.rounded((p * s).abs() + err, out), "dact")
 
 
+@pytest.mark.parametrize("layout", ["nn", "nt", "tn", "tt"])
+@pytest.mark.parametrize("M,N,K", [(33, 64, 1024), (64, 129, 1031), (200, 7, 4100), (35, 1, 2048), (129, 260, 16384), (300, 516, 2051)])
+def test_split_k(M, N, K, layout):
+    # few tiles and a long K: the sums of parts of K joined by a second kernel; the same bits on
+    # every run, nothing outside the views written, and a schedule's whole tiles agree
+    for i, (dtype, out) in enumerate([(H, H), (B, F), (B, B)]):
+        name = R.ACTS[(i + M) % 5]
+        n = R.gen(M + N + K + i)
+        a, b, ad, bd = operands(M, N, K, dtype, layout, M * N + K, pad=3 * i, offset=i)
+        bias, res = n(N).to(dtype if i else F), n(M, N).to(out)
+        rd, _ = R.padded(res, "cuda", 3, 1)
+        pd, pbuf = R.padded(torch.zeros(M, N).to(out), "cuda", 2, 1, fill=7.0)
+        cd, cbuf = R.padded(torch.zeros(M, N).to(out), "cuda", 5, 0, fill=7.0)
+        say(M, N, K, layout, dtype, out, name)
+        z, zerr = R.product(a, b, bias)
+        want, bound = R.forward(z, zerr, name, res, out)
+        first = None
+        for sched in (None, None, ts.Schedule(order="auto", mode="crosstile")):
+            cd.zero_()
+            pd.zero_()
+            ts.gemm_epilogue(ad, bd, bias=bias.cuda(), activation=name, residual=rd, preact=pd, out=cd, schedule=sched)
+            R.check(cd, want, bound, f"C {sched}")
+            R.check(pd, z, zerr + R.rounded(z.abs() + zerr, out), f"preact {sched}")
+            first = cd.clone() if first is None else first
+            assert sched is not None or torch.equal(first, cd)
+        for buf, v in ((cbuf, cd), (pbuf, pd)):
+            v.fill_(7.0)
+            assert bool((buf == 7.0).all())
+        cd.copy_(res)   # the residual in C's own memory
+        ts.gemm_epilogue(ad, bd, bias=bias.cuda(), activation=name, residual=cd, out=cd)
+        assert torch.equal(first, cd)
+        zz = n(M, N).to(out)
+        got = ts.gemm_dact(ad, bd, zz.cuda(), "silu")
+        p, perr = R.product(a, b)
+        sl = R.slope(zz.double(), "silu")
+        err = 1.2 * perr + R.ACT_ERR * (zz.double().abs() + 1) * p.abs()
+        R.check(got, p * sl, err + R.rounded((p * sl).abs() + err, out), "dact")
+
+
 @pytest.mark.parametrize("pad,offset", [(0, 1), (1, 0), (3, 5), (8, 8), (2, 2)])
 @pytest.mark.parametrize("layout", ["nn", "nt", "tn", "tt"])
 def test_strides_and_alignment(layout, pad, offset):
@@ -239,7 +278,7 @@ def quantised(x):
 @pytest.mark.parametrize("out", [H, B, F])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 128, 256), (4, 96, 48), (17, 130, 1000), (129, 257, 144),
                                    (300, 300, 33), (256, 512, 1024), (40, 64, 0), (16, 33000, 130), (32, 50, 9100),
-                                   (2, 17, 0)])
+                                   (2, 17, 0), (33, 200, 4200), (140, 130, 9001)])
 def test_scaled(M, N, K, out):
     for name, pad in (("none", 0), ("silu", 16), ("gelu", 5)):
         n = R.gen(M + N + K)

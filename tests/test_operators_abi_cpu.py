@@ -68,6 +68,12 @@ def test_workspace_sizes():
     assert need(100, 64, 100, (100, 1, 1, 100), ab=ts.TS_E4M3) == up(100 * 112) + up(64 * 112)
     assert need(0, 64, 65, (65, 1, 64, 1)) == 0
     assert need(100, 64, 64, (32, 1, 64, 1)) == INV
+    # K split among programs: fp32 sums of whole tiles in front of packed operands
+    assert need(100, 64, 1024, (1024, 1, 64, 1)) == 2 * 128 * 128 * 4
+    assert need(100, 64, 1024, (1025, 1, 64, 1)) == 2 * 128 * 128 * 4 + up(100 * 2048)
+    assert need(130, 300, 16384, (16384, 1, 300, 1)) == 32 * 6 * 128 * 128 * 4
+    assert need(32, 300, 16384, (16384, 1, 300, 1)) == 0                  # few rows
+    assert need(100, 64, 1024, (1024, 1, 64, 1), sched=ts.Schedule(tile="128x128x64")) == 0
     sk = ts.Schedule(mode="streamk", num_programs=7, tile="128x128x64")
     assert need(512, 512, 512, (512, 1, 512, 1), sched=sk) == 256 + 7 * 128 * 128 * 4
 

@@ -9,6 +9,8 @@
 // Every term is formed in fp32; preact and C are each rounded once, to C's type.
 #pragma once
 
+#include <limits.h>
+
 #include "gemm_kernel.hpp"
 
 namespace ts {
@@ -418,6 +420,25 @@ struct FusedStore {
         }
     }
 
+    // The sums themselves, fp32, to a matrix of whole tiles.
+    template <class E>
+    static __device__ __forceinline__ void store_sums(E& e, const EpiArgs& g, int m0, int n0, float* base, long long ld) {
+        Tile t = tile_of(e, g, m0, n0);
+        t.M = INT_MAX;
+        t.whole = true;
+#pragma unroll
+        for (int i = 0; i < E::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < E::FN; ++j) {
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    const float v[4] = {e.acc[i][j][4 * q], e.acc[i][j][4 * q + 1], e.acc[i][j][4 * q + 2], e.acc[i][j][4 * q + 3]};
+                    Out<OutF32>::store4(reinterpret_cast<float*>(quad_lds(t, 16 * t.hk + 32 * q)), v, 4, true);
+                }
+                flush<OutF32>(t, base, ld, t.m + 32 * i, t.n + 32 * j);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    }
     template <bool PARTS, class E>
     static __device__ __forceinline__ void store(E& e, const EpiArgs&, int m0, int n0, const typename E::Parts& pt) {
         const EpiArgs& g = fresh_args();
@@ -493,6 +514,35 @@ struct FusedStore {
         }
     }
 };
+
+// K of a product with few tiles, split: program (split, tile) sums the K steps
+// [ks split / splits, ks (split + 1) / splits) of one tile and stores the fp32 sums, in whole
+// tiles, to a matrix of its split's own; split_finish_kernel (split_finish.hip) adds them in
+// order of the splits and applies the epilogue.  Programs that share a column panel of B (the
+// tiles of one tile column, one split) are neighbours on one XCD.
+struct SplitArgs : EpiArgs {
+    float* sums;              // [splits][rows of whole tiles][ld_sums]
+    long long ld_sums, split_stride;   // fp32 elements
+    int splits;
+};
+template <class Cfg, class TI, class TO, int PATH>
+__global__ void __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(2)))
+gemm_split_kernel(SplitArgs g) {
+    __shared__ __attribute__((aligned(16))) char lds_a0[Cfg::A_SLOT], lds_a1[Cfg::A_SLOT];
+    __shared__ __attribute__((aligned(16))) char lds_b0[Cfg::B_SLOT], lds_b1[Cfg::B_SLOT];
+    __shared__ __attribute__((aligned(16))) char lds_c[Cfg::C_BYTES > 0 ? Cfg::C_BYTES : 16];
+    typedef Engine<Cfg, TI, TO, PATH> E;
+    E e(g, lds_a0, lds_a1, lds_b0, lds_b1, lds_c);
+    const int p = xcd_remap(blockIdx.x, gridDim.x, g.s.xcds);
+    const int col = p / g.s.nm, tm = p - col * g.s.nm;
+    const int split = col / g.s.nn, tn = col - split * g.s.nn;
+    const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
+    const int k0 = (int)((long long)g.s.ks * split / g.splits), k1 = (int)((long long)g.s.ks * (split + 1) / g.splits);
+    e.zero_acc();
+    e.template tile_mainloop<true>(m0, n0, k0, k1);
+    FusedStore::store_sums(e, g, m0, n0, g.sums + split * g.split_stride, g.ld_sums);
+    e.drain();
+}
 
 // The same for one activation family and one use of aux_in, for the 256 tile: a tile inside
 // M x N runs as one straight piece of code in which every accumulator, wait and store is fixed
@@ -627,9 +677,10 @@ struct SpecialStore {
 
 // Kernel instances with the fused epilogue.  The edge paths only (they differ from the
 // whole-tile paths by a compare and a select per load), and two loops: stream-K, and the
-// nested cross-tile loop for every other mode (a program of one tile is its tiled form).
+// nested cross-tile loop for every other mode (a program of one tile is its tiled form); and
+// the 128 tile with K split.
 // The special forms of the epilogue are kinds of the second.
-enum : int { EPI_STREAMK = 1, EPI_XTILE = 2, EPI_SPECIAL = 8 };   // EPI_SPECIAL + 4 * AUX_* + FAM_*
+enum : int { EPI_STREAMK = 1, EPI_XTILE = 2, EPI_SPLIT = 3, EPI_SPECIAL = 8 };   // EPI_SPECIAL + 4 * AUX_* + FAM_*
 
 template <class Cfg, class TI, class TO, int PATH, int FAM, int AUX>
 const void* epi_special() {
@@ -662,6 +713,11 @@ template <class Cfg, class TI, class TO, int PATH>
 const void* epi_kernel_by_kind(int kind) {
     if (kind == EPI_STREAMK)
         return reinterpret_cast<const void*>(&gemm_tiles_kernel<Cfg, TI, TO, PATH, MODE_STREAMK, FusedStore>);
+    if constexpr (Cfg::BM == 128) {
+        // the sums are fp32 whatever C's type, which for 8-bit operands still chooses the products
+        typedef typename std::conditional<std::is_same<TI, InE4M3>::value && !std::is_same<TO, OutF32>::value, OutBF16, OutF32>::type TS;
+        if (kind == EPI_SPLIT) return reinterpret_cast<const void*>(&gemm_split_kernel<Cfg, TI, TS, PATH>);
+    }
     return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg, TI, TO, PATH, false, FusedStore>);
 }
 

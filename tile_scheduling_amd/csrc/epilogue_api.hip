@@ -13,6 +13,7 @@
 #include "../../include/tsgemm.h"
 #include "epilogue.hpp"
 #include "few_rows.hpp"
+#include "split.hpp"
 #include "plan.hpp"
 
 namespace ts {
@@ -52,6 +53,7 @@ namespace {
 constexpr int64_t kOffsetLimit = 1LL << 30;   // in-tile byte offsets of the direct-to-LDS loads
 constexpr int64_t kMaxExtent = INT_MAX - 1024;    // rows and columns of the last tile stay ints
 constexpr int64_t kMaxStride = (1LL << 26) - 1;   // 32-bit lane offsets of the epilogue (16 rows of 4 bytes)
+constexpr int64_t kSplitPrograms = 256, kSplitSteps = 8;   // K split (splits_of): programs at most, K steps each at least
 constexpr int kSpin = 1 << 24;                // sleeps before a stream-K wait gives up (about a second)
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
@@ -75,6 +77,8 @@ struct EpiPlan {
     bool few;              // few_rows.hip runs it: none of the rest is filled
     int64_t kp;            // K as the kernel sees it, elements (a multiple of 16 bytes if an operand is kmaj)
     WorkspaceLayout sk;
+    int splits;            // EPI_SPLIT: programs that share a tile's K
+    int64_t sums_bytes;    // and their fp32 sums, at the workspace's start
     int64_t off_a, off_b, total;   // workspace offsets of the packed operands, and its size
 };
 
@@ -220,6 +224,20 @@ ts_status resolve(Plan* p, int cu_count, int ppc, int xcds) {
     return resolve_grid(p, cu_count, ppc, xcds);
 }
 
+// Programs that share the K of each of `tiles` 128 tiles of `ks` K steps; 1: none does.  A tile
+// alone waits for memory in every step (0.6 us), so K is split until a program is on each of 256
+// CUs, in parts of 8 steps at least, if the steps saved outweigh the second launch and the sums'
+// way through memory (6 steps and one for 16 programs).  Measured, whole / split, bf16: 64 x 4096 x 4096
+// 41.4 / 17.8 us, 256 x 4096 x 4096 41.2 / 22.7, 512 x 4096 x 4096 42.0 / 32.2, 1000 x 512 x 2048 23.4 / 16.1,
+// 200 x 512 x 16384 144 / 20.7; e4m3 128 x 8192 x 8192 60.0 / 27.9.  With parts of 4 steps 1000 x 512
+// x 2048 took 19.4 and 256 x 256 x 16384 24.9 against 18.7; with 512 programs 256 x 4096 x 4096 23.6, 64 x
+// 16384 x 4096 36.6 against 45.2 but [K][N] 41.4 against 39.4.  Not worth it: 1024 x 1024 x 1024 15.2 /
+// 15.9, 512 x 2048 x 1000 14.8 / 16.1.
+int splits_of(int64_t tiles, int64_t ks) {
+    const int64_t s = std::min<int64_t>(kSplitPrograms / std::max<int64_t>(tiles, 1), ks / kSplitSteps);
+    return s > 1 && ks - cdiv64(ks, s) > 6 + tiles * s / 16 ? (int)s : 1;
+}
+
 // Everything but the device: types, layouts, tile, schedule, packing.
 ts_status epi_plan(const void* A, const void* B, int64_t M, int64_t N, int64_t K, int64_t sam, int64_t sak,
                    int64_t sbk, int64_t sbn, int32_t ab, int32_t c, const ts_schedule* sp, EpiPlan* e) {
@@ -251,8 +269,10 @@ ts_status epi_plan(const void* A, const void* B, int64_t M, int64_t N, int64_t K
     e->path = e->a.kmaj ? (e->b.kmaj ? PATH_EDGE_BT : PATH_EDGE_NN) : (e->b.kmaj ? PATH_EDGE_ATBT : PATH_EDGE_AT);
 
     // few rows and a schedule that leaves everything to the library: one pass over B
-    e->few = M > 0 && M <= kFewRows && e->a.kmaj && s.order == TS_ORDER_AUTO && s.mode == TS_MODE_AUTO &&
-             s.tile_config == TS_TILE_AUTO && s.num_programs == 0;
+    const bool open = s.order == TS_ORDER_AUTO && s.mode == TS_MODE_AUTO && s.tile_config == TS_TILE_AUTO && s.num_programs == 0;
+    e->few = open && M > 0 && M <= kFewRows && e->a.kmaj;
+    e->splits = 1;
+    e->sums_bytes = 0;
     if (e->few) {
         e->kind = 0;
         return TS_OK;
@@ -292,12 +312,28 @@ ts_status epi_plan(const void* A, const void* B, int64_t M, int64_t N, int64_t K
     p.s.fastdiv = s.index_math == TS_INDEX_MULSHIFT;
     p.max_items = 0;
     e->kind = p.mode == TS_MODE_STREAMK ? EPI_STREAMK : EPI_XTILE;
+    if (open && p.cfg == CFG_128) {
+        e->splits = splits_of(nm * nn, ks);
+        if (e->splits > 1) {
+            e->kind = EPI_SPLIT;
+            e->sums_bytes = e->splits * nm * nn * (int64_t)p.bm * p.bn * 4;
+        }
+    }
     return TS_OK;
 }
 
 // The grid and the workspace; needs the device where the grid does.
 ts_status epi_resolve(EpiPlan* e, int32_t ab, int dev, const DeviceInfo* di) {
     Plan& p = e->p;
+    if (e->kind == EPI_SPLIT) {
+        p.s.grid = p.s.num_tiles * e->splits;
+        p.s.xcds = di ? di->xcds : 8;
+        e->sk = WorkspaceLayout{0, 0, 0};
+        e->off_a = e->sums_bytes;
+        e->off_b = e->off_a + e->a.packed_bytes;
+        e->total = e->off_b + e->b.packed_bytes;
+        return TS_OK;
+    }
     int ppc = 0;
     if (di) ppc = occupancy_of(dev, epi_kernel_of(*e, ab), p.cfg == CFG_128 ? Cfg128::NT : Cfg256w8::NT);
     ts_status st = di ? resolve(&p, di->cu_count, ppc, di->xcds) : resolve_grid(&p, 0, 0, 8);
@@ -352,7 +388,7 @@ extern "C" int64_t ts_gemm_epilogue_workspace(const void* A, const void* B, int6
     ts_status st = epi_plan(A, B, M, N, K, stride_am, stride_ak, stride_bk, stride_bn, ab_dtype, c_dtype, sched, &e);
     if (st != TS_OK) return st;
     if (M == 0 || N == 0 || e.few) return 0;
-    if (e.kind != EPI_STREAMK) return e.a.packed_bytes + e.b.packed_bytes;
+    if (e.kind != EPI_STREAMK) return e.sums_bytes + e.a.packed_bytes + e.b.packed_bytes;
     int dev = 0;
     DeviceInfo di;
     const bool need = grid_needs_device(e);
@@ -427,7 +463,8 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
     auto workspace_ok = [&](int64_t need) {
         return need == 0 || (workspace && workspace_bytes >= need && (uintptr_t)workspace % 256 == 0);
     };
-    if (e.kind != EPI_STREAMK && !workspace_ok(e.a.packed_bytes + e.b.packed_bytes)) return TS_ERR_INVALID_ARG;
+    if (e.kind != EPI_STREAMK && !workspace_ok(e.sums_bytes + e.a.packed_bytes + e.b.packed_bytes))
+        return TS_ERR_INVALID_ARG;
     if (e.kind == EPI_STREAMK && !grid_needs_device(e)) {
         EpiPlan q = e;
         st = epi_resolve(&q, ab_dtype, 0, nullptr);
@@ -456,7 +493,7 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
     // Sizes along K count 16-bit units (pairs of 8-bit elements).
     const int unit = 2 / e.es;
     const int64_t kk = e.kp / unit;
-    EpiArgs g;
+    SplitArgs g;
     memset(&g, 0, sizeof g);
     auto pitch = [&](const Operand& o) {
         return (o.pack ? round_up(o.cols * e.es, 16) / e.es : o.ld) / unit;
@@ -502,7 +539,14 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
     g.stagger = stagger_sleeps(e, g.aux_in != nullptr);
     const int threads = e.p.cfg == CFG_128 ? Cfg128::NT : Cfg256w8::NT;
     void* args[] = {&g};
-    if (hipLaunchKernel(epi_kernel_of(e, ab_dtype), dim3(e.p.s.grid), dim3(threads), args, 0, hs) != hipSuccess) {
+    if (e.kind == EPI_SPLIT) {
+        g.sums = reinterpret_cast<float*>(ws);
+        g.ld_sums = (int64_t)e.p.s.nn * e.p.bn;
+        g.split_stride = (int64_t)e.p.s.nm * e.p.bm * g.ld_sums;
+        g.splits = e.splits;
+    }
+    if (hipLaunchKernel(epi_kernel_of(e, ab_dtype), dim3(e.p.s.grid), dim3(threads), args, 0, hs) != hipSuccess ||
+        (e.kind == EPI_SPLIT && launch_split_finish(g, c_dtype, hs) != hipSuccess)) {
         (void)hipGetLastError();
         return TS_ERR_HIP;
     }
