@@ -552,7 +552,11 @@ gemm_split_kernel(SplitArgs g) {
 // take FusedStore.  Against it, 4096 x 16384, bf16 C: K = 1024 none 124 / 133 us, gelu 156 / 169,
 // residual 143 / 165, gelu with preact 163 / 187; K = 4096 3 to 7 us in 420 to 470 less; fp32 C
 // level without aux_in, 12 % (1024) and 2 % (4096) less with.
-enum : int { AUX_NONE = 0, AUX_RESIDUAL = 1, AUX_GRAD = 2, AUX_PREACT = 3 };
+// AUX_LINES: preact and C in 16 bits, rows of whole 128-byte lines: stored past the caches, so that
+// the two streams do not push the operands out of them (4096 x 16384 x 4096 gelu 464 -> 440 us, 16384 x
+// 8192 x 2048 530 -> 503; with rows that share lines such stores cost 170 -> 211 us, 5000 x 12290 x 1000,
+// and without preact they gain nothing).
+enum : int { AUX_NONE = 0, AUX_RESIDUAL = 1, AUX_GRAD = 2, AUX_PREACT = 3, AUX_LINES = 4 };
 template <int FAM, int AUX>
 struct SpecialStore {
     typedef EpiArgs Args;
@@ -562,6 +566,7 @@ struct SpecialStore {
     static __device__ __forceinline__ void start(const EpiArgs& g) { G::start(g); }
     static constexpr int NQ = G::NQ, NU = G::NU;
     static constexpr bool IN = AUX == AUX_RESIDUAL || AUX == AUX_GRAD;   // aux_in is read
+    static constexpr bool PRE = AUX == AUX_PREACT || AUX == AUX_LINES;   // preact is written
 
     // A walk over the staged parts of a matrix of C's type: the address of the part's first
     // row is scalar and moves on from part to part (opaque, or the addresses of all parts are
@@ -593,6 +598,16 @@ struct SpecialStore {
 #pragma unroll
             for (int u = 0; u < NU; ++u) rows[u] = *unit(u);
         }
+        __device__ __forceinline__ void store(const G::Tile& t) const {
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                const typename Elt<TO>::V v = *reinterpret_cast<const u32x4*>(G::unit_lds(t, u));
+                if constexpr (AUX == AUX_LINES)
+                    __builtin_nontemporal_store(v, unit(u));
+                else
+                    *unit(u) = v;
+            }
+        }
     };
     // z of quad q of block (i, j).
     template <class E>
@@ -600,6 +615,80 @@ struct SpecialStore {
         static_assert(!E::PAIRS, "16-bit operands (the scales of 8-bit ones cost the registers this form needs)");
 #pragma unroll
         for (int c = 0; c < 4; ++c) v[c] = e.acc[i][j][4 * q + c] + bias[j * NQ + q][c];
+    }
+    // fp32 C beside a matrix that is read: parts of 16 rows of the wave's 64 columns, 256 bytes a
+    // row.  Lanes of the other 16 rows of a block skip the write of a part, and aux_in is joined
+    // on the way out, where a lane holds the same 16 bytes of it, so it needs no way through LDS;
+    // its rows are fetched one part ahead, past the caches (they are read once).  Where C's rows
+    // are not whole lines, a line that two segments share leaves the L2 in one piece only if both come
+    // soon after another: with segments of 128 bytes, a block's time between neighbours, and the
+    // residual passing through the L2 besides, 5000 x 12290 x 1000 took 250 us, now 215 (B [N][K] 253,
+    // 208); 4096 x 16384 x 256 125, now 102.  Without aux_in the two forms are level.
+    template <class E>
+    struct WideWalk {
+        char* p;
+        long long row4;
+        uint32_t lane;
+        __device__ __forceinline__ WideWalk(const G::Tile& t, const void* base, long long ld)
+            : p(static_cast<char*>(const_cast<void*>(base)) + (t.m * ld + t.n) * 4), row4(16 * ld),
+              lane((uint32_t)(t.ln >> 4) * (uint32_t)ld * 4u + (uint32_t)(t.ln & 15) * 16u) {}
+        __device__ __forceinline__ u32x4_a4* unit(int u) const { return reinterpret_cast<u32x4_a4*>(p + u * row4 + lane); }
+        __device__ __forceinline__ void next() {
+            p += 4 * row4;
+            asm volatile("" : "+s"(p));
+        }
+        __device__ __forceinline__ void fetch(u32x4* rows) {
+#pragma unroll
+            for (int u = 0; u < NU; ++u) rows[u] = __builtin_nontemporal_load(unit(u));
+            next();
+        }
+    };
+    template <class E>
+    static __device__ __forceinline__ void store_wide(E& e, const EpiArgs& g, const G::Tile& t) {
+        static_assert(E::FN == 2, "64 columns of a wave");
+        constexpr int NP = 2 * E::FM;
+        WideWalk<E> in(t, g.aux_in, g.ld_in), w(t, g.C, g.ldc);
+        u32x4 rows[2][NU];
+        in.fetch(rows[0]);
+        float bias[E::FN * NQ][4], one[NQ][4];
+        if constexpr (AUX == AUX_RESIDUAL) {
+#pragma unroll
+            for (int j = 0; j < E::FN; ++j) G::template columns<E>(g, t, j, one, bias + j * NQ);
+        }
+        const Sigmoid coeff = sigmoid_of(g.act);
+        const int r16 = t.r32 & 15;
+        char* wr = t.st + r16 * 256;
+        const char* rd = t.st + (t.ln >> 4) * 256;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int i = p / 2;
+            float v[E::FN * NQ][4];
+#pragma unroll
+            for (int x = 0; x < E::FN * NQ; ++x)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float a = e.acc[i][x / NQ][4 * (x % NQ) + c];
+                    if (p % 2 == 0 && AUX == AUX_RESIDUAL) a = fam_value<FAM>(a + bias[x][c], coeff);
+                    e.acc[i][x / NQ][4 * (x % NQ) + c] = a;
+                    v[x][c] = a;
+                }
+            if ((t.r32 >> 4) == p % 2) {
+#pragma unroll
+                for (int x = 0; x < E::FN * NQ; ++x)
+                    Out<OutF32>::store4(reinterpret_cast<float*>(wr + (((2 * x + t.hk) ^ r16) << 4)), v[x], 4, true);
+            }
+            if (p + 1 < NP) in.fetch(rows[(p + 1) % 2]);
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                f32x4 c = __builtin_bit_cast(f32x4, *reinterpret_cast<const u32x4*>(rd + u * 1024 + (((t.ln & 15) ^ (4 * u + (t.ln >> 4))) << 4)));
+                const f32x4 r = __builtin_bit_cast(f32x4, rows[p % 2][u]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) c[k] = AUX == AUX_GRAD ? c[k] * fam_slope<FAM>(r[k], coeff) : c[k] + r[k];
+                *w.unit(u) = __builtin_bit_cast(u32x4, c);
+            }
+            w.next();
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
     template <bool PARTS, class E>
     static __device__ __forceinline__ void store(E& e, const EpiArgs&, int m0, int n0, const typename E::Parts& pt) {
@@ -612,6 +701,10 @@ struct SpecialStore {
             return;
         }
         const G::Tile t = G::tile_of(e, g, m0, n0);
+        if constexpr (K::OSZ == 4 && IN) {
+            store_wide(e, g, t);
+            return;
+        }
         K in(t, g.aux_in, g.ld_in), pre(t, g.aux_out, g.ld_out), w(t, g.C, g.ldc);
         u32x4 rows[NU];
         if constexpr (IN) {
@@ -633,15 +726,14 @@ struct SpecialStore {
                     in.next(p + 1);
                 }
             }
-            if constexpr (AUX == AUX_PREACT) {
+            if constexpr (PRE) {
 #pragma unroll
                 for (int x = 0; x < K::JB * NQ; ++x) {
                     float v[4];
                     z_of(e, i, j0 + x / NQ, x % NQ, bias, v);
                     Out<TO>::store4(reinterpret_cast<T*>(G::quad_lds(t, (4 * t.hk + 32 * (x / NQ) + 8 * (x % NQ)) * K::OSZ)), v, 4, true);
                 }
-#pragma unroll
-                for (int u = 0; u < NU; ++u) *pre.unit(u) = *reinterpret_cast<const u32x4*>(G::unit_lds(t, u));
+                pre.store(t);
                 pre.next(p);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -667,8 +759,7 @@ struct SpecialStore {
                 }
                 Out<TO>::store4(reinterpret_cast<T*>(at), v, 4, true);
             }
-#pragma unroll
-            for (int u = 0; u < NU; ++u) *w.unit(u) = *reinterpret_cast<const u32x4*>(G::unit_lds(t, u));
+            w.store(t);
             w.next(p);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -686,6 +777,11 @@ template <class Cfg, class TI, class TO, int PATH, int FAM, int AUX>
 const void* epi_special() {
     return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg, TI, TO, PATH, false, SpecialStore<FAM, AUX>>);
 }
+template <class Cfg, class TI, class TO, int PATH, int FAM>
+const void* epi_special_lines() {
+    if constexpr (std::is_same<TO, OutF32>::value) return nullptr;
+    else return epi_special<Cfg, TI, TO, PATH, FAM, AUX_LINES>();
+}
 // The special instances of one type and layout (null: none for this kind).
 template <class Cfg, class TI, class TO, int PATH>
 const void* epi_special_by_kind(int kind) {
@@ -698,6 +794,8 @@ const void* epi_special_by_kind(int kind) {
         case EPI_SPECIAL + 4 * AUX_RESIDUAL + FAM_SIGMOID: return epi_special<Cfg, TI, TO, PATH, FAM_SIGMOID, AUX_RESIDUAL>();
         case EPI_SPECIAL + 4 * AUX_PREACT + FAM_ERF: return epi_special<Cfg, TI, TO, PATH, FAM_ERF, AUX_PREACT>();
         case EPI_SPECIAL + 4 * AUX_PREACT + FAM_SIGMOID: return epi_special<Cfg, TI, TO, PATH, FAM_SIGMOID, AUX_PREACT>();
+        case EPI_SPECIAL + 4 * AUX_LINES + FAM_ERF: return epi_special_lines<Cfg, TI, TO, PATH, FAM_ERF>();
+        case EPI_SPECIAL + 4 * AUX_LINES + FAM_SIGMOID: return epi_special_lines<Cfg, TI, TO, PATH, FAM_SIGMOID>();
         case EPI_SPECIAL + 4 * AUX_GRAD + FAM_ERF: return epi_special<Cfg, TI, TO, PATH, FAM_ERF, AUX_GRAD>();
         case EPI_SPECIAL + 4 * AUX_GRAD + FAM_SIGMOID: return epi_special<Cfg, TI, TO, PATH, FAM_SIGMOID, AUX_GRAD>();
         default: return nullptr;

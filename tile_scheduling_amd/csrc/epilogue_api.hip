@@ -137,11 +137,14 @@ int stagger_sleeps(const EpiPlan& e, bool reads) {
 
 // The special form of an epilogue, 0 if it has none.  They exist where the 256 tile runs (see
 // SpecialStore): one use of aux_in or aux_out at most, 16-bit operands, A stored [M][K].
-int special_kind(const ts_epilogue& x) {
+int special_kind(const ts_epilogue& x, const void* C, int64_t stride_cm, int32_t c) {
     const int fam = x.activation == TS_ACT_NONE ? FAM_NONE : x.activation == TS_ACT_RELU ? FAM_RELU
                     : x.activation == TS_ACT_GELU ? FAM_ERF : FAM_SIGMOID;
     if (!x.grad && x.residual && x.preact) return 0;
-    const int aux = x.grad ? AUX_GRAD : x.residual ? AUX_RESIDUAL : x.preact ? AUX_PREACT : AUX_NONE;
+    int aux = x.grad ? AUX_GRAD : x.residual ? AUX_RESIDUAL : x.preact ? AUX_PREACT : AUX_NONE;
+    if (aux == AUX_PREACT && c != TS_F32 && (fam == FAM_ERF || fam == FAM_SIGMOID) && (uintptr_t)C % 128 == 0 &&
+        (uintptr_t)x.preact % 128 == 0 && stride_cm * 2 % 128 == 0 && x.stride_pm * 2 % 128 == 0)
+        aux = AUX_LINES;
     return EPI_SPECIAL + 4 * aux + fam;
 }
 
@@ -410,8 +413,6 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
     if (st != TS_OK) return st;
     st = check_epilogue(epi, M, N, ab_dtype, c_dtype);
     if (st != TS_OK) return st;
-    const ts_epilogue plain = {};
-    e.special = special_kind(epi ? *epi : plain);
     if (workspace_bytes < 0) return TS_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return TS_OK;
     if (!C || (K > 0 && (!A || !B))) return TS_ERR_INVALID_ARG;
@@ -423,6 +424,9 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
         return TS_ERR_UNSUPPORTED;
     const int ce = c_dtype == TS_F32 ? 4 : 2;
     if ((uintptr_t)A % e.es || (uintptr_t)B % e.es || (uintptr_t)C % ce) return TS_ERR_ALIGNMENT;
+
+    const ts_epilogue plain = {};
+    e.special = special_kind(epi ? *epi : plain, C, stride_cm, c_dtype);
 
     if (e.few) {
         int dev;
