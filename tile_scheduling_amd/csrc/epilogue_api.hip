@@ -18,30 +18,72 @@
 
 namespace ts {
 
-// Copies rows of row_bytes bytes (any alignment, `pitch` apart) to rows of dst_pitch bytes
-// (a multiple of 16), zero behind the data: 16 bytes of the destination per thread.  Runs
-// in front of a product whose operand the direct-to-LDS loads cannot take as it is (its
-// rows not 16-byte aligned, or K not a multiple of 16 bytes, so that a 16-byte chunk would
-// mix the end of a row with the next one).
+// Copies rows of row_bytes bytes (any alignment, `pitch` apart) to rows of `chunks` 16-byte
+// chunks, zero behind the data.  Runs in front of a product whose operand the direct-to-LDS
+// loads cannot take as it is (its rows not 16-byte aligned, or K not a multiple of 16 bytes,
+// so that a 16-byte chunk would mix the end of a row with the next one); both operands of a
+// product in one launch.  A workgroup takes 1024 consecutive chunks, four a thread in flight.
+struct PackArgs {
+    struct Matrix {
+        const uint8_t* src;
+        uint8_t* dst;
+        long long pitch, row_bytes, chunks, blocks;   // blocks: workgroups, 0 = nothing to do
+        long long rows;
+    } m[2];
+};
 typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
-__global__ void __launch_bounds__(256) pack_rows_kernel(const uint8_t* src, long long pitch, uint8_t* dst,
-                                                        long long dst_pitch, int rows, long long row_bytes) {
-    const long long chunks = dst_pitch / 16;
-    const long long n = chunks * rows;
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-        const long long r = i / chunks, b = (i - r * chunks) * 16;
-        const uint8_t* s = src + r * pitch + b;
-        const long long left = row_bytes - b;
-        u32x4 v = {0, 0, 0, 0};
-        if (left >= 16) {
-            v = *reinterpret_cast<const u32x4_a1*>(s);
-        } else {
+constexpr int kPackChunks = 1024;
+__global__ void __launch_bounds__(256) pack_rows_kernel(PackArgs g) {
+    const bool second = blockIdx.x >= g.m[0].blocks;
+    const PackArgs::Matrix& p = g.m[second];
+    const long long first = (long long)(blockIdx.x - (second ? g.m[0].blocks : 0)) * kPackChunks;
+    const long long r0 = first / p.chunks, left = p.chunks * p.rows - first;
+    const uint32_t c0 = (uint32_t)(first - r0 * p.chunks), chunks = (uint32_t)p.chunks;
+    u32x4 v[4];
+    if (p.row_bytes >= 16) {
+        // the last chunk of a row is the row's last 16 bytes, shifted: no loads behind a branch
+        uint32_t cut[4];   // bytes that the load begins before the chunk
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (e < left) v[e >> 2] |= (uint32_t)s[e] << (8 * (e & 3));
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = threadIdx.x + 256 * i < left ? threadIdx.x + 256 * i : 0;
+            const uint32_t r = (c0 + c) / chunks;
+            const long long b = (long long)(c0 + c - r * chunks) * 16, last = p.row_bytes - 16;
+            cut[i] = b > last ? (uint32_t)(b - last) : 0;
+            v[i] = *reinterpret_cast<const u32x4_a1*>(p.src + (r0 + r) * p.pitch + (b - cut[i]));
         }
-        *reinterpret_cast<u32x4*>(dst + r * dst_pitch + b) = v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint64_t lo = v[i][0] | (uint64_t)v[i][1] << 32, hi = v[i][2] | (uint64_t)v[i][3] << 32;
+            if (cut[i] >= 8) {
+                lo = hi;
+                hi = 0;
+            }
+            const uint32_t sh = 8 * (cut[i] & 7);
+            lo = sh ? lo >> sh | hi << (64 - sh) : lo;
+            hi >>= sh;
+            v[i] = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+        }
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = threadIdx.x + 256 * i;
+            u32x4 w = {0, 0, 0, 0};
+            if (c < left) {   // one chunk a row
+                const uint8_t* s = p.src + (first + c) * p.pitch;
+#pragma unroll
+                for (int e = 0; e < 15; ++e)
+                    if (e < p.row_bytes) w[e >> 2] |= (uint32_t)s[e] << (8 * (e & 3));
+            }
+            v[0] = i == 0 ? w : v[0];
+            v[1] = i == 1 ? w : v[1];
+            v[2] = i == 2 ? w : v[2];
+            v[3] = i == 3 ? w : v[3];
+        }
     }
+    u32x4* d = reinterpret_cast<u32x4*>(p.dst) + first + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (threadIdx.x + 256 * i < left) d[256 * i] = v[i];
 }
 
 __global__ void clear_flags_kernel(int* p, int n) {
@@ -367,15 +409,11 @@ ts_status check_epilogue(const ts_epilogue* x, int64_t M, int64_t N, int32_t ab,
     return TS_OK;
 }
 
-ts_status launch_pack(const Operand& o, const void* src, int es, char* dst, hipStream_t stream) {
-    const int64_t pitch = round_up(o.cols * es, 16);
-    const int64_t chunks = pitch / 16 * o.rows;
-    const int64_t blocks = std::min<int64_t>((chunks + 255) / 256, 8192);
-    if (blocks == 0) return TS_OK;
-    hipLaunchKernelGGL(pack_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, stream,
-                       static_cast<const uint8_t*>(src), (long long)(o.ld * es), reinterpret_cast<uint8_t*>(dst),
-                       (long long)pitch, (int)o.rows, (long long)(o.cols * es));
-    return hipGetLastError() == hipSuccess ? TS_OK : TS_ERR_HIP;
+PackArgs::Matrix pack_of(const Operand& o, const void* src, int es, char* dst) {
+    const int64_t chunks = round_up(o.cols * es, 16) / 16;
+    const int64_t blocks = o.pack ? cdiv64(chunks * o.rows, kPackChunks) : 0;
+    return PackArgs::Matrix{static_cast<const uint8_t*>(src), reinterpret_cast<uint8_t*>(dst), o.ld * es, o.cols * es,
+                            std::max<int64_t>(chunks, 1), blocks, o.rows};
 }
 
 }  // namespace
@@ -491,8 +529,12 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
                            words);
         if (hipGetLastError() != hipSuccess) return TS_ERR_HIP;
     }
-    if (e.a.pack && (st = launch_pack(e.a, A, e.es, ws + e.off_a, hs)) != TS_OK) return st;
-    if (e.b.pack && (st = launch_pack(e.b, B, e.es, ws + e.off_b, hs)) != TS_OK) return st;
+    const PackArgs pk = {{pack_of(e.a, A, e.es, ws + e.off_a), pack_of(e.b, B, e.es, ws + e.off_b)}};
+    const int64_t pack_blocks = pk.m[0].blocks + pk.m[1].blocks;
+    if (pack_blocks > 0) {
+        hipLaunchKernelGGL(pack_rows_kernel, dim3((unsigned)pack_blocks), dim3(256), 0, hs, pk);
+        if (hipGetLastError() != hipSuccess) return TS_ERR_HIP;
+    }
 
     // Sizes along K count 16-bit units (pairs of 8-bit elements).
     const int unit = 2 / e.es;
