@@ -394,7 +394,8 @@ typedef struct {
     const void* residual;   /* M x N of C's type, unit column stride, or NULL; may be C   */
     int64_t stride_rm;      /* elements between its rows (ignored when M <= 1)            */
     void* preact;           /* M x N of C's type, unit column stride, or NULL: written
-                               when grad is 0, read when it is 1                          */
+                               when grad is 0 (neither C nor residual), read when it is 1
+                               (may be C)                                                 */
     int64_t stride_pm;
     const float* scale_a;   /* e4m3 operands: M fp32, one per row of A; NULL: 1           */
     const float* scale_b;   /* e4m3 operands: N fp32, one per column of B; NULL: 1        */
@@ -462,6 +463,7 @@ int64_t ts_gemm_epilogue_workspace(const void* A, const void* B,
  * dZ may be dC or preact.  M == 0: dbias is set to zero.  workspace (for dbias): at
  * least ts_act_grad_workspace(M, N) bytes, 256-byte aligned, contents arbitrary, not
  * shared by calls that overlap in time.  The current device must be the stream's.
+ * TS_ERR_UNSUPPORTED: N of 2^26 or more, M of 2^30 or more.
  */
 ts_status ts_act_grad(const void* dC, const void* preact, void* dZ, void* dbias,
                       int64_t M, int64_t N, int64_t stride_dc, int64_t stride_pm, int64_t stride_dz,
@@ -480,6 +482,7 @@ int64_t ts_act_grad_workspace(int64_t M, int64_t N);
  * residual and h come together or are both NULL.  All of it in fp32; the norm reads the
  * unrounded sum, h is its one rounding.  h may be x or residual; y of x_dtype may
  * be x or residual where h is not.  The current device must be the stream's.
+ * TS_ERR_UNSUPPORTED (here and for the gradients): N of 2^26 or more, M of 2^30 or more.
  */
 ts_status ts_rmsnorm(const void* x, const void* residual, const void* weight, void* y, void* h, float* scale,
                      int64_t M, int64_t N, int64_t stride_x, int64_t stride_r, int64_t stride_y, int64_t stride_h,

@@ -87,6 +87,20 @@ def test_few_rows(N, K, layout):
         R.check(got, p * s, err + R.rounded((p * s).abs() + err, out), "dact")
 
 
+@pytest.mark.parametrize("M", [1, 2, 7, 32, 33])
+def test_outer_product(M):
+    # K = 1: the one column of A is contiguous along M and along K
+    for N in (1, 5, 70):
+        n = R.gen(M + N)
+        for dtype in (H, B):
+            a, b = n(M, 1).to(dtype), n(1, N).to(dtype)
+            for ad in (a.cuda(), a.t().contiguous().cuda().t()):
+                for bd in (b.cuda(), b.t().contiguous().cuda().t()):
+                    z, zerr = R.product(a, b)
+                    want, bound = R.forward(z, zerr, "relu", None, F)
+                    R.check(ts.gemm_epilogue(ad, bd, activation="relu", out_dtype=F), want, bound)
+
+
 @pytest.mark.parametrize("layout", ["nn", "nt", "tn", "tt"])
 @pytest.mark.parametrize("M,N,K", [(33, 64, 1024), (64, 129, 1031), (200, 7, 4100), (35, 1, 2048), (129, 260, 16384), (300, 516, 2051)])
 def test_split_k(M, N, K, layout):

@@ -168,3 +168,17 @@ def test_norm_captured_graph():
         assert torch.equal(q.float(), eager[0].float()) and torch.equal(s, eager[1]) and torch.equal(h, eager[2])
         assert torch.equal(dx, dx0) and torch.equal(dw, dw0)
         ts.rmsnorm(x, w)
+
+
+def test_norm_of_more_rows_than_a_launch_holds():
+    # one column: y = x / sqrt(x^2 + eps) w; 2^27 + 5 rows are more threads than one launch takes
+    M = (1 << 27) + 5
+    x = torch.empty(M, 1, dtype=H, device="cuda").uniform_(-2, 2)
+    w = torch.tensor([3.0], device="cuda")
+    y, _, _ = ts.rmsnorm(x, w, eps=1.0)
+    for i in range(0, M, 1 << 25):
+        v = x[i:i + (1 << 25)].float()
+        want = 3.0 * v * torch.rsqrt(v * v + 1.0)
+        # two fp32 evaluations (each within 8 roundings of 2^-24) and half a step of fp16
+        off = (y[i:i + (1 << 25)].float() - want).abs()
+        assert bool((off <= want.abs() * (2.0 ** -11 + 16 * 2.0 ** -24) + 2.0 ** -25).all()), i

@@ -36,6 +36,8 @@ def epilogue(M=64, N=64, K=64, a=FAKE, b=FAKE, c=FAKE, strides=(64, 1, 64, 1, 64
     (dict(epi=dict(grad=1, preact=FAKE, stride_pm=64, bias=FAKE, bias_dtype=1)), INV),
     (dict(epi=dict(bias=FAKE)), INV), (dict(epi=dict(bias=FAKE, bias_dtype=ts.TS_E4M3)), INV),
     (dict(epi=dict(residual=FAKE, stride_rm=63)), INV), (dict(epi=dict(preact=FAKE, stride_pm=0)), INV),
+    (dict(c=FAKE + 256, epi=dict(preact=FAKE + 256, stride_pm=64)), INV),         # preact in C's place
+    (dict(epi=dict(preact=FAKE + 512, stride_pm=64, residual=FAKE + 512, stride_rm=64)), INV),
     (dict(epi=dict(scale_a=FAKE)), INV),                                          # scales with 16-bit operands
     (dict(epi=dict(bias=FAKE + 1, bias_dtype=1)), ALI), (dict(epi=dict(residual=FAKE + 1, stride_rm=64)), ALI),
     (dict(ab=ts.TS_E4M3, ct=ts.TS_F32, strides=(64, 1, 1, 64, 64, 1), epi=dict(scale_b=FAKE + 2)), ALI),
@@ -89,7 +91,7 @@ def test_empty_outputs_are_no_ops():
     dict(), dict(strides=(64, 1, 1, 64, 64, 1)), dict(strides=(1, 64, 64, 1, 64, 1)), dict(strides=(1, 64, 1, 64, 64, 1)),
     dict(K=0), dict(M=1, strides=(0, 1, 64, 1, 0, 1)), dict(K=1, strides=(1, 1, 64, 1, 64, 1)),
     dict(ab=ts.TS_E4M3, ct=ts.TS_BF16, strides=(64, 1, 1, 64, 64, 1), epi=dict(scale_a=FAKE, scale_b=FAKE)),
-    dict(epi=dict(activation=3, bias=FAKE, bias_dtype=3, residual=FAKE, stride_rm=64, preact=FAKE, stride_pm=64)),
+    dict(epi=dict(activation=3, bias=FAKE, bias_dtype=3, residual=FAKE, stride_rm=64, preact=FAKE + 65536, stride_pm=64)),
     dict(K=65, strides=(65, 1, 64, 1, 64, 1), ws=FAKE, wb=1 << 20),
     dict(M=512, N=512, K=512, strides=(512, 1, 512, 1, 512, 1), sched=ts.Schedule(mode="streamk", num_programs=7),
          ws=FAKE, wb=1 << 24),

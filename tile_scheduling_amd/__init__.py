@@ -433,7 +433,7 @@ def _product(a, b, out, out_dtype, epi: _Epilogue, schedule, residual=None, prea
     sbk, sbn = b.stride()
     scm, scn = out.stride()
     ws, need = None, 0
-    if M > FEW_ROWS or s is not None or sak != 1:
+    if M > FEW_ROWS or s is not None or sak != 1 or K <= 1 or N >= 1 << 26:
         need = _lib.ts_gemm_epilogue_workspace(pa, pb, M, N, K, sam, sak, sbk, sbn, ab_t, c_t, s)
         ws = _scratch(need, a)
     _launch(dev, _lib.ts_gemm_epilogue, pa, pb, out.data_ptr(), M, N, K, sam, sak, sbk, sbn, scm, scn, ab_t, c_t,

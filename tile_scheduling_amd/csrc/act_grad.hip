@@ -93,7 +93,7 @@ using namespace ts;
 
 extern "C" int64_t ts_act_grad_workspace(int64_t M, int64_t N) {
     if (M < 0 || N < 0) return TS_ERR_INVALID_ARG;
-    if (M > INT_MAX / 2 || N > INT_MAX / 2) return TS_ERR_UNSUPPORTED;
+    if (M > INT_MAX / 2 || N >= 1 << 26) return TS_ERR_UNSUPPORTED;   // N: threads of the sum over the groups
     return num_groups(M, N) * N * 4;
 }
 

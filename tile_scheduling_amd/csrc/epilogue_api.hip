@@ -315,7 +315,7 @@ ts_status epi_plan(const void* A, const void* B, int64_t M, int64_t N, int64_t K
 
     // few rows and a schedule that leaves everything to the library: one pass over B
     const bool open = s.order == TS_ORDER_AUTO && s.mode == TS_MODE_AUTO && s.tile_config == TS_TILE_AUTO && s.num_programs == 0;
-    e->few = open && M > 0 && M <= kFewRows && e->a.kmaj;
+    e->few = open && M > 0 && M <= kFewRows && N < 1 << 26 && e->a.kmaj;   // N: threads of a launch
     e->splits = 1;
     e->sums_bytes = 0;
     if (e->few) {
@@ -392,7 +392,7 @@ ts_status epi_resolve(EpiPlan* e, int32_t ab, int dev, const DeviceInfo* di) {
 
 bool grid_needs_device(const EpiPlan& e) { return e.p.mode != TS_MODE_TILED && e.p.requested_programs == 0; }
 
-ts_status check_epilogue(const ts_epilogue* x, int64_t M, int64_t N, int32_t ab, int32_t c) {
+ts_status check_epilogue(const ts_epilogue* x, const void* C, int64_t M, int64_t N, int32_t ab, int32_t c) {
     if (!x) return TS_OK;
     const int ce = c == TS_F32 ? 4 : 2;
     if (x->activation < TS_ACT_NONE || x->activation > TS_ACT_SILU || (x->grad != 0 && x->grad != 1))
@@ -400,6 +400,7 @@ ts_status check_epilogue(const ts_epilogue* x, int64_t M, int64_t N, int32_t ab,
     if (x->bias && x->bias_dtype != TS_F16 && x->bias_dtype != TS_BF16 && x->bias_dtype != TS_F32)
         return TS_ERR_INVALID_ARG;
     if (x->grad && (!x->preact || x->bias || x->residual)) return TS_ERR_INVALID_ARG;
+    if (!x->grad && x->preact && (x->preact == C || x->preact == x->residual)) return TS_ERR_INVALID_ARG;
     if ((x->scale_a || x->scale_b) && ab != TS_E4M3) return TS_ERR_INVALID_ARG;
     if (x->residual && M > 1 && x->stride_rm < N) return TS_ERR_INVALID_ARG;
     if (x->preact && M > 1 && x->stride_pm < N) return TS_ERR_INVALID_ARG;
@@ -449,7 +450,7 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
     EpiPlan e;
     ts_status st = epi_plan(A, B, M, N, K, stride_am, stride_ak, stride_bk, stride_bn, ab_dtype, c_dtype, sched, &e);
     if (st != TS_OK) return st;
-    st = check_epilogue(epi, M, N, ab_dtype, c_dtype);
+    st = check_epilogue(epi, C, M, N, ab_dtype, c_dtype);
     if (st != TS_OK) return st;
     if (workspace_bytes < 0) return TS_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return TS_OK;

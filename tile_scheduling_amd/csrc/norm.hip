@@ -25,6 +25,7 @@ struct NormArgs {
     int M, N, w_type;
     long long ldx, ldr, ldy, ldh;
     float eps;
+    long long first;   // workgroups before this launch's
 };
 
 constexpr float kE4M3Max = 448.0f;
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rmsnorm_kernel(NormArgs g) 
     typedef typename Elt<TX>::T X;
     constexpr int RPW = T < 256 ? 256 / T : 1;
     __shared__ float lds[T > 64 ? T / 64 : 1];
-    const long long m = (long long)blockIdx.x * RPW + threadIdx.x / T;
+    const long long m = (g.first + blockIdx.x) * RPW + threadIdx.x / T;
     const int t = threadIdx.x % T;
     if (m >= g.M) return;   // T <= 64 only: whole rows of lanes
     const X* x = static_cast<const X*>(g.x) + m * g.ldx;
@@ -137,7 +138,7 @@ template <class TX, bool Q>
 __global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(NormArgs g) {
     typedef typename Elt<TX>::T X;
     __shared__ float lds[kLongThreads / 64];
-    const long long m = blockIdx.x;
+    const long long m = g.first + blockIdx.x;
     const X* x = static_cast<const X*>(g.x) + m * g.ldx;
     auto load_h = [&](long long n, int valid, float* v) {
         load8<TX>(x + n, valid, v);
@@ -201,11 +202,12 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(NormArgs g) 
 struct NormGradArgs {
     const void *dy, *h, *weight, *dh;
     void* dx;
-    float* part;    // partial sums of dw, one row of N per row group, or null
+    float* part;    // partial sums of dw, one row of N per workgroup, or null
     float* stats;   // long rows: r and r^3 mean(w dy h) of every row
     int M, N, w_type;
     long long ldy, ldh, lds, ldx;
     float eps;
+    long long first;   // workgroups before this launch's (the launches of one workgroup a row)
 };
 
 // T threads a row, C groups of eight columns a thread, as above; a workgroup walks rows
@@ -267,11 +269,28 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rmsnorm_grad_kernel(NormGra
             store8<TX>(static_cast<X*>(g.dx) + m * g.ldx + n, valid, d);
         }
     }
-    if (g.part) {
+    if (!g.part) return;
+    if constexpr (RPW == 1) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int n = (c * T + t) * 8, valid = g.N - n;
             if (valid > 0) store8<OutF32>(g.part + (long long)group * g.N + n, valid, dw[c]);
+        }
+    } else {   // the workgroup's row groups first, in order
+        __shared__ float sums[256][9];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            __syncthreads();   // the last readers are done
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sums[threadIdx.x][e] = dw[c][e];
+            __syncthreads();
+            for (int k = threadIdx.x; k < 8 * T; k += 256) {
+                float s = 0.0f;
+#pragma unroll
+                for (int r = 0; r < RPW; ++r) s += sums[r * T + k / 8][k % 8];
+                const int n = c * T * 8 + k;
+                if (n < g.N) g.part[(long long)blockIdx.x * g.N + n] = s;
+            }
         }
     }
 }
@@ -282,7 +301,7 @@ template <class TX>
 __global__ void __launch_bounds__(kLongThreads) rmsnorm_grad_stats_kernel(NormGradArgs g) {
     typedef typename Elt<TX>::T X;
     __shared__ float lds1[kLongThreads / 64], lds2[kLongThreads / 64];
-    const long long m = blockIdx.x;
+    const long long m = g.first + blockIdx.x;
     float s1 = 0.0f, s2 = 0.0f;
     for (long long n = threadIdx.x * 8; n < g.N; n += kLongThreads * 8) {
         const int valid = (int)std::min<long long>(g.N - n, 8);
@@ -339,7 +358,7 @@ __global__ void __launch_bounds__(256) rmsnorm_grad_dweight_kernel(NormGradArgs 
 template <class TX>
 __global__ void __launch_bounds__(kLongThreads) rmsnorm_grad_dx_kernel(NormGradArgs g) {
     typedef typename Elt<TX>::T X;
-    const long long m = blockIdx.x;
+    const long long m = g.first + blockIdx.x;
     const float r = g.stats[2 * m], k = g.stats[2 * m + 1];
     for (long long n = threadIdx.x * 8; n < g.N; n += kLongThreads * 8) {
         const int valid = (int)std::min<long long>(g.N - n, 8);
@@ -360,22 +379,27 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_grad_dx_kernel(NormGradA
 }
 
 __global__ void __launch_bounds__(1024) reduce_columns_kernel(const float* part, int rows, int N, void* out, int type) {
-    __shared__ float sums[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const long long n = (long long)blockIdx.x * 64 + lane;
+    __shared__ float sums[16][16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15;
+    const int n = (int)blockIdx.x * 16 + c;
     float s = 0.0f;
-    if (n < N)
-        for (long long r = wave; r < rows; r += 16) s += part[r * N + n];
-    sums[wave][lane] = s;
+    if (n < N) {
+        const float* p = part + n;
+#pragma unroll 4
+        for (int r = threadIdx.x >> 4; r < rows; r += 64) s += p[(long long)r * N];
+    }
+    s += __shfl_xor(s, 16, 64);
+    s += __shfl_xor(s, 32, 64);
+    if (lane < 16) sums[wave][c] = s;
     __syncthreads();
-    if (wave == 0 && n < N) {
+    if (threadIdx.x < 16 && n < N) {
 #pragma unroll
-        for (int w = 1; w < 16; ++w) s += sums[w][lane];
+        for (int w = 1; w < 16; ++w) s += sums[w][c];
         store_any(out, type, n, s);
     }
 }
 hipError_t launch_reduce_columns(const float* part, int rows, int N, void* out, int type, hipStream_t stream) {
-    hipLaunchKernelGGL(reduce_columns_kernel, dim3((unsigned)((N + 63LL) / 64)), dim3(1024), 0, stream, part, rows, N,
+    hipLaunchKernelGGL(reduce_columns_kernel, dim3((unsigned)((N + 15LL) / 16)), dim3(1024), 0, stream, part, rows, N,
                        out, type);
     return hipGetLastError();
 }
@@ -431,7 +455,7 @@ int64_t norm_grad_groups(int64_t M, int64_t N) {
     const Shape s = norm_shape(M, N, 4);
     if (s.t == 0) return std::max<int64_t>(1, std::min<int64_t>((M + 63) / 64, 64));
     const int rpw = s.t < 256 ? 256 / s.t : 1;
-    return std::min<int64_t>((M + rpw - 1) / rpw, 1024) * rpw;
+    return std::min<int64_t>((M + rpw - 1) / rpw, 1024);
 }
 
 bool row_type(int32_t t) { return t == TS_F16 || t == TS_BF16 || t == TS_F32; }
@@ -439,7 +463,7 @@ int type_size(int32_t t) { return t == TS_F32 ? 4 : t == TS_E4M3 ? 1 : 2; }
 
 ts_status norm_sizes(int64_t M, int64_t N) {
     if (M < 0 || N < 0) return TS_ERR_INVALID_ARG;
-    if (M > INT_MAX / 2 || N > INT_MAX / 2) return TS_ERR_UNSUPPORTED;
+    if (M > INT_MAX / 2 || N >= 1 << 26) return TS_ERR_UNSUPPORTED;   // N: threads of the launches over columns
     return TS_OK;
 }
 
@@ -461,28 +485,39 @@ ts_status launch(const void* fn, int64_t gx, int64_t gy, int threads, void* args
     return TS_OK;
 }
 
+// One workgroup for every few rows: a launch holds fewer than 2^32 threads, so many rows take
+// more than one.
+template <class Args>
+ts_status launch_rows(const void* fn, int64_t blocks, int threads, Args& g, hipStream_t stream) {
+    const int64_t most = (1LL << 31) / threads;
+    for (g.first = 0; g.first < blocks; g.first += most) {
+        const ts_status st = launch(fn, std::min<int64_t>(blocks - g.first, most), 1, threads, &g, stream);
+        if (st != TS_OK) return st;
+    }
+    return TS_OK;
+}
+
 template <class TX>
 ts_status run_norm(NormArgs& g, bool q, hipStream_t stream) {
     const Shape s = norm_shape(g.M, g.N, 8);
     const void* fn = q ? norm_kernel<TX, true>(s) : norm_kernel<TX, false>(s);
-    if (s.t == 0) return launch(fn, g.M, 1, kLongThreads, &g, stream);
+    if (s.t == 0) return launch_rows(fn, g.M, kLongThreads, g, stream);
     const int rpw = s.t < 256 ? 256 / s.t : 1;
-    return launch(fn, ((int64_t)g.M + rpw - 1) / rpw, 1, std::max(s.t, 256), &g, stream);
+    return launch_rows(fn, ((int64_t)g.M + rpw - 1) / rpw, std::max(s.t, 256), g, stream);
 }
 
 template <class TX>
 ts_status run_norm_grad(NormGradArgs& g, int64_t groups, hipStream_t stream) {
     const Shape s = norm_shape(g.M, g.N, 4);
     if (s.t != 0) {
-        const int rpw = s.t < 256 ? 256 / s.t : 1;
-        return launch(norm_grad_kernel<TX>(s), groups / rpw, 1, std::max(s.t, 256), &g, stream);
+        return launch(norm_grad_kernel<TX>(s), groups, 1, std::max(s.t, 256), &g, stream);
     }
-    ts_status st = launch(reinterpret_cast<const void*>(&rmsnorm_grad_stats_kernel<TX>), g.M, 1, kLongThreads, &g, stream);
+    ts_status st = launch_rows(reinterpret_cast<const void*>(&rmsnorm_grad_stats_kernel<TX>), g.M, kLongThreads, g, stream);
     if (st == TS_OK && g.part)
         st = launch(reinterpret_cast<const void*>(&rmsnorm_grad_dweight_kernel<TX>), ((int64_t)g.N + 511) / 512, groups,
                     256, &g, stream);
     if (st == TS_OK)
-        st = launch(reinterpret_cast<const void*>(&rmsnorm_grad_dx_kernel<TX>), g.M, 1, kLongThreads, &g, stream);
+        st = launch_rows(reinterpret_cast<const void*>(&rmsnorm_grad_dx_kernel<TX>), g.M, kLongThreads, g, stream);
     return st;
 }
 
