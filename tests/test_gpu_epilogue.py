@@ -424,3 +424,42 @@ def test_streams_and_captured_graph():
             for x, y in zip(outs[2:], eager):
                 assert torch.equal(x, y), i
         assert torch.equal(ts.gemm_epilogue(ad, bd, bias=bias, activation="silu"), ref)
+
+
+def some(c, rows, cols):
+    return c[rows][:, cols].double().cpu()
+
+
+@pytest.mark.parametrize("which", ["output", "wide output", "few rows nt", "few rows nn", "scaled few rows", "operand", "split"])
+def test_beyond_32_bits(which):
+    # offsets past 2^32 bytes (and, of C, past 2^31 elements): some rows and columns, the last among them
+    M, N, K, dtype, out = {"output": (66000, 33000, 24, B, B), "wide output": (33000, 33100, 40, H, F),
+                           "few rows nt": (3, 270000, 8200, B, F), "few rows nn": (20, 270001, 8200, B, B),
+                           "scaled few rows": (2, 530000, 8200, Q, B), "operand": (300, 600000, 4096, H, H),
+                           "split": (40, 130, 17000000, B, F)}[which]
+    if which == "split":
+        K = (1 << 21) - 8   # the longest K of the direct loads' offsets
+        M = 1100            # A: 4.6 GB
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+
+    def normal(r, c):
+        t = torch.empty(r, c, dtype=dtype if dtype != Q else H, device="cuda").normal_(generator=g)
+        return t.to(Q) if dtype == Q else t
+
+    a = normal(M, K)
+    bt = which in ("few rows nt", "scaled few rows", "operand", "split")
+    b = normal(N, K).t() if bt else normal(K, N)
+    say(which, M, N, K)
+    rows = sorted({0, 1, M // 2, M - 2, M - 1} & set(range(M)))
+    cols = sorted({0, 1, N // 2, N // 2 + 1, N - 2, N - 1})
+    res = torch.empty(M, N, dtype=out, device="cuda").normal_(generator=g) if which.endswith("output") else None
+    r = some(res, rows, cols) if res is not None else None
+    if dtype == Q:
+        c = ts.gemm_scaled(a, b, out_dtype=out, activation="relu")
+    else:
+        c = ts.gemm_epilogue(a, b, out_dtype=out, activation="relu", residual=res, out=res)
+    ar, bc = a[rows].float(), b[:, cols].float()
+    z, zerr = R.product(ar, bc, eight=dtype == Q)
+    want, bound = R.forward(z, zerr, "relu", r, out)
+    R.check(some(c, rows, cols), want, bound, which)

@@ -182,3 +182,24 @@ def test_norm_of_more_rows_than_a_launch_holds():
         # two fp32 evaluations (each within 8 roundings of 2^-24) and half a step of fp16
         off = (y[i:i + (1 << 25)].float() - want).abs()
         assert bool((off <= want.abs() * (2.0 ** -11 + 16 * 2.0 ** -24) + 2.0 ** -25).all()), i
+
+
+def test_beyond_32_bits():
+    # more than 2^32 bytes, and 2^31 elements, in every matrix: the last rows
+    M, N = 300005, 8000
+    x = torch.empty(M, N, dtype=B, device="cuda").normal_()
+    w = torch.empty(N, dtype=B, device="cuda").uniform_(0.5, 1.5)
+    rows = [0, 1, M // 2, M - 2, M - 1]
+    x64, w64 = x[rows].double().cpu(), w.double().cpu()
+    y, _, _ = ts.rmsnorm(x, w)
+    want, r = norm64(x64, w64)
+    R.check(y[rows], want, y_error(want, N) + R.rounded(want.abs() * 1.01, B), "y")
+    dy = y[rows].double().cpu()
+    dx, dw = ts.rmsnorm_backward(y, x, w, dh=y, out=y)   # dy and dh are y itself
+    k = r ** 3 * (w64 * dy * x64).mean(1, keepdim=True)
+    full = r * w64 * dy - x64 * k + dy
+    # the sums of N products in r and k (N 2^-24 each, r cubed), a few products, one rounding to bf16
+    size = (r * w64 * dy).abs() + x64.abs() * r ** 3 * (w64 * dy * x64).abs().mean(1, keepdim=True) + dy.abs()
+    err = (3 * N + 32) * R.U * size
+    R.check(dx[rows], full, err + R.rounded(full.abs() + err, B), "dx")
+    assert torch.isfinite(dw.float()).all()

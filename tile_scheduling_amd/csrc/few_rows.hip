@@ -52,12 +52,26 @@ __device__ __forceinline__ f32x4 mfma_pair16(const u32x4* a, const u32x4* b, f32
     }
 }
 
-// 16 bytes at p, those at or past `left` zero.
-__device__ __forceinline__ u32x4 load16_left(const uint8_t* p, long long left) {
+// 16 bytes at p, those at or past `left` zero; `room`: bytes of the row before p.  Where the row
+// has 16 bytes, its last 16 are loaded and shifted: byte loads behind branches wait one for another.
+__device__ __forceinline__ u32x4 load16_left(const uint8_t* p, long long left, long long room) {
     u32x4 v = {0, 0, 0, 0};
-    if (left >= 16) return *reinterpret_cast<const u32x4_a1*>(p);
+    if (left <= 0) return v;
+    const int cut = left < 16 ? 16 - (int)left : 0;
+    if (room >= cut) {
+        v = *reinterpret_cast<const u32x4_a1*>(p - cut);
+        uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
+        if (cut >= 8) {
+            lo = hi;
+            hi = 0;
+        }
+        const int sh = 8 * (cut & 7);
+        lo = sh ? lo >> sh | hi << (64 - sh) : lo;
+        hi >>= sh;
+        return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+    }
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
+    for (int e = 0; e < 15; ++e)
         if (e < left) v[e >> 2] |= (uint32_t)p[e] << (8 * (e & 3));
     return v;
 }
@@ -179,9 +193,9 @@ __global__ void __launch_bounds__(kNtWaves * 64) few_nt_kernel(FewArgs g) {
         for (int h = 0; h < 2; ++h) {
             const long long left = kb - off - at - 16 * h;
 #pragma unroll
-            for (int x = 0; x < NX; ++x) fb[x][h] = load16_left(b[x] + off + 16 * h, left);
+            for (int x = 0; x < NX; ++x) fb[x][h] = load16_left(b[x] + off + 16 * h, left, kb - left);
 #pragma unroll
-            for (int y = 0; y < MT; ++y) fa[y][h] = load16_left(a[y] + off + 16 * h, left);
+            for (int y = 0; y < MT; ++y) fa[y][h] = load16_left(a[y] + off + 16 * h, left, kb - left);
         }
 #pragma unroll
         for (int x = 0; x < NX; ++x)
@@ -269,7 +283,7 @@ __global__ void __launch_bounds__(kNnWaves * 64) few_nn_kernel(FewArgs g) {
             if (j < left) row_of(b + (k + j) * g.ldb, w[j]);
         }
 #pragma unroll
-        for (int y = 0; y < MT; ++y) fa[y] = load16_left(reinterpret_cast<const uint8_t*>(a[y] + k), 2 * left);
+        for (int y = 0; y < MT; ++y) fa[y] = load16_left(reinterpret_cast<const uint8_t*>(a[y] + k), 2 * left, 2LL * (k + kg));
         multiply(w, fa);
     }
     meet_and_finish<TO, kNnWaves, V, MT, V, 1>(g, acc, red, n0);
