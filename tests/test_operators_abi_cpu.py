@@ -133,7 +133,8 @@ def test_norm_backward_refusals(kw, expect):
     (dict(dc=0), INV), (dict(z=0), INV), (dict(ws=None), INV), (dict(wb=8), INV), (dict(ld=(63, 64, 64)), INV),
     (dict(ld=(64, 64, 63)), INV), (dict(dz=FAKE + 1), ALI), (dict(db=FAKE + 2), ALI)])
 def test_act_grad_refusals(kw, expect):
-    def call(M=4, N=64, dc=FAKE, z=FAKE, dz=FAKE, db=FAKE, ld=(64, 64, 64), t=(1, 1, 3), act=2, ws=FAKE, wb=1 << 24):
+    assert ts._lib.ts_act_grad_workspace(16, 64) == 0 and ts._lib.ts_act_grad_workspace(40, 64) == 3 * 64 * 4
+    def call(M=40, N=64, dc=FAKE, z=FAKE, dz=FAKE, db=FAKE, ld=(64, 64, 64), t=(1, 1, 3), act=2, ws=FAKE, wb=1 << 24):
         return ts._lib.ts_act_grad(dc, z, dz, db, M, N, *ld, *t, act, None, ws, wb)
 
     assert call(**kw) == expect

@@ -566,9 +566,9 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch
     dtype = x.dtype
     out_dtype = out_dtype or (out.dtype if out is not None else dtype)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=x.device)
+        out = torch.empty_like(x) if out_dtype == dtype else torch.empty(shape, dtype=out_dtype, device=x.device)
     if residual is not None and h is None:
-        h = torch.empty(shape, dtype=dtype, device=x.device)
+        h = torch.empty_like(x)
     dev = _device_of(x, weight, residual, out, h)
     ldx = _rows(x, shape, "x")
     ldy = _rows(out, shape, "out", out_dtype)
