@@ -165,16 +165,16 @@ ts_status operand_pack(Operand* o, uintptr_t base, int es, int tile) {
 }
 
 // Sleeps (320 clocks, FusedStore::start) between the starts of the eight groups of programs.
-// With fp32 C and a matrix read beside it a 256 tile moves 512 KiB after its K loop, as long as
-// 18 K steps at the copy rate while all CUs do it at once; spread over most of a tile's
-// time, the groups' traffic overlaps the others' products.  Measured with 4 tiles a
-// program (4096 x 16384, residual): K = 512 176 -> 138 us, 1024 222 -> 184, 2048 320 -> 287, 4096
-// 511 -> 532, so up to 32 K steps; with 16-bit C, or without a read, 0 to 10 % slower at every K,
-// so not there.
+// With fp32 C a 256 tile moves 256 KiB after its K loop, 512 KiB with a matrix read beside it, as
+// long as 9 or 18 K steps at the copy rate while all CUs do it at once; spread over a part of a
+// tile's time, the groups' traffic overlaps the others' products.  Measured with 4 tiles a program
+// (4096 x 16384), together / spread: with residual K = 512 131 / 121 us, 1024 177 / 166, 2048 274 / 261,
+// 4096 488 / 473; without 512 95 / 86, 1024 137 / 135, and no gain from 2048 on.  With 16-bit C 0 to 10 %
+// slower at every K.  Spread by XCD instead (its programs share operands): residual 512 136, 1024 182.
 int stagger_sleeps(const EpiPlan& e, bool reads) {
     const SchedArgs& s = e.p.s;
-    if (e.kind != EPI_XTILE || e.p.cfg != CFG_256W8 || e.out != TS_F32 || !reads) return 0;
-    return s.ks <= 32 && s.num_tiles >= 3 * (int64_t)s.grid ? 3 * s.ks / 4 : 0;
+    if (e.kind != EPI_XTILE || e.p.cfg != CFG_256W8 || e.out != TS_F32 || s.num_tiles < 3 * (int64_t)s.grid) return 0;
+    return reads ? std::min(s.ks, 64) / 4 + 4 : s.ks <= 16 ? s.ks / 4 : 0;
 }
 
 // The special form of an epilogue, 0 if it has none.  They exist where the 256 tile runs (see
