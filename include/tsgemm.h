@@ -421,8 +421,8 @@ typedef struct {
  *   bit-identical results; TS_MODE_STREAMK as in ts_gemm.  Tiles: TS_TILE_AUTO,
  *   TS_TILE_128x128x64, TS_TILE_256x256x64_W8 (others: TS_ERR_UNSUPPORTED); with
  *   8-bit operands a K step holds 128 values.
- *   Up to 32 rows, A stored [M][K], and a schedule that leaves order, mode, tile and
- *   programs to the library: one pass over B with K split over the waves of a workgroup
+ *   Up to 32 rows, A stored [M][K] (B stored [K][N]: K below 4096, up to 16 rows below
+ *   8192), and a schedule that leaves order, mode, tile and programs to the library: one pass over B with K split over the waves of a workgroup
  *   (sums in another order than the tile kernels', the same on every run), no workspace.
  *   With such a schedule and few tiles, K is split among programs (whole fp32 tiles of sums in
  *   the workspace) and a second kernel adds the parts, in order, and applies the epilogue.

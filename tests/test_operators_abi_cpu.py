@@ -74,7 +74,9 @@ def test_workspace_sizes():
     assert need(100, 64, 1024, (1024, 1, 64, 1)) == 2 * 128 * 128 * 4
     assert need(100, 64, 1024, (1025, 1, 64, 1)) == 2 * 128 * 128 * 4 + up(100 * 2048)
     assert need(130, 300, 16384, (16384, 1, 300, 1)) == 32 * 6 * 128 * 128 * 4
-    assert need(32, 300, 16384, (16384, 1, 300, 1)) == 0                  # few rows
+    assert need(32, 300, 16384, (16384, 1, 1, 16384)) == 0                # few rows, B [N][K]
+    assert need(32, 300, 4088, (4088, 1, 300, 1)) == 0                    # and [K][N]
+    assert need(32, 300, 4096, (4096, 1, 300, 1)) > 0 and need(16, 300, 4096, (4096, 1, 300, 1)) == 0
     assert need(100, 64, 1024, (1024, 1, 64, 1), sched=ts.Schedule(tile="128x128x64")) == 0
     sk = ts.Schedule(mode="streamk", num_programs=7, tile="128x128x64")
     assert need(512, 512, 512, (512, 1, 512, 1), sched=sk) == 256 + 7 * 128 * 128 * 4

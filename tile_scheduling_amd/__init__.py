@@ -30,7 +30,7 @@ _i32, _i64, _p = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 # status codes, element types and schedule enums (include/tsgemm.h)
 TS_OK, TS_ERR_INVALID_ARG, TS_ERR_UNSUPPORTED, TS_ERR_ALIGNMENT, TS_ERR_HIP, TS_ERR_NO_DEVICE = 0, -1, -2, -3, -4, -5
 TS_F16, TS_BF16, TS_F32, TS_E4M3 = 1, 2, 3, 4
-FEW_ROWS = 32   # products of up to this many rows need no workspace (ts_gemm_epilogue)
+FEW_ROWS = 32   # products of up to this many rows mostly need no workspace (ts_gemm_epilogue)
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 ORDERS = {"row_major": 0, "grouped": 1, "auto": 2}
 MODES = {"tiled": 0, "persistent": 1, "crosstile": 2, "streamk": 3, "auto": 4}
@@ -433,7 +433,7 @@ def _product(a, b, out, out_dtype, epi: _Epilogue, schedule, residual=None, prea
     sbk, sbn = b.stride()
     scm, scn = out.stride()
     ws, need = None, 0
-    if M > FEW_ROWS or s is not None or sak != 1 or K <= 1 or N >= 1 << 26:
+    if M > FEW_ROWS or s is not None or sak != 1 or K <= 1 or N >= 1 << 26 or (sbk != 1 and K >= 4096):
         need = _lib.ts_gemm_epilogue_workspace(pa, pb, M, N, K, sam, sak, sbk, sbn, ab_t, c_t, s)
         ws = _scratch(need, a)
     _launch(dev, _lib.ts_gemm_epilogue, pa, pb, out.data_ptr(), M, N, K, sam, sak, sbk, sbn, scm, scn, ab_t, c_t,

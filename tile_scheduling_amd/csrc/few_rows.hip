@@ -291,9 +291,18 @@ __global__ void __launch_bounds__(kNnWaves * 64) few_nn_kernel(FewArgs g) {
 
 namespace {
 
-// Column groups a workgroup: two where that still leaves four workgroups a CU.
+// Column groups a workgroup of few_nt: as few as leave one workgroup on each of 256 CUs, up to two,
+// with more than 16 rows four: the rows of A are read for each group of columns by every
+// workgroup, which for 32 rows is 2 / NX times the bytes of B.  Measured, K = 4096, bf16, one / two / four groups: 1 row
+// N = 4096 7.8 / 10.8 / 18.7 us, 8192 16.6 / 15.2 / 20.7, 28672 47.5 / 46.9 / 47.8; 16 rows 8192 20.7 / 15.9 / 23.9,
+// 28672 64.8 / 50.8 / 50.9; 32 rows 4096 14.1 / 18.6 / 26.8, 8192 27.4 / 20.4 / 28.5, 12290 50.0 / 36.9 / 30.3, 28672
+// 89.9 / 72.6 / 58.4; e4m3, 32 rows, 28672 52.6 / 42.6 / 38.4.
+// Columns a lane of few_nn: two, or four where two make more than 256 workgroups (of 16 waves, one on a
+// CU): 16 rows 8192 x 8192 41.8 / 46.3 us, 12290 x 4096 39.6 / 35.3, 28672 x 4096 77.3 / 59.7.
+constexpr int kGroups = 256;
 template <class TI, class TO, int MT>
 const void* nt_kernel(int nx) {
+    if (nx == 4) return reinterpret_cast<const void*>(&few_nt_kernel<TI, TO, 4, MT, (MT == 1 ? 3 : 2)>);
     if (nx == 2) return reinterpret_cast<const void*>(&few_nt_kernel<TI, TO, 2, MT, 4>);
     return reinterpret_cast<const void*>(&few_nt_kernel<TI, TO, 1, MT, (MT == 1 ? 8 : 4)>);
 }
@@ -318,10 +327,10 @@ hipError_t launch_few_rows(FewArgs& g, int ab, int c, bool b_kmaj, hipStream_t s
     const int mt = g.M > 16 ? 2 : 1;
     int width, cols;
     if (b_kmaj) {
-        width = ((int64_t)g.N + 31) / 32 >= 1024 ? 2 : 1;
+        width = g.N <= 16 * kGroups ? 1 : mt == 1 || g.N <= 32 * kGroups ? 2 : 4;
         cols = 16 * width;
     } else {
-        width = ((int64_t)g.N + 63) / 64 >= 256 ? 4 : 2;
+        width = g.N <= 32 * kGroups ? 2 : 4;
         cols = 16 * width;
     }
     g.tiles = (int)(((int64_t)g.N + cols - 1) / cols);
