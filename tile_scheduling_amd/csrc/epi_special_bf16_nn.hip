@@ -8,4 +8,10 @@ const void* epi_special_bf16_nn(int out_f32, int kind) {
     return out_f32 ? epi_special_by_kind<Cfg256w8, InBF16, OutF32, PATH_EDGE_NN>(kind)
                    : epi_special_by_kind<Cfg256w8, InBF16, OutBF16, PATH_EDGE_NN>(kind);
 }
+// A [K][M]: the plain product only, the weight's gradient.
+const void* epi_special_bf16_tn(int out_f32, int kind) {
+    if (kind != EPI_SPECIAL + 4 * AUX_NONE + FAM_NONE) return nullptr;
+    return out_f32 ? epi_special<Cfg256w8, InBF16, OutF32, PATH_EDGE_AT, FAM_NONE, AUX_NONE>()
+                   : epi_special<Cfg256w8, InBF16, OutBF16, PATH_EDGE_AT, FAM_NONE, AUX_NONE>();
+}
 }  // namespace ts

@@ -805,6 +805,8 @@ const void* epi_special_by_kind(int kind) {
 const void* epi_special_f16_nn(int out_f32, int kind);
 const void* epi_special_f16_nt(int out_f32, int kind);
 const void* epi_special_bf16_nn(int out_f32, int kind);
+const void* epi_special_f16_tn(int out_f32, int kind);
+const void* epi_special_bf16_tn(int out_f32, int kind);
 const void* epi_special_bf16_nt(int out_f32, int kind);
 
 template <class Cfg, class TI, class TO, int PATH>

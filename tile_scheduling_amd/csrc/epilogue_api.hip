@@ -198,6 +198,8 @@ const void* epi_kernel_of(const EpiPlan& e, int32_t ab) {
             fn = ab == TS_F16 ? epi_special_f16_nn(f32, e.special) : ab == TS_BF16 ? epi_special_bf16_nn(f32, e.special) : nullptr;
         if (e.path == PATH_EDGE_BT)
             fn = ab == TS_F16 ? epi_special_f16_nt(f32, e.special) : ab == TS_BF16 ? epi_special_bf16_nt(f32, e.special) : nullptr;
+        if (e.path == PATH_EDGE_AT)
+            fn = ab == TS_F16 ? epi_special_f16_tn(f32, e.special) : ab == TS_BF16 ? epi_special_bf16_tn(f32, e.special) : nullptr;
         if (fn) return fn;
     }
     if (e.p.cfg == CFG_128) {
