@@ -349,6 +349,50 @@ def test_large_tile_and_ragged_large_product():
     R.check(c, z, zerr + R.rounded(z.abs() + zerr, F))
 
 
+@pytest.mark.parametrize("pad,offset", [(60, 0), (3, 1)])
+@pytest.mark.parametrize("dtype,out", [(B, B), (H, H), (B, F), (H, F)])
+@pytest.mark.parametrize("layout", ["nn", "nt", "tn", "tt"])
+def test_every_epilogue_on_the_256_tile(layout, dtype, out, pad, offset):
+    # tiles inside the matrix and on its edges, several a program; C, residual and preact with rows of
+    # whole 128-byte lines (pad 60) and not; every activation with every use of a second matrix
+    M, N, K = 600, 900, 200
+    sched = ts.Schedule(order="auto", mode="auto", tile="256x256x64w8", num_programs=3)
+    a, b, ad, bd = operands(M, N, K, dtype, layout, 77)
+    n = R.gen(5)
+    bias, res = n(N).to(dtype), n(M, N).to(out)
+    z0, zerr0 = R.product(a, b)
+    z1, zerr1 = R.product(a, b, bias)
+    cd, cbuf = R.padded(res, "cuda", pad, offset, fill=7.0)
+    pd, pbuf = R.padded(res, "cuda", pad, offset, fill=7.0)
+    for name in R.ACTS:
+        say(layout, dtype, out, pad, name)
+        ts.gemm_epilogue(ad, bd, bias=bias.cuda(), activation=name, out=cd, schedule=sched)
+        want, bound = R.forward(z1, zerr1, name, None, out)
+        R.check(cd, want, bound, f"{name}")
+        pd.zero_()
+        ts.gemm_epilogue(ad, bd, bias=bias.cuda(), activation=name, preact=pd, out=cd, schedule=sched)
+        R.check(cd, want, bound, f"{name} with preact")
+        R.check(pd, z1, zerr1 + R.rounded(z1.abs() + zerr1, out), f"{name} preact")
+        cd.copy_(res)   # in place
+        ts.gemm_epilogue(ad, bd, bias=bias.cuda(), activation=name, residual=cd, out=cd, schedule=sched)
+        want, bound = R.forward(z1, zerr1, name, res, out)
+        R.check(cd, want, bound, f"{name} with residual")
+        pd.zero_()
+        rd = res.cuda()
+        ts.gemm_epilogue(ad, bd, activation=name, residual=rd, preact=pd, out=cd, schedule=sched)
+        want, bound = R.forward(z0, zerr0, name, res, out)
+        R.check(cd, want, bound, f"{name} with both")
+        R.check(pd, z0, zerr0 + R.rounded(z0.abs() + zerr0, out), f"{name} preact of both")
+        pd.copy_(res)
+        ts.gemm_dact(ad, bd, pd, name, out=pd, schedule=sched)   # in place
+        sl = R.slope(res.double(), name)
+        err = 1.2 * zerr0 + R.ACT_ERR * (res.double().abs() + 1) * z0.abs()
+        R.check(pd, z0 * sl, err + R.rounded((z0 * sl).abs() + err, out), f"{name} gradient")
+    for buf, v in ((cbuf, cd), (pbuf, pd)):   # nothing outside the views was written
+        v.fill_(7.0)
+        assert bool((buf == 7.0).all())
+
+
 def test_layer_forward_and_backward_together():
     # norm -> up projection with activation -> down projection with residual, and back
     M, D, E = 130, 192, 320
