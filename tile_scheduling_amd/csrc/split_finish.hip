@@ -1,6 +1,7 @@
 // Sums of a product's splits along K, in order, and the epilogue of the joined sums: eight
 // columns of a row a thread.  The sums lie in whole tiles, so only C's side has edges.  Bound
-// by the splits x M x N x 4 bytes just written, which the memory-side cache still holds.
+// by the splits x M x N x 4 bytes just written, which the memory-side cache still holds: 4 splits
+// of 1000 x 512 4.2 us, most of it the launch.
 #include <hip/hip_runtime.h>
 
 #include "rows.hpp"
