@@ -549,9 +549,9 @@ gemm_split_kernel(SplitArgs g) {
 // at compile time.  A load's wait then leaves the stores issued after it in flight (loads
 // and stores retire in order on one counter; behind a branch the compiler has to wait for
 // all of them), so the rows of aux_in are fetched one staged part ahead.  Tiles on the edge
-// take FusedStore.  Against it, 4096 x 16384, bf16 C: K = 1024 none 124 / 133 us, gelu 156 / 169,
-// residual 143 / 165, gelu with preact 163 / 187; K = 4096 3 to 7 us in 420 to 470 less; fp32 C
-// level without aux_in, 12 % (1024) and 2 % (4096) less with.
+// take FusedStore.  Against it, us, 4096 x 16384, bf16 C: K = 1024 none 124 / 133, gelu 156 / 169, residual
+// 143 / 165, with relu 142 / 165, gelu with preact 163 / 187, relu's gradient 146 / 170; K = 4096 3 to 27 less in
+// 420 to 480; fp32 C level without aux_in, with residual and relu 172 / 214 (K = 1024) and 469 / 510 (4096).
 // AUX_LINES: preact and C in 16 bits, rows of whole 128-byte lines: stored past the caches, so that
 // the two streams do not push the operands out of them (4096 x 16384 x 4096 gelu 464 -> 440 us, 16384 x
 // 8192 x 2048 530 -> 503; with rows that share lines such stores cost 170 -> 211 us, 5000 x 12290 x 1000,
@@ -777,10 +777,12 @@ template <class Cfg, class TI, class TO, int PATH, int FAM, int AUX>
 const void* epi_special() {
     return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg, TI, TO, PATH, false, SpecialStore<FAM, AUX>>);
 }
-template <class Cfg, class TI, class TO, int PATH, int FAM>
-const void* epi_special_lines() {
+// Two outputs in 16 bits; in fp32 the general form is faster (5000 x 12290 x 1000 relu 252 / 281 us,
+// 4096 x 16384 x 1024 209 / 220).
+template <class Cfg, class TI, class TO, int PATH, int FAM, int AUX>
+const void* epi_special_two() {
     if constexpr (std::is_same<TO, OutF32>::value) return nullptr;
-    else return epi_special<Cfg, TI, TO, PATH, FAM, AUX_LINES>();
+    else return epi_special<Cfg, TI, TO, PATH, FAM, AUX>();
 }
 // The special instances of one type and layout (null: none for this kind).
 template <class Cfg, class TI, class TO, int PATH>
@@ -791,11 +793,16 @@ const void* epi_special_by_kind(int kind) {
         case EPI_SPECIAL + 4 * AUX_NONE + FAM_ERF: return epi_special<Cfg, TI, TO, PATH, FAM_ERF, AUX_NONE>();
         case EPI_SPECIAL + 4 * AUX_NONE + FAM_SIGMOID: return epi_special<Cfg, TI, TO, PATH, FAM_SIGMOID, AUX_NONE>();
         case EPI_SPECIAL + 4 * AUX_RESIDUAL + FAM_NONE: return epi_special<Cfg, TI, TO, PATH, FAM_NONE, AUX_RESIDUAL>();
+        case EPI_SPECIAL + 4 * AUX_RESIDUAL + FAM_RELU: return epi_special<Cfg, TI, TO, PATH, FAM_RELU, AUX_RESIDUAL>();
+        case EPI_SPECIAL + 4 * AUX_RESIDUAL + FAM_ERF: return epi_special<Cfg, TI, TO, PATH, FAM_ERF, AUX_RESIDUAL>();
         case EPI_SPECIAL + 4 * AUX_RESIDUAL + FAM_SIGMOID: return epi_special<Cfg, TI, TO, PATH, FAM_SIGMOID, AUX_RESIDUAL>();
-        case EPI_SPECIAL + 4 * AUX_PREACT + FAM_ERF: return epi_special<Cfg, TI, TO, PATH, FAM_ERF, AUX_PREACT>();
-        case EPI_SPECIAL + 4 * AUX_PREACT + FAM_SIGMOID: return epi_special<Cfg, TI, TO, PATH, FAM_SIGMOID, AUX_PREACT>();
-        case EPI_SPECIAL + 4 * AUX_LINES + FAM_ERF: return epi_special_lines<Cfg, TI, TO, PATH, FAM_ERF>();
-        case EPI_SPECIAL + 4 * AUX_LINES + FAM_SIGMOID: return epi_special_lines<Cfg, TI, TO, PATH, FAM_SIGMOID>();
+        case EPI_SPECIAL + 4 * AUX_PREACT + FAM_NONE: return epi_special_two<Cfg, TI, TO, PATH, FAM_NONE, AUX_PREACT>();
+        case EPI_SPECIAL + 4 * AUX_PREACT + FAM_RELU: return epi_special_two<Cfg, TI, TO, PATH, FAM_RELU, AUX_PREACT>();
+        case EPI_SPECIAL + 4 * AUX_PREACT + FAM_ERF: return epi_special_two<Cfg, TI, TO, PATH, FAM_ERF, AUX_PREACT>();
+        case EPI_SPECIAL + 4 * AUX_PREACT + FAM_SIGMOID: return epi_special_two<Cfg, TI, TO, PATH, FAM_SIGMOID, AUX_PREACT>();
+        case EPI_SPECIAL + 4 * AUX_LINES + FAM_ERF: return epi_special_two<Cfg, TI, TO, PATH, FAM_ERF, AUX_LINES>();
+        case EPI_SPECIAL + 4 * AUX_LINES + FAM_SIGMOID: return epi_special_two<Cfg, TI, TO, PATH, FAM_SIGMOID, AUX_LINES>();
+        case EPI_SPECIAL + 4 * AUX_GRAD + FAM_RELU: return epi_special<Cfg, TI, TO, PATH, FAM_RELU, AUX_GRAD>();
         case EPI_SPECIAL + 4 * AUX_GRAD + FAM_ERF: return epi_special<Cfg, TI, TO, PATH, FAM_ERF, AUX_GRAD>();
         case EPI_SPECIAL + 4 * AUX_GRAD + FAM_SIGMOID: return epi_special<Cfg, TI, TO, PATH, FAM_SIGMOID, AUX_GRAD>();
         default: return nullptr;
