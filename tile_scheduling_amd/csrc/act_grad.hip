@@ -100,6 +100,7 @@ using namespace ts;
 extern "C" int64_t ts_act_grad_workspace(int64_t M, int64_t N) {
     if (M < 0 || N < 0) return TS_ERR_INVALID_ARG;
     if (M > INT_MAX / 2 || N >= 1 << 26) return TS_ERR_UNSUPPORTED;   // N: threads of the sum over the groups
+    if (N == 0) return 0;   // no strips to deal the groups over
     const int64_t groups = num_groups(M, N);
     return groups > 1 ? groups * N * 4 : 0;
 }
