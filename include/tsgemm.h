@@ -478,7 +478,8 @@ int64_t ts_act_grad_workspace(int64_t M, int64_t N);
  * weight: N contiguous elements of w_dtype (x_dtype or TS_F32) or NULL (1); y: M x N of
  * y_dtype, x_dtype or TS_E4M3.  With TS_E4M3 also one fp32 scale per row, max|y| / 448
  * but at least 2^-100, and y holds y / scale rounded to nearest even: the row operand of
- * ts_gemm_epilogue (A with scale_a).  A row with a NaN in y has a NaN scale.
+ * ts_gemm_epilogue (A with scale_a).  A row with a NaN in y has a NaN scale; with N == 0
+ * every row has the least one.
  * residual and h come together or are both NULL.  All of it in fp32; the norm reads the
  * unrounded sum, h is its one rounding.  h may be x or residual; y of x_dtype may
  * be x or residual where h is not.  The current device must be the stream's.

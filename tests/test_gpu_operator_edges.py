@@ -28,3 +28,18 @@ def test_gradients_of_no_columns(M):
         da, dw, db = ts.gemm_epilogue_backward(dc, a, b, preact=z, activation=name)
         assert torch.equal(da, torch.zeros(M, 7, dtype=dtype, device="cuda"))
         assert dw.shape == (7, 0) and db.shape == (0,)
+
+
+@pytest.mark.parametrize("M", [1, 17, 5000])
+def test_norm_of_no_columns(M):
+    # rows without elements: nothing to norm, and the least scale (2^-100) for the e4m3 form
+    filled = [torch.full((max(M, 128),), 5.0, device="cuda") for _ in range(4)]   # what is freed here may come back as the scale
+    del filled
+    for dtype in (H, B, F):
+        x = torch.empty(M, 0, dtype=dtype, device="cuda")
+        for res in (None, torch.empty(M, 0, dtype=dtype, device="cuda")):
+            y, scale, h = ts.rmsnorm(x, torch.empty(0, dtype=dtype, device="cuda"), residual=res)
+            assert y.shape == (M, 0) and scale is None and h.shape == (M, 0)
+            q, scale, h = ts.rmsnorm(x, residual=res, out_dtype=Q)
+            assert q.shape == (M, 0) and h.shape == (M, 0)
+            assert torch.equal(scale, torch.full((M,), 2.0 ** -100, device="cuda"))

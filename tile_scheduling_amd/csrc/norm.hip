@@ -539,9 +539,12 @@ extern "C" ts_status ts_rmsnorm(const void* x, const void* residual, const void*
         return TS_ERR_INVALID_ARG;
     const bool q = y_dtype == TS_E4M3;
     if ((!q && y_dtype != x_dtype) || (weight && w_dtype != x_dtype && w_dtype != TS_F32)) return TS_ERR_UNSUPPORTED;
-    if (M == 0 || N == 0) return TS_OK;
-    if (!x || !y || (residual && !h) || (!residual && h) || (q && !scale)) return TS_ERR_INVALID_ARG;
-    if (M > 1 && (stride_x < N || stride_y < N || (residual && (stride_r < N || stride_h < N)))) return TS_ERR_INVALID_ARG;
+    if (M == 0 || (N == 0 && !q)) return TS_OK;
+    // rows without elements still have their scale, the least one: the kernel below reads and
+    // writes nothing else of them
+    if (q && !scale) return TS_ERR_INVALID_ARG;
+    if (N > 0 && (!x || !y || (residual && !h) || (!residual && h))) return TS_ERR_INVALID_ARG;
+    if (N > 0 && M > 1 && (stride_x < N || stride_y < N || (residual && (stride_r < N || stride_h < N)))) return TS_ERR_INVALID_ARG;
     const int xs = type_size(x_dtype);
     if ((uintptr_t)x % xs || (uintptr_t)residual % xs || (uintptr_t)h % xs || (uintptr_t)y % type_size(y_dtype) ||
         (weight && (uintptr_t)weight % type_size(w_dtype)) || (uintptr_t)scale % 4)
