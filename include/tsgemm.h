@@ -483,6 +483,8 @@ int64_t ts_act_grad_workspace(int64_t M, int64_t N);
  * residual and h come together or are both NULL.  All of it in fp32; the norm reads the
  * unrounded sum, h is its one rounding.  h may be x or residual; y of x_dtype may
  * be x or residual where h is not.  The current device must be the stream's.
+ * Squares are summed in fp32 (here and for the gradients): a row's sum of squares has to lie below
+ * 3.4e38 (else y is 0), and with eps of 0 its mean above 1e-38.
  * TS_ERR_UNSUPPORTED (here and for the gradients): N of 2^26 or more, M of 2^30 or more.
  */
 ts_status ts_rmsnorm(const void* x, const void* residual, const void* weight, void* y, void* h, float* scale,

@@ -43,3 +43,32 @@ def test_norm_of_no_columns(M):
             q, scale, h = ts.rmsnorm(x, residual=res, out_dtype=Q)
             assert q.shape == (M, 0) and h.shape == (M, 0)
             assert torch.equal(scale, torch.full((M,), 2.0 ** -100, device="cuda"))
+
+
+@pytest.mark.parametrize("M,N", [(3, 7), (5, 64), (40, 520), (6, 4096), (9, 16384), (5, 20000), (3, 32776)])
+@pytest.mark.parametrize("dtype", [B, F])
+def test_norm_backward_far_from_unit_scale(M, N, dtype):
+    # rows of every magnitude that the forward pass takes: r^3 is outside fp32's range for most of them,
+    # dx is not
+    n = R.gen(M + 5 * N)
+    at = torch.tensor([1e15, 1e-14, 1e12, 1e17, 1e-17, 1.0, 1e-6, 1e9, 3e16] * 5)[:M]
+    h = (n(M, N) * at[:, None]).to(dtype)
+    # dy aligned with h in part, so that the mean is no small difference
+    unit = h.double() / at[:, None].double()
+    dy, w = (n(M, N) + unit.float()).to(dtype), (1 + 0.2 * n(N)).to(dtype)
+    say(M, N, dtype)
+    for eps in (1e-36, 0.0):
+        dx, dw = ts.rmsnorm_backward(dy.cuda(), h.cuda(), w.cuda(), eps=eps)
+        h64, dy64, w64 = h.double(), dy.double(), w.double()
+        r = 1.0 / torch.sqrt((h64 * h64).mean(1, keepdim=True) + eps)
+        g, u = w64 * dy64, h64 * r
+        mean = (g * u).mean(1, keepdim=True)
+        want = r * (g - u * mean)
+        # r: (N/2 + 8) U; the mean's sum N U of its terms' magnitudes and r twice; then a few products
+        rerr = (N / 2 + 8) * R.U
+        merr = (g * u).abs().mean(1, keepdim=True) * ((N + 8) * R.U + 2 * rerr)
+        err = (r * g).abs() * (rerr + 4 * R.U) + (r * u).abs() * (merr + (rerr + 4 * R.U) * mean.abs()) + 2 * R.U * want.abs()
+        R.check(dx, want, err + R.rounded(want.abs() + err, dtype) + 2.0 ** -126, f"dx eps {eps}")
+        wd = (dy64 * u).sum(0)
+        derr = (dy64 * u).abs().sum(0) * ((M + 4) * R.U + rerr)
+        R.check(dw, wd, derr + R.rounded(wd.abs() + derr, dtype), "dweight")

@@ -4,6 +4,10 @@
 //   h = x + residual,  r = 1 / sqrt(mean(h^2) + eps),  y = h r w
 //   dx = r (w dy) - h r^3 mean(w dy h) + dh,  dw = sum over rows of dy h r
 //
+// r^3 is never formed: from an rms of 4e12 on it is too small for fp32, below 1e-13 too large, far
+// inside the range of h.  The second term is (h r) (r (r mean(w dy h))), whose every factor is of
+// the size of h's own unit vector, dy or dx.
+//
 // Both are bound by memory: a row is read once into registers, where its sums, its largest
 // |y| and its outputs are formed; nothing is read twice.  Measured, bf16: 5000 x 8192 with residual to
 // e4m3 54 us (287 MB, 5.3 TB/s); gradients of 8192 x 4096 with dh 47 us (268 MB) and 6.5 us for the sum of
@@ -205,7 +209,7 @@ struct NormGradArgs {
     const void *dy, *h, *weight, *dh;
     void* dx;
     float* part;    // partial sums of dw, one row of N per workgroup, or null
-    float* stats;   // long rows: r and r^3 mean(w dy h) of every row
+    float* stats;   // long rows: r and r^2 mean(w dy h) of every row
     int M, N, w_type;
     long long ldy, ldh, lds, ldx;
     float eps;
@@ -251,7 +255,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rmsnorm_grad_kernel(NormGra
         s1 = row_sum<T>(s1, lds1);
         s2 = row_sum<T>(s2, lds2);
         const float r = 1.0f / __builtin_sqrtf(s1 / (float)g.N + g.eps);
-        const float k = r * r * r * (s2 / (float)g.N);
+        const float k = r * (r * (s2 / (float)g.N));
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int n = (c * T + t) * 8, valid = g.N - n;
@@ -259,8 +263,9 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rmsnorm_grad_kernel(NormGra
             float d[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                dw[c][e] = __builtin_fmaf(dy[c][e], h[c][e] * r, dw[c][e]);
-                d[e] = __builtin_fmaf(r * w[c][e], dy[c][e], -(h[c][e] * k));
+                const float unit = h[c][e] * r;
+                dw[c][e] = __builtin_fmaf(dy[c][e], unit, dw[c][e]);
+                d[e] = __builtin_fmaf(r * w[c][e], dy[c][e], -(unit * k));
             }
             if (g.dh) {
                 float a[8];
@@ -324,7 +329,7 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_grad_stats_kernel(NormGr
     if (threadIdx.x == 0) {
         const float r = 1.0f / __builtin_sqrtf(s1 / (float)g.N + g.eps);
         g.stats[2 * m] = r;
-        g.stats[2 * m + 1] = r * r * r * (s2 / (float)g.N);
+        g.stats[2 * m + 1] = r * (r * (s2 / (float)g.N));
     }
 }
 // 256 threads: 64 strips of eight columns x 4 rows; blockIdx.y is the row group.
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_grad_dx_kernel(NormGradA
         if (g.weight) load8_vec<TX>(g.weight, g.w_type, n, valid, w);
         if (g.dh) load8<TX>(static_cast<const X*>(g.dh) + m * g.lds + n, valid, a);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] += __builtin_fmaf(r * w[e], dy[e], -(h[e] * k));
+        for (int e = 0; e < 8; ++e) a[e] += __builtin_fmaf(r * w[e], dy[e], -(h[e] * r * k));
         store8<TX>(static_cast<X*>(g.dx) + m * g.ldx + n, valid, a);
     }
 }
