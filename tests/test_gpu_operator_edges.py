@@ -72,3 +72,60 @@ def test_norm_backward_far_from_unit_scale(M, N, dtype):
         wd = (dy64 * u).sum(0)
         derr = (dy64 * u).abs().sum(0) * ((M + 4) * R.U + rerr)
         R.check(dw, wd, derr + R.rounded(wd.abs() + derr, dtype), "dweight")
+
+
+def infinite(M, N, K, dtype):
+    """Operands whose product is infinite, of either sign, in rows 1 and 2 and finite elsewhere."""
+    n = R.gen(M + N + K)
+    a, b = n(M, K).to(dtype), (n(K, N) / max(K, 1) ** 0.5).to(dtype)
+    a[1, 0] = float("inf")
+    a[min(2, M - 1), K - 1] = float("-inf")
+    return a, b
+
+
+@pytest.mark.parametrize("layout", ["nn", "nt"])
+@pytest.mark.parametrize("M,N,K,tile", [(3, 40, 96, None), (32, 300, 72, None), (60, 70, 2048, None), (200, 140, 96, None),
+                                        (600, 520, 128, "256x256x64w8")])
+@pytest.mark.parametrize("name", R.ACTS)
+def test_infinite_products(M, N, K, tile, layout, name):
+    # few rows, K split, the 128 and the 256 tile: act(+-inf) as the definition evaluates it, the other
+    # rows untouched
+    sched = None if tile is None else ts.Schedule(order="auto", mode="auto", tile=tile, num_programs=3)
+    for dtype, out in ((H, H), (B, F)):
+        a, b = infinite(M, N, K, dtype)
+        ad, bd = a.cuda(), (b.cuda() if layout == "nn" else b.t().contiguous().cuda().t())
+        say(M, N, K, tile, layout, name, dtype)
+        z, zerr = R.product(a, b)
+        _, bound = R.forward(z, zerr, name, None, out)
+        want = z.clamp_min(0.0) if name == "relu" else R.act(z, name)
+        finite = torch.isfinite(z)
+        res = torch.ones(M, N, dtype=out, device="cuda")
+        for residual in (None, res):
+            add = 0.0 if residual is None else 1.0
+            c = ts.gemm_epilogue(ad, bd, activation=name, residual=residual, out_dtype=out, schedule=sched).double().cpu()
+            w = want + add
+            same = (c == w) | (c.isnan() & w.isnan())
+            assert bool(same[~finite].all()), (name, "infinite sums")
+            off = (c - w).abs()[finite]
+            assert bool((off <= (bound + 2 * R.U * (w.abs() + 1) + R.rounded(w.abs(), out))[finite]).all()), (name, "finite sums")
+
+
+@pytest.mark.parametrize("name", R.ACTS)
+def test_activation_of_every_magnitude(name):
+    # z itself as the product with a unit matrix, from the smallest to the largest, and its ends
+    mags = torch.tensor([10.0 ** e for e in range(-37, 39)] + [64.0, 88.0, 104.0, 128.0, 3.0e38, float("inf")])
+    z = torch.cat([mags, -mags, torch.tensor([0.0, float("nan")])]).to(B)
+    for M in (1, 40):
+        c = ts.gemm_epilogue(torch.ones(M, 1, dtype=B, device="cuda"), z[None].cuda(), activation=name, out_dtype=F)
+        z64 = z.double()
+        want = (z64.clamp_min(0.0) if name == "relu" else R.act(z64, name)).expand(M, -1)
+        got = c.double().cpu()
+        nan = want.isnan()
+        assert bool(got.isnan()[nan].all()), name
+        inf = want.isinf()
+        assert bool((got == want)[inf].all()), name
+        rest = ~nan & ~inf
+        size = z64.abs().expand(M, -1)
+        # positive arguments: relative; negative ones leave a tail, absolutely small
+        bound = R.ACT_ERR * torch.where(z64 > 0, size, (size + 1).clamp_max(300.0)) + 2.0 ** -126
+        assert bool(((got - want).abs()[rest] <= bound[rest]).all()), name

@@ -55,6 +55,9 @@ enum : int { FAM_NONE = 0, FAM_RELU = 1, FAM_ERF = 2, FAM_SIGMOID = 3 };
 struct Sigmoid {
     float w0, w1;
 };
+// From here on the sigmoid of both is 1 in fp32; the argument stops there, as silu's w1 z would be
+// 0 times infinity at the end of the range.  NaN comes back through the factor z.
+constexpr float kSaturated = 64.0f;
 __device__ __forceinline__ Sigmoid sigmoid_of(int act) {
     return act == ACT_SILU ? Sigmoid{1.0f, 0.0f} : Sigmoid{kTanhW0, kTanhW1};
 }
@@ -65,7 +68,10 @@ __device__ __forceinline__ float fam_value(float z, Sigmoid c) {
         const float q = tail_scaled(__builtin_fabsf(z)) * __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z);
         return z * (z < 0.0f ? q : 1.0f - q);
     }
-    if constexpr (FAM == FAM_SIGMOID) return z * sigmoid(z * __builtin_fmaf(c.w1 * z, z, c.w0));
+    if constexpr (FAM == FAM_SIGMOID) {
+        const float t = __builtin_fminf(z, kSaturated);
+        return z * sigmoid(t * __builtin_fmaf(c.w1 * t, t, c.w0));
+    }
     return z;
 }
 template <int FAM>
