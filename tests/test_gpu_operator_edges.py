@@ -129,3 +129,33 @@ def test_activation_of_every_magnitude(name):
         # positive arguments: relative; negative ones leave a tail, absolutely small
         bound = R.ACT_ERR * torch.where(z64 > 0, size, (size + 1).clamp_max(300.0)) + 2.0 ** -126
         assert bool(((got - want).abs()[rest] <= bound[rest]).all()), name
+
+
+@pytest.mark.parametrize("name", R.ACTS)
+@pytest.mark.parametrize("dtype", [B, F])
+def test_slopes_of_every_magnitude(name, dtype):
+    # act' of any finite value is finite: act_grad, and the product's gradient form on each of its kernels
+    mags = torch.tensor([10.0 ** e for e in range(-37, 39)] + [64.0, 88.0, 104.0, 128.0, 3.0e38])
+    z = torch.cat([mags, -mags, torch.tensor([0.0])]).to(dtype)
+    N = z.numel()
+    want = R.slope(z.double(), name)
+    # far out the definition's own 64-bit terms overflow to NaN: the limit there
+    far = z.double().abs() > 1e6
+    if name != "relu" and name != "none":
+        want = torch.where(far, (z.double() > 0).double(), want)
+    bound = R.ACT_ERR * (z.double().abs() + 1).clamp_max(300.0)
+    dz, _ = ts.act_grad(torch.ones(9, N, dtype=dtype, device="cuda"), z.expand(9, N).contiguous().cuda(), name)
+    R.check(dz, want.expand(9, N), (bound + R.rounded(want.abs() + bound, dtype)).expand(9, N), "act_grad")
+    op = B if dtype == B else H
+    for M, K, tile in ((4, 8, None), (40, 8, None), (40, 2048, None), (300, 64, "256x256x64w8")):
+        reps = 1 if tile is None else 4
+        zz = z.repeat(reps).expand(M, -1).contiguous().cuda()
+        a = torch.zeros(M, K, dtype=op, device="cuda")
+        a[:, 0] = 1.0
+        b = torch.zeros(K, N * reps, dtype=op, device="cuda")
+        b[0] = 1.0
+        sched = None if tile is None else ts.Schedule(order="auto", mode="auto", tile=tile)
+        say(name, dtype, M, K, tile)
+        got = ts.gemm_dact(a, b, zz, name, schedule=sched)
+        w, bo = want.repeat(reps).expand(M, -1), bound.repeat(reps).expand(M, -1)
+        R.check(got, w, bo + R.rounded(w.abs() + bo, dtype), f"dact {M} {K}")

@@ -84,7 +84,9 @@ __device__ __forceinline__ float fam_slope(float z, Sigmoid c) {
     }
     if constexpr (FAM == FAM_SIGMOID) {
         const float g = sigmoid(z * __builtin_fmaf(c.w1 * z, z, c.w0));
-        return __builtin_fmaf(z * (g * (1.0f - g)), __builtin_fmaf(3.0f * c.w1 * z, z, c.w0), g);
+        // where z^2 overflows, g (1 - g) is 0: the factor beside it stays finite
+        const float d = __builtin_fminf(__builtin_fmaf(3.0f * c.w1 * z, z, c.w0), 1e30f);
+        return __builtin_fmaf(z * (g * (1.0f - g)), d, g);
     }
     return 1.0f;
 }
