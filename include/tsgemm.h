@@ -403,12 +403,12 @@ typedef struct {
 
 /*
  * The product with a fused epilogue, in one pass over C:
- *     z = (A @ B) * scale_a[m] * scale_b[n] + bias[n]
+ *     z = ((A @ B) * scale_a[m]) * scale_b[n] + bias[n]
  *     grad 0:  preact = z (if given),  C = act(z) + residual
  *     grad 1:  C = z * act'(preact)    (the gradient of a product that feeds an
  *              activation; no bias, no residual)
- * All of it in fp32 from the fp32 sums; preact and C are each rounded once, to C's
- * type.  epi == NULL: the plain product.
+ * All of it in fp32 from the fp32 sums (the scales multiply in this order: what overflows on the
+ * way is infinite); preact and C are each rounded once, to C's type.  epi == NULL: the plain product.
  *   ab_dtype / c_dtype: TS_F16 -> TS_F16, TS_F32; TS_BF16 -> TS_BF16, TS_F32;
  *   TS_E4M3 -> TS_F16, TS_BF16, TS_F32.  Layouts and strides of A, B and C as in
  *   ts_gemm; with TS_E4M3 only A stored [M][K] and B stored [N][K] (stride_bk == 1).

@@ -159,3 +159,24 @@ def test_slopes_of_every_magnitude(name, dtype):
         got = ts.gemm_dact(a, b, zz, name, schedule=sched)
         w, bo = want.repeat(reps).expand(M, -1), bound.repeat(reps).expand(M, -1)
         R.check(got, w, bo + R.rounded(w.abs() + bo, dtype), f"dact {M} {K}")
+
+
+@pytest.mark.parametrize("M,K,sched", [(1, 64, None), (32, 64, None), (33, 64, None), (33, 2048, None), (200, 64, "128x128x64"),
+                                       (300, 256, "256x256x64w8"), (300, 2048, "streamk")])
+def test_scales_multiply_in_the_order_they_are_written(M, K, sched):
+    # ((A @ B) * scale_a) * scale_b on every kernel: the scales' own product is outside fp32's range
+    s = None
+    if sched == "streamk":
+        s = ts.Schedule(mode="streamk", num_programs=7, tile="128x128x64")
+    elif sched:
+        s = ts.Schedule(order="auto", mode="auto", tile=sched)
+    N = 130 if sched != "256x256x64w8" else 520
+    for ea, eb, va, vb in ((70, 60, 2.0 ** -9, 2.0 ** -9), (-100, -50, 256.0, 256.0), (100, -120, 1.0, 1.0)):
+        a, b = torch.zeros(M, K), torch.zeros(N, K)
+        a[:, 5], b[:, 5] = va, vb
+        a[:, K - 1], b[:, K - 1] = va, vb
+        want = ((2 * va * vb) * 2.0 ** ea) * 2.0 ** eb
+        say(M, K, sched, ea, eb)
+        c = ts.gemm_scaled(a.to(Q).cuda(), b.to(Q).cuda().t(), torch.full((M,), 2.0 ** ea, device="cuda"),
+                           torch.full((N,), 2.0 ** eb, device="cuda"), out_dtype=F, schedule=s)
+        assert bool((c.double() == want).all()), (ea, eb, float(c[0, 0]), want)

@@ -472,7 +472,7 @@ def gemm_scaled(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor | None =
                 residual: torch.Tensor | None = None, preact: torch.Tensor | None = None,
                 out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
                 schedule: Schedule | None = None) -> torch.Tensor:
-    """C = act((A @ B) * scale_a[:, None] * scale_b[None, :] + bias) + residual with e4m3 A
+    """C = act(((A @ B) * scale_a[:, None]) * scale_b[None, :] + bias) + residual with e4m3 A
     [M,K] (rows contiguous) and B [K,N] stored [N][K] (a transposed view of [N,K] weights).
 
     ``scale_a`` [M] and ``scale_b`` [N] are fp32 (None: 1); an element's value is

@@ -2,7 +2,9 @@
 // 8-bit operands, applied to the fp32 accumulators before their one rounding, and the
 // activations with their derivatives.
 //
-//   z = acc * scale_a[m] * scale_b[n] + bias[n]        (scales: 8-bit operands only)
+//   z = (acc * scale_a[m]) * scale_b[n] + bias[n]      (scales: 8-bit operands only; in this order
+//                                                       on every path, as their own product may
+//                                                       leave the range)
 //   forward   preact = z;  C = act(z) + residual
 //   gradient  C = z * act'(preact)
 //
@@ -393,7 +395,7 @@ struct FusedStore {
                     if (PARTS) e.add_parts(a, pt, (i * E::FN + j) * 4 + q, tt);
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        e.acc[i][j][4 * q + c] = E::PAIRS ? __builtin_fmaf(a[c], sa[i] * sb[q][c], bias[q][c]) : a[c] + bias[q][c];
+                        e.acc[i][j][4 * q + c] = E::PAIRS ? __builtin_fmaf(a[c] * sa[i], sb[q][c], bias[q][c]) : a[c] + bias[q][c];
                 }
             __builtin_amdgcn_sched_barrier(0);
         }

@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(256) split_finish_kernel(SplitArgs g) {
         float sb[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
         if (g.scale_b) load8<OutF32>(g.scale_b + n, valid, sb);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= sa * sb[e];
+        for (int e = 0; e < 8; ++e) v[e] = v[e] * sa * sb[e];
     }
     if (g.bias) {
         float bias[8];
