@@ -180,3 +180,24 @@ def test_scales_multiply_in_the_order_they_are_written(M, K, sched):
         c = ts.gemm_scaled(a.to(Q).cuda(), b.to(Q).cuda().t(), torch.full((M,), 2.0 ** ea, device="cuda"),
                            torch.full((N,), 2.0 ** eb, device="cuda"), out_dtype=F, schedule=s)
         assert bool((c.double() == want).all()), (ea, eb, float(c[0, 0]), want)
+
+
+def test_stream_k_order_does_not_depend_on_earlier_calls():
+    # the automatic order depends on the grid, and a stream-K grid on the number of K steps: a call with few
+    # steps in front must not lend its order to one with many on the same tiles, where it would move the cuts
+    # along K and with them the bits
+    tile, P = "256x256x64w8", 72
+    for nm, nn, short, long in ((3, 5, 2, 12), (4, 6, 2, 12), (5, 4, 2, 16)):
+        M, N = 256 * nm, 256 * nn
+        n = R.gen(nm)
+        auto = ts.Schedule(order="auto", mode="streamk", num_programs=P, tile=tile)
+        got = []
+        for K in (64 * short, 64 * long):
+            a, b = n(M, K).to(H).cuda(), (n(K, N) / K ** 0.5).to(H).cuda()
+            q = ts.query(M, N, K, auto)
+            fixed = ts.Schedule(order=("row_major", "grouped")[q["order"]], group_m=max(q["group_m"], 1), mode="streamk",
+                                num_programs=P, xcd_remap=bool(q["xcd_remap"]), tile=tile)
+            say(nm, nn, K, fixed.label())
+            got.append((q["order"], q["group_m"], q["xcd_remap"]))
+            assert torch.equal(ts.gemm_epilogue(a, b, out_dtype=F, schedule=auto), ts.gemm_epilogue(a, b, out_dtype=F, schedule=fixed))
+        assert got[0] != got[1]   # the shapes are such that the choice differs

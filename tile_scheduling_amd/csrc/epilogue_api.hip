@@ -236,16 +236,15 @@ int occupancy_of(int dev, const void* fn, int threads) {
     return n;
 }
 
-// resolve_grid with the chosen order kept by tile grid.
+// resolve_grid with the chosen order kept by what it depends on: the tile grid, the programs (in
+// stream-K mode at most one per K step, so the number of K steps counts) and how many of them run
+// together.
 ts_status resolve(Plan* p, int cu_count, int ppc, int xcds) {
     if (!p->auto_order || p->s.num_tiles == 0) return resolve_grid(p, cu_count, ppc, xcds);
-    Plan q = *p;   // the grid does not depend on the order
-    q.auto_order = false;
-    q.s.num_tiles = p->s.num_tiles;
+    const int64_t cap = p->mode == TS_MODE_STREAMK ? (int64_t)p->s.num_tiles * std::max(p->s.ks, 1) : p->s.num_tiles;
     const int64_t want = p->mode == TS_MODE_TILED ? p->s.num_tiles
                                                   : (p->requested_programs ? p->requested_programs : cu_count * ppc);
-    const auto key = std::make_tuple(p->s.nm, p->s.nn, (int)(want < INT_MAX ? want : INT_MAX), cu_count * ppc,
-                                     xcds * 8 + p->mode);
+    const auto key = std::make_tuple(p->s.nm, p->s.nn, (int)std::min(want, cap), cu_count * ppc, xcds * 8 + p->mode);
     OrderChoice c;
     bool found = false;
     {
