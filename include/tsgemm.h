@@ -430,6 +430,7 @@ typedef struct {
  *   256-byte aligned, contents arbitrary (a stream-K launch clears its own flags);
  *   calls that share one must not overlap in time.  NULL where none is needed.
  *   The current device must be the stream's.
+ *   C and preact lie on no input, except as stated at ts_epilogue, and then with its row stride.
  *   Errors: as ts_gemm; TS_ERR_INVALID_ARG for a bad epilogue.  TS_ERR_UNSUPPORTED: rows
  *   of 2^30 bytes per tile or more (K of 2^21 16-bit elements on the 256 tile), row
  *   strides of C, residual or preact of 2^26 elements or more.
@@ -460,7 +461,7 @@ int64_t ts_gemm_epilogue_workspace(const void* A, const void* B,
  * (in_dtype; from TS_F32 any of the three), unit column strides; dbias: N contiguous
  * elements of bias_dtype.  dZ or dbias may be NULL (not wanted); preact is read unless
  * activation is TS_ACT_NONE.  dbias sums the unrounded fp32 products in a fixed order.
- * dZ may be dC or preact.  M == 0: dbias is set to zero.  workspace (for dbias): at
+ * dZ may be dC or preact, in their type and row stride.  M == 0: dbias is set to zero.  workspace (for dbias): at
  * least ts_act_grad_workspace(M, N) bytes, 256-byte aligned, contents arbitrary, not
  * shared by calls that overlap in time.  The current device must be the stream's.
  * TS_ERR_UNSUPPORTED: N of 2^26 or more, M of 2^30 or more.
@@ -482,7 +483,7 @@ int64_t ts_act_grad_workspace(int64_t M, int64_t N);
  * every row has the least one.
  * residual and h come together or are both NULL.  All of it in fp32; the norm reads the
  * unrounded sum, h is its one rounding.  h may be x or residual; y of x_dtype may
- * be x or residual where h is not.  The current device must be the stream's.
+ * be x or residual where h is not; with its row stride.  The current device must be the stream's.
  * Squares are summed in fp32 (here and for the gradients): a row's sum of squares has to lie below
  * 3.4e38 (else y is 0), and with eps of 0 its mean above 1e-38.
  * TS_ERR_UNSUPPORTED (here and for the gradients): N of 2^26 or more, M of 2^30 or more.
@@ -496,7 +497,7 @@ ts_status ts_rmsnorm(const void* x, const void* residual, const void* weight, vo
  *     dx = r weight dy - h r^3 mean(weight dy h) + dh      (x's and the residual's alike)
  *     dweight[n] = sum over m of dy h r
  * dy, h, dh (NULL: 0; the gradient that reaches h along the residual stream) and dx:
- * M x N of dtype; dx may be dy or dh.  weight NULL: 1.  dweight: w_dtype, or NULL.  Sums
+ * M x N of dtype; dx may be dy or dh, with its row stride.  weight NULL: 1.  dweight: w_dtype, or NULL.  Sums
  * in fp32, in a fixed order.  workspace (with dweight, and for rows of more than 32768):
  * at least ts_rmsnorm_backward_workspace(M, N) bytes, 256-byte aligned, contents
  * arbitrary, not shared by calls that overlap in time.

@@ -201,3 +201,16 @@ def test_stream_k_order_does_not_depend_on_earlier_calls():
             got.append((q["order"], q["group_m"], q["xcd_remap"]))
             assert torch.equal(ts.gemm_epilogue(a, b, out_dtype=F, schedule=auto), ts.gemm_epilogue(a, b, out_dtype=F, schedule=fixed))
         assert got[0] != got[1]   # the shapes are such that the choice differs
+
+
+def test_outputs_that_would_overwrite_what_is_still_read():
+    # dZ of 16 bits over an fp32 dC, y over h, another row stride in place: errors before any launch
+    x, w = torch.ones(40, 40, dtype=B, device="cuda"), torch.ones(40, 40, dtype=B, device="cuda")
+    dc = torch.ones(40, 40, dtype=F, device="cuda")
+    for call in (lambda: ts.act_grad(dc, None, "none", out=dc.view(B)[:, :40]),
+                 lambda: ts.rmsnorm(x, w[0], residual=w, h=x, out=x),
+                 lambda: ts.rmsnorm(dc[:, :20], out=dc.view(-1)[:800].view(40, 20))):
+        with pytest.raises(ts.TsError) as e:
+            call()
+        assert e.value.status == ts.TS_ERR_INVALID_ARG
+    assert bool((x == 1).all()) and bool((w == 1).all()) and bool((dc == 1).all())

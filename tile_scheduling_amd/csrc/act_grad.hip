@@ -122,6 +122,9 @@ extern "C" ts_status ts_act_grad(const void* dc, const void* preact, void* dz, v
     if ((uintptr_t)dc % type_size(in_dtype) || (uintptr_t)preact % type_size(in_dtype) ||
         (uintptr_t)dz % type_size(out_dtype) || (dbias && (uintptr_t)dbias % type_size(bias_dtype)))
         return TS_ERR_ALIGNMENT;
+    if (!in_place_ok(dz, dc, out_dtype == in_dtype, M, stride_dz, stride_dc) ||
+        !in_place_ok(dz, preact, out_dtype == in_dtype, M, stride_dz, stride_pm))
+        return TS_ERR_INVALID_ARG;
     if (dbias && need > 0 && (!workspace || workspace_bytes < need || (uintptr_t)workspace % 256)) return TS_ERR_INVALID_ARG;
     int dev;
     if (hipGetDevice(&dev) != hipSuccess) {

@@ -15,6 +15,7 @@
 #include "few_rows.hpp"
 #include "split.hpp"
 #include "plan.hpp"
+#include "rows.hpp"
 
 namespace ts {
 
@@ -472,6 +473,9 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
         return TS_ERR_UNSUPPORTED;
     const int ce = c_dtype == TS_F32 ? 4 : 2;
     if ((uintptr_t)A % e.es || (uintptr_t)B % e.es || (uintptr_t)C % ce) return TS_ERR_ALIGNMENT;
+    if (epi && (!in_place_ok(C, epi->residual, true, M, stride_cm, epi->stride_rm) ||
+                !in_place_ok(C, epi->preact, true, M, stride_cm, epi->stride_pm)))
+        return TS_ERR_INVALID_ARG;
 
     const ts_epilogue plain = {};
     e.special = special_kind(epi ? *epi : plain, C, stride_cm, c_dtype);

@@ -554,6 +554,10 @@ extern "C" ts_status ts_rmsnorm(const void* x, const void* residual, const void*
     if ((uintptr_t)x % xs || (uintptr_t)residual % xs || (uintptr_t)h % xs || (uintptr_t)y % type_size(y_dtype) ||
         (weight && (uintptr_t)weight % type_size(w_dtype)) || (uintptr_t)scale % 4)
         return TS_ERR_ALIGNMENT;
+    if (N > 0 && (y == h || !in_place_ok(h, x, true, M, stride_h, stride_x) ||
+                  !in_place_ok(h, residual, true, M, stride_h, stride_r) ||
+                  !in_place_ok(y, x, !q, M, stride_y, stride_x) || !in_place_ok(y, residual, !q, M, stride_y, stride_r)))
+        return TS_ERR_INVALID_ARG;
     st = have_device();
     if (st != TS_OK) return st;
     NormArgs g = {x, residual, weight, y, h, scale, (int)M, (int)N, w_dtype, stride_x, stride_r, stride_y, stride_h, eps};
@@ -589,6 +593,9 @@ extern "C" ts_status ts_rmsnorm_backward(const void* dy, const void* h, const vo
     if ((uintptr_t)dy % xs || (uintptr_t)h % xs || (uintptr_t)dh % xs || (uintptr_t)dx % xs ||
         ((weight || dweight) && ((uintptr_t)weight % type_size(w_dtype) || (uintptr_t)dweight % type_size(w_dtype))))
         return TS_ERR_ALIGNMENT;
+    if (!in_place_ok(dx, dy, true, M, stride_dx, stride_dy) || !in_place_ok(dx, h, true, M, stride_dx, stride_h) ||
+        !in_place_ok(dx, dh, true, M, stride_dx, stride_dh))
+        return TS_ERR_INVALID_ARG;
     const bool long_rows = norm_shape(M, N, 4).t == 0;
     const int64_t groups = M > 0 ? norm_grad_groups(M, N) : 0;
     const int64_t part = (groups * N * 4 + 255) / 256 * 256;

@@ -9,6 +9,12 @@
 
 namespace ts {
 
+// Whether an output at `out` may lie on an input at `in`: not on it at all, or element on element
+// (each is read before it is written, by the same thread), so of one type and row stride.
+inline bool in_place_ok(const void* out, const void* in, bool same_type, int64_t M, int64_t ld_out, int64_t ld_in) {
+    return !out || out != in || (same_type && (M <= 1 || ld_out == ld_in));
+}
+
 // Eight consecutive elements of a row <-> eight floats, whatever the type: one 16-byte
 // access (two for fp32) at element alignment; `valid` < 8 at the end of a row.
 template <class TO>
