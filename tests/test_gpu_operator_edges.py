@@ -214,3 +214,16 @@ def test_outputs_that_would_overwrite_what_is_still_read():
             call()
         assert e.value.status == ts.TS_ERR_INVALID_ARG
     assert bool((x == 1).all()) and bool((w == 1).all()) and bool((dc == 1).all())
+
+
+def test_output_on_an_operand_is_refused():
+    x, w = torch.ones(40, 40, dtype=B, device="cuda"), torch.ones(40, 40, dtype=B, device="cuda")
+    for out in (x, w):
+        with pytest.raises(ValueError, match="operand"):
+            ts.gemm_epilogue(x, w, out=out)
+        with pytest.raises(ValueError, match="operand"):
+            ts.gemm_epilogue(x, w.t(), out=out, activation="gelu")
+    assert bool((x == 1).all()) and bool((w == 1).all())
+    # nothing to write: an operand of no elements may lie anywhere
+    e = torch.empty(0, 40, dtype=B, device="cuda")
+    assert ts.gemm_epilogue(e, w, out=e).shape == (0, 40)

@@ -428,7 +428,9 @@ def _product(a, b, out, out_dtype, epi: _Epilogue, schedule, residual=None, prea
         epi.scale_b = scale_b.data_ptr()
     s = ctypes.byref(schedule._c()) if schedule is not None else None
     ab_t, c_t = _DTYPE.get(a.dtype, 0), _DTYPE.get(out_dtype, 0)
-    pa, pb = a.data_ptr(), b.data_ptr()
+    pa, pb, pc = a.data_ptr(), b.data_ptr(), out.data_ptr()
+    if (pc == pa or pc == pb) and M and N and K:
+        raise ValueError("out must not be an operand of the product")
     sam, sak = a.stride()
     sbk, sbn = b.stride()
     scm, scn = out.stride()
@@ -436,7 +438,7 @@ def _product(a, b, out, out_dtype, epi: _Epilogue, schedule, residual=None, prea
     if M > FEW_ROWS or s is not None or sak != 1 or K <= 1 or N >= 1 << 26 or (sbk != 1 and K >= 4096):
         need = _lib.ts_gemm_epilogue_workspace(pa, pb, M, N, K, sam, sak, sbk, sbn, ab_t, c_t, s)
         ws = _scratch(need, a)
-    _launch(dev, _lib.ts_gemm_epilogue, pa, pb, out.data_ptr(), M, N, K, sam, sak, sbk, sbn, scm, scn, ab_t, c_t,
+    _launch(dev, _lib.ts_gemm_epilogue, pa, pb, pc, M, N, K, sam, sak, sbk, sbn, scm, scn, ab_t, c_t,
             ctypes.byref(epi), s, _raw_stream(dev), ws.data_ptr() if need else None, need)
     return out
 
