@@ -227,3 +227,86 @@ def test_output_on_an_operand_is_refused():
     # nothing to write: an operand of no elements may lie anywhere
     e = torch.empty(0, 40, dtype=B, device="cuda")
     assert ts.gemm_epilogue(e, w, out=e).shape == (0, 40)
+
+
+def quantised(x):
+    s = (x.abs().amax(1) / 448).clamp_min(2.0 ** -100)
+    return (x / s[:, None]).to(Q), s
+
+
+@pytest.mark.parametrize("out", [H, B, F])
+@pytest.mark.parametrize("K,pad", [(272, 0), (272, 16), (333, 0), (400, 7)])
+def test_every_epilogue_of_8_bit_products_on_the_256_tile(K, pad, out):
+    # the 8-bit products (16-bit C) and the widened ones (fp32 C): tiles inside the matrix and on its
+    # edges, several a program; rows that the loads take and rows that are packed
+    M, N = 600, 900
+    sched = ts.Schedule(order="auto", mode="auto", tile="256x256x64w8", num_programs=3)
+    n = R.gen(K + pad)
+    qa, sa = quantised(n(M, K))
+    qb, sb = quantised(n(N, K) / K ** 0.5)
+    ad, bd = (torch.full((q.shape[0], K + pad), 448.0).to(Q).cuda()[:, :K].copy_(q.cuda()) for q in (qa, qb))
+    bias, res = n(N).to(out), n(M, N).to(out)
+    z0, zerr0 = R.product(qa.float(), qb.float().t(), None, sa, sb, eight=out != F)
+    z1, zerr1 = R.product(qa.float(), qb.float().t(), bias, sa, sb, eight=out != F)
+    p0, perr0 = R.product(qa.float() * 2.0 ** -9, qb.float().t() * 2.0 ** -9, eight=out != F)
+    cd, cbuf = R.padded(res, "cuda", 3, 1, fill=7.0)
+    pd, pbuf = R.padded(res, "cuda", 3, 1, fill=7.0)
+    sa, sb, bias, rd = sa.cuda(), sb.cuda(), bias.cuda(), res.cuda()
+    for name in R.ACTS:
+        say(K, pad, out, name)
+        ts.gemm_scaled(ad, bd.t(), sa, sb, bias=bias, activation=name, out=cd, schedule=sched)
+        want, bound = R.forward(z1, zerr1, name, None, out)
+        R.check(cd, want, bound, name)
+        pd.zero_()
+        ts.gemm_scaled(ad, bd.t(), sa, sb, bias=bias, activation=name, preact=pd, out=cd, schedule=sched)
+        R.check(cd, want, bound, f"{name} with preact")
+        R.check(pd, z1, zerr1 + R.rounded(z1.abs() + zerr1, out), f"{name} preact")
+        cd.copy_(res)   # in place
+        ts.gemm_scaled(ad, bd.t(), sa, sb, bias=bias, activation=name, residual=cd, out=cd, schedule=sched)
+        want, bound = R.forward(z1, zerr1, name, res, out)
+        R.check(cd, want, bound, f"{name} with residual")
+        pd.zero_()
+        ts.gemm_scaled(ad, bd.t(), sa, sb, activation=name, residual=rd, preact=pd, out=cd, schedule=sched)
+        want, bound = R.forward(z0, zerr0, name, res, out)
+        R.check(cd, want, bound, f"{name} with both")
+        R.check(pd, z0, zerr0 + R.rounded(z0.abs() + zerr0, out), f"{name} preact of both")
+        # the gradient form has no scales; 2^-18 in all keeps its values in fp16
+        pd.copy_(res)
+        ones = torch.full((M,), 2.0 ** -9, device="cuda"), torch.full((N,), 2.0 ** -9, device="cuda")
+        plain = ts.gemm_scaled(ad, bd.t(), *ones, out_dtype=out, schedule=sched)
+        R.check(plain, p0, perr0 + R.rounded(p0.abs() + perr0, out), "powers of two as scales")
+        if out != H:
+            got = ts.gemm_dact(ad, bd.t(), pd, name, out=pd, schedule=sched)   # in place
+            sl, p, perr = R.slope(res.double(), name), p0 * 2.0 ** 18, perr0 * 2.0 ** 18
+            err = 1.2 * perr + R.ACT_ERR * (res.double().abs() + 1) * p.abs()
+            R.check(got, p * sl, err + R.rounded((p * sl).abs() + err, out), f"{name} gradient")
+    for buf, v in ((cbuf, cd), (pbuf, pd)):   # nothing outside the views was written
+        v.fill_(7.0)
+        assert bool((buf == 7.0).all())
+
+
+@pytest.mark.parametrize("tile", ["128x128x64", "256x256x64w8"])
+@pytest.mark.parametrize("out", [H, B, F])
+def test_8_bit_products_in_every_mode(tile, out):
+    # whole tiles a program: the same bits in every mode; K cut in stream-K mode: the bound, the same bits twice
+    M, N, K = 520, 700, 1000
+    n = R.gen(12)
+    qa, sa = quantised(n(M, K))
+    qb, sb = quantised(n(N, K) / K ** 0.5)
+    bias, res = n(N).to(out), n(M, N).to(out)
+    want, bound = R.forward(*R.product(qa.float(), qb.float().t(), bias, sa, sb, eight=out != F), "gelu", res, out)
+    qa, qb, sa, sb, bias, res = (t.cuda() for t in (qa, qb, sa, sb, bias, res))
+
+    def run(**kw):
+        say(tile, out, kw)
+        return ts.gemm_scaled(qa, qb.t(), sa, sb, bias=bias, activation="gelu", residual=res, out_dtype=out,
+                              schedule=ts.Schedule(tile=tile, **kw))
+
+    ref = run()
+    R.check(ref, want, bound, "tiled")
+    for mode, P in (("persistent", 3), ("crosstile", 5), ("auto", 0)):
+        assert torch.equal(ref, run(mode=mode, num_programs=P, order="grouped", group_m=2)), mode
+    for P in (5, 7, 0):
+        x = run(mode="streamk", num_programs=P, order="auto")
+        R.check(x, want, bound, f"stream-K {P}")
+        assert torch.equal(x, run(mode="streamk", num_programs=P, order="auto"))
