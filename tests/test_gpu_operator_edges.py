@@ -1,6 +1,8 @@
 """The operators around the product on the GPU at the edges of what their contract allows: empty
 matrices, values at the ends of the types' ranges, infinities, calls that overlap in time.  Against
 definitions in 64 bits (bounds derived in operator_reference)."""
+import threading
+
 import pytest
 import torch
 
@@ -310,3 +312,101 @@ def test_8_bit_products_in_every_mode(tile, out):
         x = run(mode="streamk", num_programs=P, order="auto")
         R.check(x, want, bound, f"stream-K {P}")
         assert torch.equal(x, run(mode="streamk", num_programs=P, order="auto"))
+
+
+def calls_of_every_kind():
+    """Name -> a call whose outputs are a tuple of tensors: one for each kernel that takes a workspace,
+    and the few-row and norm kernels."""
+    n = R.gen(33)
+
+    def dev(t):
+        return t.cuda()
+
+    a, b = dev(n(200, 77).to(B)), dev((n(333, 77) / 9).to(B)).t()              # packed
+    s1, s2 = dev(n(60, 2048).to(H)), dev((n(2048, 130) / 45).to(H))            # K split
+    x, w = dev(n(5, 1000).to(B)), dev((n(700, 1000) / 31).to(B)).t()           # few rows
+    l1, l2 = dev(n(700, 512).to(B)), dev((n(900, 512) / 22).to(B)).t()         # tiles
+    qa, sa = quantised(n(130, 500))
+    qb, sb = quantised(n(260, 500))
+    qa, sa, qb, sb = dev(qa), dev(sa), dev(qb).t(), dev(sb)
+    h, dy, g = dev(n(300, 1032).to(B)), dev(n(300, 1032).to(B)), dev(n(1032).to(B))
+    z, dc = dev(n(200, 333).to(B)), dev(n(200, 333).to(B))
+    sk = ts.Schedule(mode="streamk", num_programs=7, tile="128x128x64")
+    return {
+        "packed": lambda: (ts.gemm_epilogue(a, b, activation="gelu"),),
+        "split": lambda: (ts.gemm_epilogue(s1, s2, activation="silu", out_dtype=F),),
+        "few rows": lambda: (ts.gemm_epilogue(x, w, activation="relu"),),
+        "tiles": lambda: (ts.gemm_epilogue(l1, l2, activation="gelu_tanh"),),
+        "stream-K": lambda: (ts.gemm_epilogue(l1, l2, activation="gelu", schedule=sk),),
+        "8 bits": lambda: (ts.gemm_scaled(qa, qb, sa, sb, activation="silu"),),
+        "backward": lambda: ts.gemm_epilogue_backward(dc, a, b, preact=z, activation="gelu"),
+        "norm": lambda: tuple(ts.rmsnorm(h, g, residual=dy)[i] for i in (0, 2)),
+        "norm backward": lambda: ts.rmsnorm_backward(dy, h, g, dh=dy),
+    }
+
+
+def same(got, want, what):
+    assert len(got) == len(want)
+    for x, y in zip(got, want):
+        assert torch.equal(x, y), what
+
+
+def test_two_streams_at_the_same_time():
+    # the same calls in opposite orders on two streams that do not wait for one another, and a captured
+    # run of them replayed on a third: each has workspaces of its own
+    calls = calls_of_every_kind()
+    want = {k: f() for k, f in calls.items()}
+    torch.cuda.synchronize()
+    graph, captured = torch.cuda.CUDAGraph(), {}
+    with torch.cuda.graph(graph):
+        for k, f in calls.items():
+            captured[k] = f()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for turn in range(3):
+        for outs in captured.values():
+            for o in outs:
+                o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        got = [[], []]
+        for i in range(4):
+            with torch.cuda.stream(streams[2]):
+                graph.replay()
+            for k1, k2 in zip(calls, reversed(calls)):
+                for s, k in ((0, k1), (1, k2)):
+                    with torch.cuda.stream(streams[s]):
+                        got[s].append((k, calls[k]()))
+        torch.cuda.synchronize()
+        for k, outs in got[0] + got[1] + list(captured.items()):
+            same(outs, want[k], (turn, k))
+
+
+def test_threads():
+    # four threads, each on a stream of its own, the first calls of some of them being the process's first
+    calls = calls_of_every_kind()
+    names = list(calls)
+    torch.cuda.synchronize()
+    got, errors = [[] for _ in range(4)], []
+
+    def work(t):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for i in range(3 * len(names)):
+                    k = names[(i * (t + 1) + t) % len(names)]
+                    got[t].append((k, calls[k]()))
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:   # noqa: BLE001 (reported below, in the test's own thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(t,)) for t in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+        assert not t.is_alive()
+    assert not errors, errors
+    want = {k: f() for k, f in calls.items()}
+    for outs in got:
+        assert len(outs) == 3 * len(names)
+        for k, o in outs:
+            same(o, want[k], k)
