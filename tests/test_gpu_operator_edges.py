@@ -410,3 +410,36 @@ def test_threads():
         assert len(outs) == 3 * len(names)
         for k, o in outs:
             same(o, want[k], k)
+
+
+@pytest.mark.parametrize("N", [40, 512, 4096, 30000, 70000])
+@pytest.mark.parametrize("dtype", [B, F])
+def test_e4m3_is_the_quotient_rounded_once(N, dtype):
+    # rows of +-1 with eps 0 have r = 1, so y is the weight itself: values next to the middle between two
+    # e4m3 numbers times the scale, where a quotient off by one step of fp32 lands on the other side
+    n = R.gen(N)
+    x = torch.where(n(3, N) > 0, 1.0, -1.0).to(dtype)
+    for i in range(8):
+        most = float(n(1).abs() + 0.1) * 10.0 ** (2 * i - 8)
+        scale = torch.tensor(most) / 448
+        steps = torch.arange(0, 255, dtype=torch.uint8).view(Q).float()
+        steps = steps[steps.isfinite() & (steps >= 0)].unique().double()
+        middle = (steps[1:] + steps[:-1]) / 2 * float(scale)
+        pick = torch.randint(0, len(middle), (N,), generator=torch.Generator().manual_seed(i))
+        w = middle[pick].float()
+        w = (w.view(torch.int32) + torch.randint(-2, 3, (N,), generator=torch.Generator().manual_seed(i + 50), dtype=torch.int32)).view(F)
+        w[N // 2] = most
+        q, s, _ = ts.rmsnorm(x.cuda(), w.cuda(), eps=0.0, out_dtype=Q)
+        say(N, dtype, i)
+        assert bool((s.cpu() == w.max() / 448).all())
+        want = (w / s.cpu()[:, None] * x.float()).to(Q).float()   # division and rounding of IEEE 754
+        assert torch.equal(q.float().cpu(), want), int((q.float().cpu() != want).sum())
+
+
+def test_e4m3_of_rows_with_infinite_weights():
+    w = torch.ones(100)
+    w[7] = float("inf")
+    q, s, _ = ts.rmsnorm(torch.ones(4, 100, device="cuda"), w.cuda(), out_dtype=Q)
+    assert bool((s == float("inf")).all())
+    q = q.float()
+    assert bool(q[:, 7].isnan().all()) and bool((q[:, :7] == 0).all()) and bool((q[:, 8:] == 0).all())

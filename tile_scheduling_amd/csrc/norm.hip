@@ -72,6 +72,20 @@ __device__ __forceinline__ float row_scale(uint32_t max_bits) {
     return s < kMinScale ? kMinScale : s;   // NaN stays NaN
 }
 
+// y / scale with one rounding: the product with the reciprocal, off by up to a step and a half of
+// fp32, and one correction by its remainder.  (The product alone puts values next to the middle between
+// two e4m3 numbers on the wrong side.)  An infinite scale has the reciprocal 0 and no remainder, so
+// that finite values become 0.
+struct Quotient {
+    float inv, scale;
+    __device__ __forceinline__ explicit Quotient(float s)
+        : inv(1.0f / s), scale(s > 3.4028234e38f ? 0.0f : s) {}
+    __device__ __forceinline__ float operator()(float v) const {
+        const float q = v * inv;
+        return __builtin_fmaf(__builtin_fmaf(-q, scale, v), inv, q);
+    }
+};
+
 // T threads a row (T <= 256: 256 / T rows a workgroup), up to C groups of eight columns a
 // thread, T * C * 8 >= N.
 template <class TX, bool Q, int T, int C>
@@ -123,14 +137,14 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rmsnorm_kernel(NormArgs g) 
     }
     if constexpr (Q) {
         const float s = row_scale(row_max<T>(most, lds));
-        const float inv = 1.0f / s;
+        const Quotient by(s);
         if (t == 0) g.scale[m] = s;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int n = (c * T + t) * 8, valid = g.N - n;
             if (valid <= 0) continue;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[c][e] *= inv;
+            for (int e = 0; e < 8; ++e) v[c][e] = by(v[c][e]);
             store8_e4m3(static_cast<uint8_t*>(g.y) + m * g.ldy + n, valid, v[c]);
         }
     }
@@ -169,7 +183,7 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(NormArgs g) 
     }
     sum = row_sum<kLongThreads>(sum, lds);
     const float r = 1.0f / __builtin_sqrtf(sum / (float)g.N + g.eps);
-    float inv = 1.0f;
+    Quotient by(1.0f);
     if constexpr (Q) {
         uint32_t most = 0;
         for (long long n = threadIdx.x * 8; n < g.N; n += kLongThreads * 8) {
@@ -182,7 +196,7 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(NormArgs g) 
             most = max8_bits(v, most);
         }
         const float s = row_scale(row_max<kLongThreads>(most, lds));
-        inv = 1.0f / s;
+        by = Quotient(s);
         if (threadIdx.x == 0) g.scale[m] = s;
     }
     for (long long n = threadIdx.x * 8; n < g.N; n += kLongThreads * 8) {
@@ -195,7 +209,7 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(NormArgs g) 
         for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[e];
         if constexpr (Q) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= inv;
+            for (int e = 0; e < 8; ++e) v[e] = by(v[e]);
             store8_e4m3(static_cast<uint8_t*>(g.y) + m * g.ldy + n, valid, v);
         } else {
             store8<TX>(static_cast<X*>(g.y) + m * g.ldy + n, valid, v);
