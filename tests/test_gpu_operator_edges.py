@@ -443,3 +443,23 @@ def test_e4m3_of_rows_with_infinite_weights():
     assert bool((s == float("inf")).all())
     q = q.float()
     assert bool(q[:, 7].isnan().all()) and bool((q[:, :7] == 0).all()) and bool((q[:, 8:] == 0).all())
+
+
+def test_an_error_left_by_another_call_is_not_this_calls():
+    # the caller's own failed HIP call leaves its error behind; the operators report their launches only
+    import ctypes
+
+    hip = ctypes.CDLL(next(line.split()[-1] for line in open("/proc/self/maps") if "libamdhip64" in line))
+    calls = calls_of_every_kind()
+    want = {k: f() for k, f in calls.items()}
+    torch.cuda.synchronize()
+    for k, f in calls.items():
+        f()   # dropped: what the call below allocates is there already (torch would report the error otherwise)
+        torch.cuda.synchronize()
+        assert hip.hipSetDevice(4096) != 0   # no such device: an error, and nothing else
+        try:
+            got = f()
+        finally:
+            left = hip.hipGetLastError()
+        assert left != 0, k                  # still there for the caller to see
+        same(got, want[k], k)

@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "../../include/tsgemm.h"
+#include "plan.hpp"
 #include "rows.hpp"
 
 namespace ts {
@@ -138,13 +139,9 @@ extern "C" ts_status ts_act_grad(const void* dc, const void* preact, void* dz, v
                          groups > 1 ? nullptr : dbias, (int)M, (int)N, activation, (int)group_rows(M, N), bias_dtype,
                          stride_dc, stride_pm, stride_dz};
         void* args[] = {&g};
-        if (hipLaunchKernel(kernel_of(in_dtype, dz ? out_dtype : in_dtype), dim3((unsigned)((N + 255) / 256), (unsigned)groups),
-                            dim3(256), args, 0, hs) != hipSuccess) {
-            (void)hipGetLastError();
-            return TS_ERR_HIP;
-        }
+        if (!enqueue(kernel_of(in_dtype, dz ? out_dtype : in_dtype), (N + 255) / 256, 256, args, hs, groups)) return TS_ERR_HIP;
     }
-    if (dbias && groups != 1 && launch_reduce_columns(static_cast<float*>(workspace), (int)groups, (int)N, dbias, bias_dtype, hs) != hipSuccess)
+    if (dbias && groups != 1 && !launch_reduce_columns(static_cast<float*>(workspace), (int)groups, (int)N, dbias, bias_dtype, hs))
         return TS_ERR_HIP;
     return TS_OK;
 }

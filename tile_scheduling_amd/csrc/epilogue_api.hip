@@ -509,11 +509,7 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
             f.scale_a = epi->scale_a;
             f.scale_b = epi->scale_b;
         }
-        if (launch_few_rows(f, ab_dtype, c_dtype, e.b.kmaj, static_cast<hipStream_t>(stream)) != hipSuccess) {
-            (void)hipGetLastError();
-            return TS_ERR_HIP;
-        }
-        return TS_OK;
+        return launch_few_rows(f, ab_dtype, c_dtype, e.b.kmaj, static_cast<hipStream_t>(stream)) ? TS_OK : TS_ERR_HIP;
     }
 
     auto workspace_ok = [&](int64_t need) {
@@ -538,16 +534,16 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     if (e.sk.total > 0) {
-        const int words = (int)(e.sk.header / 4);
-        hipLaunchKernelGGL(clear_flags_kernel, dim3((words + 255) / 256), dim3(256), 0, hs, reinterpret_cast<int*>(ws),
-                           words);
-        if (hipGetLastError() != hipSuccess) return TS_ERR_HIP;
+        int* flags = reinterpret_cast<int*>(ws);
+        int words = (int)(e.sk.header / 4);
+        void* argv[] = {&flags, &words};
+        if (!enqueue(reinterpret_cast<const void*>(&clear_flags_kernel), (words + 255) / 256, 256, argv, hs)) return TS_ERR_HIP;
     }
-    const PackArgs pk = {{pack_of(e.a, A, e.es, ws + e.off_a), pack_of(e.b, B, e.es, ws + e.off_b)}};
+    PackArgs pk = {{pack_of(e.a, A, e.es, ws + e.off_a), pack_of(e.b, B, e.es, ws + e.off_b)}};
     const int64_t pack_blocks = pk.m[0].blocks + pk.m[1].blocks;
     if (pack_blocks > 0) {
-        hipLaunchKernelGGL(pack_rows_kernel, dim3((unsigned)pack_blocks), dim3(256), 0, hs, pk);
-        if (hipGetLastError() != hipSuccess) return TS_ERR_HIP;
+        void* argv[] = {&pk};
+        if (!enqueue(reinterpret_cast<const void*>(&pack_rows_kernel), pack_blocks, 256, argv, hs)) return TS_ERR_HIP;
     }
 
     // Sizes along K count 16-bit units (pairs of 8-bit elements).
@@ -605,10 +601,8 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
         g.split_stride = (int64_t)e.p.s.nm * e.p.bm * g.ld_sums;
         g.splits = e.splits;
     }
-    if (hipLaunchKernel(epi_kernel_of(e, ab_dtype), dim3(e.p.s.grid), dim3(threads), args, 0, hs) != hipSuccess ||
-        (e.kind == EPI_SPLIT && launch_split_finish(g, c_dtype, hs) != hipSuccess)) {
-        (void)hipGetLastError();
+    if (!enqueue(epi_kernel_of(e, ab_dtype), e.p.s.grid, threads, args, hs) ||
+        (e.kind == EPI_SPLIT && !launch_split_finish(g, c_dtype, hs)))
         return TS_ERR_HIP;
-    }
     return TS_OK;
 }

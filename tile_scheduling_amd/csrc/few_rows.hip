@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "few_rows.hpp"
+#include "plan.hpp"
 #include "schedule.hpp"
 
 namespace ts {
@@ -325,7 +326,7 @@ const void* few_kernel(bool b_kmaj, int mt, int width) {
 
 }  // namespace
 
-hipError_t launch_few_rows(FewArgs& g, int ab, int c, bool b_kmaj, hipStream_t stream) {
+bool launch_few_rows(FewArgs& g, int ab, int c, bool b_kmaj, hipStream_t stream) {
     const int mt = g.M > 16 ? 2 : 1;
     int width, cols;
     if (b_kmaj) {
@@ -342,7 +343,7 @@ hipError_t launch_few_rows(FewArgs& g, int ab, int c, bool b_kmaj, hipStream_t s
     else fn = c == ELT_F32 ? few_kernel<InE4M3, OutF32>(true, mt, width)
               : c == ELT_F16 ? few_kernel<InE4M3, OutF16>(true, mt, width) : few_kernel<InE4M3, OutBF16>(true, mt, width);
     void* args[] = {&g};
-    return hipLaunchKernel(fn, dim3((unsigned)g.tiles), dim3((b_kmaj ? kNtWaves : kNnWaves) * 64), args, 0, stream);
+    return enqueue(fn, g.tiles, (b_kmaj ? kNtWaves : kNnWaves) * 64, args, stream);
 }
 
 }  // namespace ts

@@ -21,7 +21,8 @@ struct FewArgs {
     int tiles, xcds;           // workgroups; XCDs they are dealt over
 };
 
-// Enqueues the kernel for operands of type ab (ELT_*) and C of type c; b_kmaj: B stored [N][K].
-hipError_t launch_few_rows(FewArgs& g, int ab, int c, bool b_kmaj, hipStream_t stream);
+// Enqueues the kernel for operands of type ab (ELT_*) and C of type c; b_kmaj: B stored [N][K].  False
+// if that failed.
+bool launch_few_rows(FewArgs& g, int ab, int c, bool b_kmaj, hipStream_t stream);
 
 }  // namespace ts

@@ -20,6 +20,7 @@
 #include <algorithm>
 
 #include "../../include/tsgemm.h"
+#include "plan.hpp"
 #include "rows.hpp"
 
 namespace ts {
@@ -419,10 +420,9 @@ __global__ void __launch_bounds__(1024) reduce_columns_kernel(const float* part,
         store_any(out, type, n, s);
     }
 }
-hipError_t launch_reduce_columns(const float* part, int rows, int N, void* out, int type, hipStream_t stream) {
-    hipLaunchKernelGGL(reduce_columns_kernel, dim3((unsigned)((N + 15LL) / 16)), dim3(1024), 0, stream, part, rows, N,
-                       out, type);
-    return hipGetLastError();
+bool launch_reduce_columns(const float* part, int rows, int N, void* out, int type, hipStream_t stream) {
+    void* args[] = {&part, &rows, &N, &out, &type};
+    return enqueue(reinterpret_cast<const void*>(&reduce_columns_kernel), (N + 15LL) / 16, 1024, args, stream);
 }
 
 namespace {
@@ -499,11 +499,7 @@ ts_status have_device() {
 
 ts_status launch(const void* fn, int64_t gx, int64_t gy, int threads, void* args, hipStream_t stream) {
     void* argv[] = {args};
-    if (hipLaunchKernel(fn, dim3((unsigned)gx, (unsigned)gy), dim3(threads), argv, 0, stream) != hipSuccess) {
-        (void)hipGetLastError();
-        return TS_ERR_HIP;
-    }
-    return TS_OK;
+    return enqueue(fn, gx, threads, argv, stream, gy) ? TS_OK : TS_ERR_HIP;
 }
 
 // One workgroup for every few rows: a launch holds fewer than 2^32 threads, so many rows take
@@ -626,7 +622,7 @@ extern "C" ts_status ts_rmsnorm_backward(const void* dy, const void* h, const vo
              : dtype == TS_BF16 ? run_norm_grad<OutBF16>(g, groups, hs) : run_norm_grad<OutF32>(g, groups, hs);
         if (st != TS_OK) return st;
     }
-    if (dweight && launch_reduce_columns(static_cast<float*>(workspace), (int)groups, (int)N, dweight, w_dtype, hs) != hipSuccess)
+    if (dweight && !launch_reduce_columns(static_cast<float*>(workspace), (int)groups, (int)N, dweight, w_dtype, hs))
         return TS_ERR_HIP;
     return TS_OK;
 }

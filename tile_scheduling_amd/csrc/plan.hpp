@@ -47,6 +47,15 @@ inline ts_status current_device(int* dev_out, DeviceInfo* info) {
     return TS_OK;
 }
 
+// Enqueues a kernel; false if that failed.  Judged by this launch alone: the runtime's last error may
+// be one that another call of the program left.
+inline bool enqueue(const void* fn, int64_t grid_x, int threads, void** args, hipStream_t stream, int64_t grid_y = 1) {
+    if (hipLaunchKernel(fn, dim3((unsigned)grid_x, (unsigned)grid_y), dim3((unsigned)threads), args, 0, stream) == hipSuccess)
+        return true;
+    (void)hipGetLastError();   // reported by the caller's status
+    return false;
+}
+
 struct Plan {
     bool auto_order;        // TS_ORDER_AUTO: order, G and remap chosen in resolve_grid
     int l2_reuse_pm;        // the locality model's reuse of the resolved order (1/1000)

@@ -98,7 +98,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, float* lds) {
 // fixed order, so the result does not depend on timing.
 __global__ void reduce_columns_kernel(const float* part, int rows, int N, void* out, int type);
 
-// Enqueues reduce_columns_kernel.
-hipError_t launch_reduce_columns(const float* part, int rows, int N, void* out, int type, hipStream_t stream);
+// Enqueues reduce_columns_kernel; false if that failed.
+bool launch_reduce_columns(const float* part, int rows, int N, void* out, int type, hipStream_t stream);
 
 }  // namespace ts

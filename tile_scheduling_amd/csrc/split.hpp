@@ -5,7 +5,7 @@
 
 namespace ts {
 
-// Enqueues the sum over the splits and the epilogue, C of type c (ELT_*).
-hipError_t launch_split_finish(const SplitArgs& g, int c, hipStream_t stream);
+// Enqueues the sum over the splits and the epilogue, C of type c (ELT_*); false if that failed.
+bool launch_split_finish(SplitArgs& g, int c, hipStream_t stream);
 
 }  // namespace ts

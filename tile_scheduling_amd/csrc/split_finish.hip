@@ -4,6 +4,7 @@
 // of 1000 x 512 4.2 us, most of it the launch.
 #include <hip/hip_runtime.h>
 
+#include "plan.hpp"
 #include "rows.hpp"
 #include "split.hpp"
 
@@ -54,13 +55,13 @@ __global__ void __launch_bounds__(256) split_finish_kernel(SplitArgs g) {
     store8<TO>(static_cast<T*>(g.C) + m * g.ldc + n, valid, v);
 }
 
-hipError_t launch_split_finish(const SplitArgs& g, int c, hipStream_t stream) {
+bool launch_split_finish(SplitArgs& g, int c, hipStream_t stream) {
     const long long threads = (long long)g.M * ((g.N + 7) / 8);
-    const dim3 grid((unsigned)((threads + 255) / 256)), block(256);
-    if (c == ELT_F32) hipLaunchKernelGGL(split_finish_kernel<OutF32>, grid, block, 0, stream, g);
-    else if (c == ELT_F16) hipLaunchKernelGGL(split_finish_kernel<OutF16>, grid, block, 0, stream, g);
-    else hipLaunchKernelGGL(split_finish_kernel<OutBF16>, grid, block, 0, stream, g);
-    return hipGetLastError();
+    const void* fn = c == ELT_F32   ? reinterpret_cast<const void*>(&split_finish_kernel<OutF32>)
+                     : c == ELT_F16 ? reinterpret_cast<const void*>(&split_finish_kernel<OutF16>)
+                                    : reinterpret_cast<const void*>(&split_finish_kernel<OutBF16>);
+    void* args[] = {&g};
+    return enqueue(fn, (threads + 255) / 256, 256, args, stream);
 }
 
 }  // namespace ts
