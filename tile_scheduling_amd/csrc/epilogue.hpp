@@ -22,10 +22,7 @@ enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SI
 // Element types (same numbering as TS_F16, TS_BF16, TS_F32, TS_E4M3); 0 = absent.
 enum : int { ELT_NONE = 0, ELT_F16 = 1, ELT_BF16 = 2, ELT_F32 = 3, ELT_E4M3 = 4 };
 
-constexpr float kLog2e = 1.44269504088896340736f;
-
-__device__ __forceinline__ float exp_neg(float x) { return __builtin_amdgcn_exp2f(-kLog2e * x); }   // e^-x
-__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_neg(x)); }
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 // Upper tail of the normal distribution times e^(x^2/2), x >= 0: a degree 8 polynomial
 // without constant term in t = 1 / (1 + 0.305 x), fitted to 0.5 erfcx(x / sqrt 2) by
@@ -54,14 +51,18 @@ constexpr float kInvSqrt2Pi = 0.39894228040143267794f;
 // The activation is one wave-uniform number; silu and gelu_tanh are one function with
 // different coefficients: z sigmoid(z (w0 + w1 z^2)).  Calls f(tag) with the family's tag.
 enum : int { FAM_NONE = 0, FAM_RELU = 1, FAM_ERF = 2, FAM_SIGMOID = 3 };
+// The coefficients carry the -log2(e) of the exponential: 1 / (1 + 2^(z (e0 + e1 z^2))).
 struct Sigmoid {
-    float w0, w1;
+    float e0, e1;
 };
-// From here on the sigmoid of both is 1 in fp32; the argument stops there, as silu's w1 z would be
+// From here on the sigmoid of both is 1 in fp32; the argument stops there, as silu's e1 z would be
 // 0 times infinity at the end of the range.  NaN comes back through the factor z.
 constexpr float kSaturated = 64.0f;
 __device__ __forceinline__ Sigmoid sigmoid_of(int act) {
-    return act == ACT_SILU ? Sigmoid{1.0f, 0.0f} : Sigmoid{kTanhW0, kTanhW1};
+    return act == ACT_SILU ? Sigmoid{-kLog2e, 0.0f} : Sigmoid{-kLog2e * kTanhW0, -kLog2e * kTanhW1};
+}
+__device__ __forceinline__ float sigmoid(float z, Sigmoid c) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * __builtin_fmaf(c.e1 * z, z, c.e0)));
 }
 template <int FAM>
 __device__ __forceinline__ float fam_value(float z, Sigmoid c) {
@@ -70,10 +71,7 @@ __device__ __forceinline__ float fam_value(float z, Sigmoid c) {
         const float q = tail_scaled(__builtin_fabsf(z)) * __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z);
         return z * (z < 0.0f ? q : 1.0f - q);
     }
-    if constexpr (FAM == FAM_SIGMOID) {
-        const float t = __builtin_fminf(z, kSaturated);
-        return z * sigmoid(t * __builtin_fmaf(c.w1 * t, t, c.w0));
-    }
+    if constexpr (FAM == FAM_SIGMOID) return z * sigmoid(__builtin_fminf(z, kSaturated), c);
     return z;
 }
 template <int FAM>
@@ -85,9 +83,9 @@ __device__ __forceinline__ float fam_slope(float z, Sigmoid c) {
         return __builtin_fmaf(z * kInvSqrt2Pi, e, z < 0.0f ? q : 1.0f - q);
     }
     if constexpr (FAM == FAM_SIGMOID) {
-        const float g = sigmoid(z * __builtin_fmaf(c.w1 * z, z, c.w0));
+        const float g = sigmoid(z, c);
         // where z^2 overflows, g (1 - g) is 0: the factor beside it stays finite
-        const float d = __builtin_fminf(__builtin_fmaf(3.0f * c.w1 * z, z, c.w0), 1e30f);
+        const float d = -kLn2 * __builtin_fmaxf(__builtin_fmaf(3.0f * c.e1 * z, z, c.e0), -1e30f);
         return __builtin_fmaf(z * (g * (1.0f - g)), d, g);
     }
     return 1.0f;
