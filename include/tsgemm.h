@@ -427,8 +427,11 @@ typedef struct {
  *   With such a schedule and few tiles, K is split among programs (whole fp32 tiles of sums in
  *   the workspace) and a second kernel adds the parts, in order, and applies the epilogue.
  *   workspace: at least ts_gemm_epilogue_workspace bytes for the same arguments,
- *   256-byte aligned, contents arbitrary (a stream-K launch clears its own flags);
+ *   256-byte aligned, contents arbitrary (a stream-K launch clears its own flags and
+ *   timeout counter, which lie as in ts_gemm_workspace's, and so counts its own waits);
  *   calls that share one must not overlap in time.  NULL where none is needed.
+ *   Stream-K on the 256 tile spills 150 to 270 registers beside this epilogue and is
+ *   slower than the other modes (4096 x 8192 x 2048 gelu 179 us, 138 with a NULL schedule).
  *   The current device must be the stream's.
  *   C and preact lie on no input, except as stated at ts_epilogue, and then with its row stride.
  *   Errors: as ts_gemm; TS_ERR_INVALID_ARG for a bad epilogue.  TS_ERR_UNSUPPORTED: rows

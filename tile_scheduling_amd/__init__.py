@@ -454,7 +454,8 @@ def gemm_epilogue(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = 
     tensor of C's type that receives A @ B + bias, for the backward pass.  A and B may be
     transposed views and have any row stride; ``schedule=None`` chooses order, mode and tile.
     Enqueued on the current stream of A's device.  A 2-D product: batched or 1-D operands
-    are reshaped by the caller.  The gradients: ``gemm_epilogue_backward``.
+    are reshaped by the caller.  The gradients: ``gemm_epilogue_backward`` (autograd does not see
+    the call, as it does not see ``gemm``).
     """
     epi = _Epilogue(_activation(activation))
     return _product(a, b, out, out_dtype or (out.dtype if out is not None else a.dtype), epi, schedule, residual, preact,
@@ -465,7 +466,7 @@ def gemm_dact(a: torch.Tensor, b: torch.Tensor, preact: torch.Tensor, activation
               out: torch.Tensor | None = None, schedule: Schedule | None = None) -> torch.Tensor:
     """C = (A @ B) * act'(preact): the gradient that reaches the input of an activation whose
     output feeds a product, in that product's own backward launch (A the gradient of its
-    output, B its weights transposed).  C has ``preact``'s type."""
+    output, B its weights transposed).  C has ``preact``'s type and may be ``preact``."""
     return _product(a, b, out, preact.dtype, _Epilogue(_activation(activation), 1), schedule, preact=preact)
 
 
@@ -558,7 +559,8 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch
     The tensor given as ``h`` receives it and may be ``residual`` or x (in place).
     y has ``out_dtype``: x's type (default) or torch.float8_e4m3fn, which adds one fp32
     ``scale`` per row, max|y| / 448 (at least 2^-100), with y = e4m3 * scale: the operand and
-    scale_a of ``gemm_scaled``.  Else scale is None.
+    scale_a of ``gemm_scaled``.  Else scale is None.  The gradients: ``rmsnorm_backward``
+    (autograd does not see the call).
     """
     if x.dim() != 2:
         raise ValueError("x must be a matrix of rows")

@@ -97,7 +97,9 @@ namespace {
 constexpr int64_t kOffsetLimit = 1LL << 30;   // in-tile byte offsets of the direct-to-LDS loads
 constexpr int64_t kMaxExtent = INT_MAX - 1024;    // rows and columns of the last tile stay ints
 constexpr int64_t kMaxStride = (1LL << 26) - 1;   // 32-bit lane offsets of the epilogue (16 rows of 4 bytes)
-constexpr int64_t kSplitPrograms = 256, kSplitSteps = 8;   // K split (splits_of): programs at most, K steps each at least
+// K split (splits_of): programs at most, K steps each at least.  256, here, in the choice of the tile
+// and in few_rows.hip: the CUs of a whole MI355X; a workspace's size then needs no device.
+constexpr int64_t kSplitPrograms = 256, kSplitSteps = 8;
 constexpr int kSpin = 1 << 24;                // sleeps before a stream-K wait gives up (about a second)
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }

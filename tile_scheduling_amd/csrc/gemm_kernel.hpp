@@ -335,9 +335,6 @@ struct Engine {
                                PATH == PATH_EDGE_BT || PATH == PATH_EDGE_ATBT;   // B stored [N][K]
     static constexpr bool AT = PATH == PATH_FULL_AT || PATH == PATH_FULL_ATBT ||
                                PATH == PATH_EDGE_AT || PATH == PATH_EDGE_ATBT;   // A stored [K][M]
-    // 8-bit operands: both k-contiguous, so a row of K bytes is a row of K / 2 16-bit
-    // pairs and everything but the product (addresses, slots, fragments) is the 16-bit
-    // engine's.  Sizes along K (g.K, lda, ldb, slices) count pairs.
     // Edge paths of the 8-wave tile: a K step forms the per-lane offset of its first A and
     // first B load, with the out-of-range bit of chunks past K in it, and each further load
     // adds the distance of a load group.  Held per load instead (PATH_EDGE), the eight
@@ -350,6 +347,9 @@ struct Engine {
     // by the 16-bit immediate of one register; only the cost depends on that layout.
     static constexpr int A_BIAS = STEP_OFFS ? Cfg::C_BYTES : 0;
     static constexpr int B_BIAS = STEP_OFFS ? Cfg::C_BYTES + Cfg::A_BYTES : 0;
+    // 8-bit operands: both k-contiguous, so a row of K bytes is a row of K / 2 16-bit
+    // pairs and everything but the product (addresses, slots, fragments) is the 16-bit
+    // engine's.  Sizes along K (g.K, lda, ldb, slices) count pairs.
     static constexpr bool PAIRS = std::is_same<TI, InE4M3>::value;
     static constexpr bool WIDE8 = !std::is_same<TO, OutF32>::value;   // 8-bit products; else widened
     static constexpr bool EDGES = PATH != PATH_FULL;   // C stores masked to M x N
