@@ -6,7 +6,7 @@
 // workspace, the same bits on every run.  The 16 x 16 matrix instructions do the products
 // with the rows of A padded to 16: rows past M (and columns past N) repeat the last one and
 // are not stored.  Every load takes any element alignment, so nothing is packed.  Measured, bf16, B [N][K]:
-// 1 x 4096 x 4096 7.7 us (4.4 TB/s), 1 x 28672 x 4096 46 us (5.1 TB/s); e4m3 4 x 8192 x 8192 14.5 us (4.6 TB/s);
+// 1 x 4096 x 4096 7.7 us (4.4 TB/s), 1 x 28672 x 4096 46 us (5.1 TB/s); e4m3 4 x 8192 x 8192 12.8 us (5.3 TB/s);
 // B [K][N] 13 x 12290 x 1000 8.9 us (2.8 TB/s), 1 x 28672 x 4096 52 us (4.6 TB/s).
 //
 //   B [N][K] (few_nt): a wave reads 128 bytes of 16 rows of B a step, lane group g bytes
