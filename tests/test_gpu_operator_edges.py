@@ -225,6 +225,9 @@ def test_output_on_an_operand_is_refused():
             ts.gemm_epilogue(x, w, out=out)
         with pytest.raises(ValueError, match="operand"):
             ts.gemm_epilogue(x, w.t(), out=out, activation="gelu")
+        with pytest.raises(ValueError, match="operand"):
+            ts.gemm_epilogue(x, w, preact=out, activation="gelu")
+        assert ts.gemm_dact(x, w, out, "relu").shape == (40, 40)   # there it is only read
     assert bool((x == 1).all()) and bool((w == 1).all())
     # nothing to write: an operand of no elements may lie anywhere
     e = torch.empty(0, 40, dtype=B, device="cuda")

@@ -431,6 +431,8 @@ def _product(a, b, out, out_dtype, epi: _Epilogue, schedule, residual=None, prea
     pa, pb, pc = a.data_ptr(), b.data_ptr(), out.data_ptr()
     if (pc == pa or pc == pb) and M and N and K:
         raise ValueError("out must not be an operand of the product")
+    if preact is not None and not epi.grad and epi.preact in (pa, pb) and M and N and K:
+        raise ValueError("preact must not be an operand of the product")
     sam, sak = a.stride()
     sbk, sbn = b.stride()
     scm, scn = out.stride()
