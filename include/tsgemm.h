@@ -46,8 +46,10 @@ typedef enum {
 
 /* element types */
 enum { TS_F16 = 1, TS_BF16 = 2, TS_F32 = 3,
-       TS_E4M3 = 4 };   /* 8-bit float, 4 exponent and 3 mantissa bits, largest value 448
-                           (operands of ts_gemm_epilogue, output of ts_rmsnorm)         */
+       TS_E4M3 = 4,     /* 8-bit float, 4 exponent and 3 mantissa bits, largest value 448
+                           (operands of ts_gemm_epilogue, output of the norms)          */
+       TS_I8 = 5,       /* 8-bit whole numbers (likewise)                               */
+       TS_Q8 = 6 };     /* rows kept in 8 bits, as ts_checkpoint_pack writes them       */
 
 /* tile order: which output tile a linear tile id denotes */
 enum {
@@ -390,15 +392,17 @@ typedef struct {
     int32_t grad;           /* 0: forward; 1: C = z * act'(preact)                        */
     const void* bias;       /* N elements, contiguous, or NULL                            */
     int32_t bias_dtype;     /* TS_F16, TS_BF16 or TS_F32 (read when bias is given)        */
-    int32_t reserved;       /* 0                                                          */
+    int32_t preact_dtype;   /* type of preact: 0 (C's) or TS_Q8                           */
     const void* residual;   /* M x N of C's type, unit column stride, or NULL; may be C   */
     int64_t stride_rm;      /* elements between its rows (ignored when M <= 1)            */
     void* preact;           /* M x N of C's type, unit column stride, or NULL: written
                                when grad is 0 (neither C nor residual), read when it is 1
-                               (may be C)                                                 */
-    int64_t stride_pm;
-    const float* scale_a;   /* e4m3 operands: M fp32, one per row of A; NULL: 1           */
-    const float* scale_b;   /* e4m3 operands: N fp32, one per column of B; NULL: 1        */
+                               (may be C).  TS_Q8: rows as ts_checkpoint_pack writes them,
+                               16-byte aligned; 16-bit operands, A stored [M][K], no
+                               TS_MODE_STREAMK; written from the fp32 z                   */
+    int64_t stride_pm;      /* elements; TS_Q8: bytes, a multiple of 16                   */
+    const float* scale_a;   /* 8-bit operands: M fp32, one per row of A; NULL: 1          */
+    const float* scale_b;   /* 8-bit operands: N fp32, one per column of B; NULL: 1       */
 } ts_epilogue;
 
 /*
@@ -408,10 +412,11 @@ typedef struct {
  *     grad 1:  C = z * act'(preact)    (the gradient of a product that feeds an
  *              activation; no bias, no residual)
  * All of it in fp32 from the fp32 sums (the scales multiply in this order: what overflows on the
- * way is infinite); preact and C are each rounded once, to C's type.  epi == NULL: the plain product.
+ * way is infinite); preact and C are each rounded once, to C's type (preact: or to 8 bits).  TS_I8: the
+ * sums are exact whole numbers, rounded once to fp32.  epi == NULL: the plain product.
  *   ab_dtype / c_dtype: TS_F16 -> TS_F16, TS_F32; TS_BF16 -> TS_BF16, TS_F32;
- *   TS_E4M3 -> TS_F16, TS_BF16, TS_F32.  Layouts and strides of A, B and C as in
- *   ts_gemm; with TS_E4M3 only A stored [M][K] and B stored [N][K] (stride_bk == 1).
+ *   TS_E4M3, TS_I8 -> TS_F16, TS_BF16, TS_F32.  Layouts and strides of A, B and C as in
+ *   ts_gemm; with 8-bit operands only A stored [M][K] and B stored [N][K] (stride_bk == 1).
  *   Any M, N, K and row stride.  An operand whose rows the direct-to-LDS loads cannot
  *   take (stored along K: base, row stride and K multiples of 16 bytes; stored along M
  *   or N: base 4-byte aligned, row stride and row length even) is first copied into
@@ -435,7 +440,8 @@ typedef struct {
  *   The current device must be the stream's.
  *   C and preact lie on no input, except as stated at ts_epilogue, and then with its row stride.
  *   Errors: as ts_gemm; TS_ERR_INVALID_ARG for a bad epilogue.  TS_ERR_UNSUPPORTED: rows
- *   of 2^30 bytes per tile or more (K of 2^21 16-bit elements on the 256 tile), row
+ *   of 2^30 bytes per tile or more (K of 2^21 16-bit elements on the 256 tile), TS_I8 with K
+ *   above 131071 (where an int32 sum could overflow), row
  *   strides of C, residual or preact of 2^26 elements or more.
  */
 ts_status ts_gemm_epilogue(const void* A, const void* B, void* C,
@@ -480,8 +486,8 @@ int64_t ts_act_grad_workspace(int64_t M, int64_t N);
  *     h = x + residual,   y = h / sqrt(mean(h^2) + eps) * weight
  * x, residual, h: M x N of x_dtype (TS_F16, TS_BF16, TS_F32), unit column strides;
  * weight: N contiguous elements of w_dtype (x_dtype or TS_F32) or NULL (1); y: M x N of
- * y_dtype, x_dtype or TS_E4M3.  With TS_E4M3 also one fp32 scale per row, max|y| / 448
- * but at least 2^-100, and y holds y / scale rounded to nearest even: the row operand of
+ * y_dtype, x_dtype, TS_E4M3 or TS_I8.  With these two also one fp32 scale per row, max|y| / 448
+ * or / 127 but at least 2^-100, and y holds y / scale rounded to nearest even: the row operand of
  * ts_gemm_epilogue (A with scale_a).  A row with a NaN in y has a NaN scale; with N == 0
  * every row has the least one.
  * residual and h come together or are both NULL.  All of it in fp32; the norm reads the
@@ -510,6 +516,69 @@ ts_status ts_rmsnorm_backward(const void* dy, const void* h, const void* weight,
                               int64_t stride_dh, int64_t stride_dx, int32_t dtype, int32_t w_dtype, float eps,
                               void* stream, void* workspace, int64_t workspace_bytes);
 int64_t ts_rmsnorm_backward_workspace(int64_t M, int64_t N);
+
+/*
+ * Layer norm of rows, with the residual's addition in front of it:
+ *     h = x + residual,   y = (h - mean(h)) / sqrt(var(h) + eps) * weight + bias
+ * var(h) = mean((h - mean(h))^2).  As ts_rmsnorm, and: weight and bias are N contiguous elements
+ * of w_dtype or NULL (1 and 0); kept (or NULL) receives h in 8 bits, as ts_checkpoint_pack writes
+ * it but from the unrounded sum, stride_kept bytes a row.  kept lies on no other operand.
+ * TS_ERR_UNSUPPORTED (here and for everything below): N of 2^26 or more, M of 2^30 or more.
+ */
+ts_status ts_layernorm(const void* x, const void* residual, const void* weight, const void* bias, void* y, void* h,
+                       float* scale, void* kept, int64_t M, int64_t N, int64_t stride_x, int64_t stride_r,
+                       int64_t stride_y, int64_t stride_h, int64_t stride_kept, int32_t x_dtype, int32_t w_dtype,
+                       int32_t y_dtype, float eps, void* stream);
+
+/*
+ * Its gradients, with u = (h - mean(h)) r, r = 1 / sqrt(var(h) + eps), g = weight dy:
+ *     dx = r (g - mean(g) - u mean(g u)) + dh      (x's and the residual's alike)
+ *     dweight[n] = sum over m of dy u,   dbias[n] = sum over m of dy
+ * As ts_rmsnorm_backward; h: M x N of h_dtype, dtype or TS_Q8 (stride_h then in bytes).  dweight and
+ * dbias: w_dtype, either may be NULL.  workspace (with one of them, and for rows of more than 16384): at
+ * least ts_layernorm_backward_workspace(M, N) bytes, 256-byte aligned, contents arbitrary, not
+ * shared by calls that overlap in time.  TS_ERR_UNSUPPORTED here: N of 2^25 or more.
+ */
+ts_status ts_layernorm_backward(const void* dy, const void* h, const void* weight, const void* dh, void* dx,
+                                void* dweight, void* dbias, int64_t M, int64_t N, int64_t stride_dy, int64_t stride_h,
+                                int64_t stride_dh, int64_t stride_dx, int32_t dtype, int32_t h_dtype, int32_t w_dtype,
+                                float eps, void* stream, void* workspace, int64_t workspace_bytes);
+int64_t ts_layernorm_backward_workspace(int64_t M, int64_t N);
+
+/*
+ * Rows of x (M x N of TS_F16, TS_BF16 or TS_F32) in 8 bits, y_dtype TS_E4M3 or TS_I8, with one
+ * fp32 scale per row, as the norms write them: the row operand of ts_gemm_epilogue where no norm
+ * stands before the product.
+ */
+ts_status ts_quantize_rows(const void* x, void* y, float* scale, int64_t M, int64_t N, int64_t stride_x,
+                           int64_t stride_y, int32_t x_dtype, int32_t y_dtype, void* stream);
+
+/*
+ * Rows kept in 8 bits (TS_Q8), what a forward pass keeps for its backward pass.  32 neighbours of
+ * a row share a step 2^e, e the least for which the largest of them is at most 127 steps (-126 at
+ * least); a value is round(x / 2^e), ties to even.  A row of N columns: 32 ceil(N / 32) int8 values,
+ * zero behind column N, then one byte e + 127 for each 32, or 255 where they hold an infinity or
+ * a NaN: all of them then stand for NaN.  Rows are stride_kept bytes apart, a multiple of 16 and
+ * at least ts_checkpoint_row_bytes(N), and 16-byte aligned; what lies behind a row's last exponent
+ * is neither read nor written.
+ */
+int64_t ts_checkpoint_row_bytes(int64_t N);
+ts_status ts_checkpoint_pack(const void* x, void* kept, int64_t M, int64_t N, int64_t stride_x, int64_t stride_kept,
+                             int32_t x_dtype, void* stream);
+/* y = act(value), y of y_dtype. */
+ts_status ts_checkpoint_unpack(const void* kept, void* y, int64_t M, int64_t N, int64_t stride_kept, int64_t stride_y,
+                               int32_t y_dtype, int32_t activation, void* stream);
+
+/*
+ * ts_act_grad with preact of in_dtype or in 8 bits (preact_dtype TS_Q8, stride_pm in bytes), and a
+ * further output, value = act(preact), M x N of out_dtype or NULL: the operand of the next weight's
+ * gradient.  dZ, value and dbias may each be NULL; preact is read unless activation is TS_ACT_NONE
+ * and value NULL.  value may take dC's or a preact of in_dtype's place, as dZ may.
+ */
+ts_status ts_act_grad_value(const void* dC, const void* preact, void* dZ, void* value, void* dbias, int64_t M, int64_t N,
+                            int64_t stride_dc, int64_t stride_pm, int64_t stride_dz, int64_t stride_v, int32_t in_dtype,
+                            int32_t preact_dtype, int32_t out_dtype, int32_t bias_dtype, int32_t activation,
+                            void* stream, void* workspace, int64_t workspace_bytes);
 
 /* Static, human-readable name of a status code.  This library's own addition
    (the pages define no error reporting). */

@@ -29,7 +29,7 @@ _i32, _i64, _p = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 
 # status codes, element types and schedule enums (include/tsgemm.h)
 TS_OK, TS_ERR_INVALID_ARG, TS_ERR_UNSUPPORTED, TS_ERR_ALIGNMENT, TS_ERR_HIP, TS_ERR_NO_DEVICE = 0, -1, -2, -3, -4, -5
-TS_F16, TS_BF16, TS_F32, TS_E4M3 = 1, 2, 3, 4
+TS_F16, TS_BF16, TS_F32, TS_E4M3, TS_I8, TS_Q8 = 1, 2, 3, 4, 5, 6
 FEW_ROWS = 32   # products of up to this many rows mostly need no workspace (ts_gemm_epilogue)
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 ORDERS = {"row_major": 0, "grouped": 1, "auto": 2}
@@ -82,7 +82,7 @@ _lib.ts_query.restype = _i32
 
 
 class _Epilogue(ctypes.Structure):
-    _fields_ = [("activation", _i32), ("grad", _i32), ("bias", _p), ("bias_dtype", _i32), ("reserved", _i32),
+    _fields_ = [("activation", _i32), ("grad", _i32), ("bias", _p), ("bias_dtype", _i32), ("preact_dtype", _i32),
                 ("residual", _p), ("stride_rm", _i64), ("preact", _p), ("stride_pm", _i64),
                 ("scale_a", _p), ("scale_b", _p)]
 
@@ -102,13 +102,31 @@ _lib.ts_act_grad.argtypes = [_p] * 4 + [_i64] * 5 + [_i32] * 4 + [_p, _p, _i64]
 _lib.ts_act_grad.restype = _i32
 _lib.ts_act_grad_workspace.argtypes = [_i64, _i64]
 _lib.ts_act_grad_workspace.restype = _i64
+_lib.ts_act_grad_value.argtypes = [_p] * 5 + [_i64] * 6 + [_i32] * 5 + [_p, _p, _i64]
+_lib.ts_act_grad_value.restype = _i32
+_lib.ts_layernorm.argtypes = [_p] * 8 + [_i64] * 7 + [_i32] * 3 + [ctypes.c_float, _p]
+_lib.ts_layernorm.restype = _i32
+_lib.ts_layernorm_backward.argtypes = [_p] * 7 + [_i64] * 6 + [_i32] * 3 + [ctypes.c_float, _p, _p, _i64]
+_lib.ts_layernorm_backward.restype = _i32
+_lib.ts_layernorm_backward_workspace.argtypes = [_i64, _i64]
+_lib.ts_layernorm_backward_workspace.restype = _i64
+_lib.ts_quantize_rows.argtypes = [_p] * 3 + [_i64] * 4 + [_i32] * 2 + [_p]
+_lib.ts_quantize_rows.restype = _i32
+_lib.ts_checkpoint_row_bytes.argtypes = [_i64]
+_lib.ts_checkpoint_row_bytes.restype = _i64
+_lib.ts_checkpoint_pack.argtypes = [_p] * 2 + [_i64] * 4 + [_i32, _p]
+_lib.ts_checkpoint_pack.restype = _i32
+_lib.ts_checkpoint_unpack.argtypes = [_p] * 2 + [_i64] * 4 + [_i32] * 2 + [_p]
+_lib.ts_checkpoint_unpack.restype = _i32
 _lib.ts_status_string.argtypes = [_i32]
 _lib.ts_status_string.restype = ctypes.c_char_p
 
 EXPORTS = ("ts_gemm", "ts_gemm_workspace", "ts_gemm_noalloc", "ts_noalloc_scratch_bytes", "ts_gemm_clocked", "ts_schedule_trace", "ts_schedule_trace_host", "ts_query",
            "ts_status_string", "ts_mfma_loop_probe", "ts_mfma_phase_probe", "ts_gemm_epilogue",
            "ts_gemm_epilogue_workspace", "ts_rmsnorm", "ts_rmsnorm_backward", "ts_rmsnorm_backward_workspace",
-           "ts_act_grad", "ts_act_grad_workspace")
+           "ts_act_grad", "ts_act_grad_workspace", "ts_act_grad_value", "ts_layernorm", "ts_layernorm_backward",
+           "ts_layernorm_backward_workspace", "ts_quantize_rows", "ts_checkpoint_row_bytes", "ts_checkpoint_pack",
+           "ts_checkpoint_unpack")
 
 
 class TsError(RuntimeError):
@@ -335,7 +353,7 @@ def schedule_trace_host(M: int, N: int, K: int, schedule: Schedule, cu_count: in
 
 # ---- operators around the product ------------------------------------------------------
 
-_DTYPE = {**_TORCH_DTYPE, torch.float8_e4m3fn: TS_E4M3}
+_DTYPE = {**_TORCH_DTYPE, torch.float8_e4m3fn: TS_E4M3, torch.int8: TS_I8}
 
 
 # Calls of a few microseconds of GPU time are bound by what surrounds them on the host, so the
@@ -394,6 +412,49 @@ def _vector(t: torch.Tensor, n: int, what: str, dtype=None) -> None:
         raise ValueError(f"{what} is {t.dtype}")
 
 
+class Checkpoint:
+    """Rows kept in 8 bits for a backward pass: an [M, N] matrix in ``data``, a uint8 [M, pitch] CUDA
+    tensor of unit column stride (16-byte aligned, row stride a multiple of 16).
+
+    32 neighbours of a row share one step 2^e, the least for which the largest of them is at most
+    127 steps; a value is a whole number of steps (int8), off by at most half a step.  A row of ``data``:
+    32 ceil(N / 32) values, then a byte e + 127 for each 32; 255: they held an infinity or a NaN, and
+    all of them stand for NaN.  ``checkpoint_pack``, ``layernorm`` and the product (``preact``) write
+    it; ``checkpoint_unpack``, ``act_grad``, ``gemm_dact``, the products' and the norms' gradients read it.
+    Its rows are ``data``'s: a slice of those is a checkpoint of the same rows.
+    """
+
+    __slots__ = ("data", "n")
+
+    def __init__(self, data: torch.Tensor, n: int):
+        self.data, self.n = data, int(n)
+        if data.dim() != 2 or data.dtype != torch.uint8:
+            raise ValueError("a checkpoint's data is a uint8 matrix")
+        if n < 0 or data.shape[1] < 33 * -(-self.n // 32):
+            raise ValueError(f"rows of {data.shape[1]} bytes do not hold {n} columns")
+        row, col = data.stride()
+        if (col != 1 and data.shape[1] > 1) or (row % 16 and data.shape[0] > 1) or data.data_ptr() % 16:
+            raise ValueError("a checkpoint's rows are contiguous and 16-byte aligned")
+
+    @classmethod
+    def empty(cls, m: int, n: int, device=None) -> "Checkpoint":
+        """Room for an [m, n] matrix (rows of whole 64-byte lines)."""
+        return cls(torch.empty((m, -(-33 * -(-n // 32) // 64) * 64), dtype=torch.uint8, device=device or "cuda"), n)
+
+    @property
+    def shape(self):
+        return torch.Size((self.data.shape[0], self.n))
+
+    @property
+    def device(self):
+        return self.data.device
+
+    def _rows(self, shape, what: str) -> int:
+        if self.shape != shape:
+            raise ValueError(f"{what} has shape {tuple(self.shape)}, expected {tuple(shape)}")
+        return self.data.stride(0)
+
+
 def _activation(name) -> int:
     if name not in ACTIVATIONS:
         raise ValueError(f"activation {name!r}: one of {', '.join(ACTIVATIONS)}")
@@ -406,7 +467,8 @@ def _product(a, b, out, out_dtype, epi: _Epilogue, schedule, residual=None, prea
         raise ValueError(f"shapes {tuple(a.shape)} @ {tuple(b.shape)} do not multiply")
     if a.dtype != b.dtype:
         raise ValueError(f"A is {a.dtype}, B is {b.dtype}")
-    dev = _device_of(a, b, out, bias, residual, preact, scale_a, scale_b)
+    kept = type(preact) is Checkpoint
+    dev = _device_of(a, b, out, bias, residual, preact.data if kept else preact, scale_a, scale_b)
     (M, K), N = a.shape, b.shape[1]
     shape = (M, N)
     if out is None:
@@ -415,7 +477,9 @@ def _product(a, b, out, out_dtype, epi: _Epilogue, schedule, residual=None, prea
         raise ValueError("out has the wrong shape or type")
     if residual is not None:
         epi.residual, epi.stride_rm = residual.data_ptr(), _rows(residual, shape, "residual", out_dtype)
-    if preact is not None:
+    if kept:
+        epi.preact, epi.stride_pm, epi.preact_dtype = preact.data.data_ptr(), preact._rows(shape, "preact"), TS_Q8
+    elif preact is not None:
         epi.preact, epi.stride_pm = preact.data_ptr(), _rows(preact, shape, "preact", out_dtype)
     if bias is not None:
         _vector(bias, N, "bias")
@@ -446,14 +510,15 @@ def _product(a, b, out, out_dtype, epi: _Epilogue, schedule, residual=None, prea
 
 
 def gemm_epilogue(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = None, activation: str = "none",
-                  residual: torch.Tensor | None = None, preact: torch.Tensor | None = None,
+                  residual: torch.Tensor | None = None, preact: torch.Tensor | Checkpoint | None = None,
                   out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
                   schedule: Schedule | None = None) -> torch.Tensor:
     """C = act(A @ B + bias) + residual, A [M,K] and B [K,N] fp16/bf16; C fp16/bf16/fp32.
 
     ``activation``: "none", "relu", "gelu" (exact), "gelu_tanh" or "silu".  ``bias``: [N],
     fp16/bf16/fp32.  ``residual``: [M,N] of C's type (may be ``out``).  ``preact``: an [M,N]
-    tensor of C's type that receives A @ B + bias, for the backward pass.  A and B may be
+    tensor of C's type that receives A @ B + bias, for the backward pass, or a ``Checkpoint``
+    that receives it in 8 bits (A's rows contiguous, no stream-K).  A and B may be
     transposed views and have any row stride; ``schedule=None`` chooses order, mode and tile.
     Enqueued on the current stream of A's device.  A 2-D product: batched or 1-D operands
     are reshaped by the caller.  The gradients: ``gemm_epilogue_backward`` (autograd does not see
@@ -464,12 +529,15 @@ def gemm_epilogue(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = 
                     bias)
 
 
-def gemm_dact(a: torch.Tensor, b: torch.Tensor, preact: torch.Tensor, activation: str,
+def gemm_dact(a: torch.Tensor, b: torch.Tensor, preact: torch.Tensor | Checkpoint, activation: str,
               out: torch.Tensor | None = None, schedule: Schedule | None = None) -> torch.Tensor:
     """C = (A @ B) * act'(preact): the gradient that reaches the input of an activation whose
     output feeds a product, in that product's own backward launch (A the gradient of its
-    output, B its weights transposed).  C has ``preact``'s type and may be ``preact``."""
-    return _product(a, b, out, preact.dtype, _Epilogue(_activation(activation), 1), schedule, preact=preact)
+    output, B its weights transposed).  C has ``preact``'s type and may be ``preact``; with a
+    ``Checkpoint`` it has A's type (or ``out``'s)."""
+    kept = type(preact) is Checkpoint
+    dtype = preact.dtype if not kept else out.dtype if out is not None else a.dtype
+    return _product(a, b, out, dtype, _Epilogue(_activation(activation), 1), schedule, preact=preact)
 
 
 def gemm_scaled(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor | None = None,
@@ -477,59 +545,74 @@ def gemm_scaled(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor | None =
                 residual: torch.Tensor | None = None, preact: torch.Tensor | None = None,
                 out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
                 schedule: Schedule | None = None) -> torch.Tensor:
-    """C = act(((A @ B) * scale_a[:, None]) * scale_b[None, :] + bias) + residual with e4m3 A
+    """C = act(((A @ B) * scale_a[:, None]) * scale_b[None, :] + bias) + residual with e4m3 or int8 A
     [M,K] (rows contiguous) and B [K,N] stored [N][K] (a transposed view of [N,K] weights).
 
-    ``scale_a`` [M] and ``scale_b`` [N] are fp32 (None: 1); an element's value is
-    e4m3 * scale, as ``rmsnorm(..., out_dtype=torch.float8_e4m3fn)`` returns them.  C is
-    fp16, bf16 (default) or fp32.  Otherwise as ``gemm_epilogue``.
+    ``scale_a`` [M] (tokens) and ``scale_b`` [N] (channels) are fp32 (None: 1); an element's value is
+    code * scale, as the norms and ``quantize_rows`` return them.  int8: the sums are exact (K up to
+    131071) and rounded once, to fp32.  C is fp16, bf16 (default) or fp32.  Otherwise as
+    ``gemm_epilogue`` (``preact``: a tensor).
     """
-    if a.dtype != torch.float8_e4m3fn:
-        raise ValueError(f"A is {a.dtype}, expected torch.float8_e4m3fn")
+    if a.dtype != torch.float8_e4m3fn and a.dtype != torch.int8:
+        raise ValueError(f"A is {a.dtype}, expected torch.float8_e4m3fn or torch.int8")
     epi = _Epilogue(_activation(activation))
     return _product(a, b, out, out_dtype or (out.dtype if out is not None else torch.bfloat16), epi, schedule, residual,
                     preact, bias, scale_a, scale_b)
 
 
-def act_grad(dc: torch.Tensor, preact: torch.Tensor | None = None, activation: str = "none",
+def act_grad(dc: torch.Tensor, preact: torch.Tensor | Checkpoint | None = None, activation: str = "none",
              out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, dbias: bool = True,
-             dbias_dtype: torch.dtype = torch.float32):
+             dbias_dtype: torch.dtype = torch.float32, act_out: torch.Tensor | None = None):
     """dZ = dC * act'(preact) and the bias gradient, its column sums; returns (dZ, dbias).
 
-    dC and ``preact`` are [M,N] of one type (fp16, bf16, fp32).  dZ: ``out`` or a new tensor
-    of ``out_dtype`` (dC's type; fp16 or bf16 from fp32).  dbias sums the unrounded fp32
-    products in a fixed order (the same bits on every run); None if ``dbias`` is False.
-    With activation "none", ``preact`` is not read, and dZ is dC itself (not a copy) unless
-    ``out`` or ``out_dtype`` asks for one.
+    dC and ``preact`` are [M,N] of one type (fp16, bf16, fp32), or ``preact`` is a ``Checkpoint``.  dZ:
+    ``out`` or a new tensor of ``out_dtype`` (dC's type; fp16 or bf16 from fp32).  dbias sums the
+    unrounded fp32 products in a fixed order (the same bits on every run); None if ``dbias`` is False.
+    ``act_out``: an [M,N] tensor of dZ's type that receives act(preact), the operand of the next weight's
+    gradient, which the forward pass then need not keep.
+    With activation "none", ``preact`` is read for ``act_out`` only, and dZ is dC itself (not a copy)
+    unless ``out`` or ``out_dtype`` asks for one.
     """
     act = _activation(activation)
     if dc.dim() != 2:
         raise ValueError("dC must be a matrix")
     M, N = shape = dc.shape
-    if act and preact is None:
+    reads = act or act_out is not None
+    if reads and preact is None:
         raise ValueError("preact is needed for this activation")
-    if not act:
+    if not reads:
         preact = None
+    kept = type(preact) is Checkpoint
     ldc = _rows(dc, shape, "dC")
-    ldz = _rows(preact, shape, "preact", dc.dtype) if preact is not None else N
+    ldz = preact._rows(shape, "preact") if kept else _rows(preact, shape, "preact", dc.dtype) if preact is not None else N
     if out is None and (act or out_dtype not in (None, dc.dtype)):
         out = torch.empty(shape, dtype=out_dtype or dc.dtype, device=dc.device)
-    dev = _device_of(dc, preact, out)
+    z = preact.data if kept else preact
+    dev = _device_of(dc, z, out, act_out)
     ldo = _rows(out, shape, "out", out_dtype) if out is not None else N
     db = torch.empty(N, dtype=dbias_dtype, device=dc.device) if dbias else None
-    if out is None and db is None:
+    if out is None and db is None and act_out is None:
         return dc, None
     need = _lib.ts_act_grad_workspace(M, N) if dbias else 0
     ws = _scratch(need, dc)
     in_t = _DTYPE.get(dc.dtype, 0)
-    _launch(dev, _lib.ts_act_grad, dc.data_ptr(), preact.data_ptr() if preact is not None else None,
-            out.data_ptr() if out is not None else None, db.data_ptr() if dbias else None, M, N, ldc, ldz, ldo, in_t,
-            _DTYPE.get(out.dtype, 0) if out is not None else in_t, _DTYPE.get(dbias_dtype, 0), act, _raw_stream(dev),
-            ws.data_ptr() if need else None, need)
+    out_t = _DTYPE.get(out.dtype, 0) if out is not None else _DTYPE.get(act_out.dtype, 0) if act_out is not None else in_t
+    pz, po = z.data_ptr() if z is not None else None, out.data_ptr() if out is not None else None
+    pd, pw = db.data_ptr() if dbias else None, ws.data_ptr() if need else None
+    if kept or act_out is not None:
+        pv, ldv = None, N
+        if act_out is not None:
+            pv, ldv = act_out.data_ptr(), _rows(act_out, shape, "act_out", out.dtype if out is not None else None)
+        _launch(dev, _lib.ts_act_grad_value, dc.data_ptr(), pz, po, pv, pd, M, N, ldc, ldz, ldo, ldv, in_t,
+                TS_Q8 if kept else in_t, out_t, _DTYPE.get(dbias_dtype, 0), act, _raw_stream(dev), pw, need)
+    else:
+        _launch(dev, _lib.ts_act_grad, dc.data_ptr(), pz, po, pd, M, N, ldc, ldz, ldo, in_t, out_t,
+                _DTYPE.get(dbias_dtype, 0), act, _raw_stream(dev), pw, need)
     return (out if out is not None else dc), db
 
 
-def gemm_epilogue_backward(dc: torch.Tensor, a: torch.Tensor, b: torch.Tensor, preact: torch.Tensor | None = None,
+def gemm_epilogue_backward(dc: torch.Tensor, a: torch.Tensor | Checkpoint, b: torch.Tensor,
+                           preact: torch.Tensor | Checkpoint | None = None,
                            activation: str = "none", dbias: bool = True,
                            dbias_dtype: torch.dtype = torch.float32, schedule: Schedule | None = None):
     """Gradients of C = act(A @ B + bias) + residual given dC: returns (dA, dB, dbias).
@@ -537,8 +620,11 @@ def gemm_epilogue_backward(dc: torch.Tensor, a: torch.Tensor, b: torch.Tensor, p
     dZ = dC * act'(preact) is formed once, rounded to A's type (an operand of the two
     products that follow); dA = dZ @ B^T and dB = A^T @ dZ have A's and B's type, dbias
     (None if not asked for) sums the unrounded dZ.  The residual's gradient is dC itself.
-    ``preact`` is what the forward call stored, of dC's type; not needed for "none".
+    ``preact`` is what the forward call stored, of dC's type or in 8 bits; not needed for "none".  A
+    kept in 8 bits is read back in B's type first (one pass).
     """
+    if type(a) is Checkpoint:
+        a = checkpoint_unpack(a, out_dtype=b.dtype)
     if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[0] or tuple(dc.shape) != (a.shape[0], b.shape[1]):
         raise ValueError(f"dC {tuple(dc.shape)} is not the gradient of {tuple(a.shape)} @ {tuple(b.shape)}")
     if a.dtype not in (torch.float16, torch.bfloat16) or b.dtype != a.dtype:
@@ -559,8 +645,8 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch
     fp32 (None: 1).  The norm reads the unrounded fp32 sum; h (x itself without a residual)
     is its rounding to x's type, what the next block adds to and ``rmsnorm_backward`` takes.
     The tensor given as ``h`` receives it and may be ``residual`` or x (in place).
-    y has ``out_dtype``: x's type (default) or torch.float8_e4m3fn, which adds one fp32
-    ``scale`` per row, max|y| / 448 (at least 2^-100), with y = e4m3 * scale: the operand and
+    y has ``out_dtype``: x's type (default), torch.float8_e4m3fn or torch.int8, which add one fp32
+    ``scale`` per row, max|y| / 448 or / 127 (at least 2^-100), with y = code * scale: the operand and
     scale_a of ``gemm_scaled``.  Else scale is None.  The gradients: ``rmsnorm_backward``
     (autograd does not see the call).
     """
@@ -587,7 +673,7 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch
     if weight is not None:
         _vector(weight, N, "weight")
         pw, w_t = weight.data_ptr(), _TORCH_DTYPE[weight.dtype]
-    if out_dtype == torch.float8_e4m3fn:
+    if out_dtype == torch.float8_e4m3fn or out_dtype == torch.int8:
         scale = torch.empty(M, dtype=torch.float32, device=x.device)
         ps = scale.data_ptr()
     _launch(dev, _lib.ts_rmsnorm, x.data_ptr(), pr, pw, out.data_ptr(), ph, ps, M, N, ldx, ldr, ldy, ldh,
@@ -595,16 +681,19 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch
     return out, scale, (h if h is not None else x)
 
 
-def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,
+def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor | Checkpoint, weight: torch.Tensor | None = None, eps: float = 1e-6,
                      dh: torch.Tensor | None = None, dweight: bool = True, out: torch.Tensor | None = None):
     """Gradients of y = h / sqrt(mean(h^2) + eps) * weight given dy; returns (dx, dweight).
 
     dx = dL/dh + ``dh``, where ``dh`` is the gradient that reaches h along the residual
     stream (None: 0): the gradient of x and of the residual alike.  dy, h and dh are [M,N]
     of one type, dx has it too (``out`` may be dy or dh).  dweight has weight's type, summed
-    in fp32 in a fixed order; None without a weight or if ``dweight`` is False.  The e4m3
-    output of the forward pass is differentiated as y itself (straight through).
+    in fp32 in a fixed order; None without a weight or if ``dweight`` is False.  The 8-bit
+    output of the forward pass is differentiated as y itself (straight through).  h kept in 8 bits
+    is read back in dy's type first (one pass).
     """
+    if type(h) is Checkpoint:
+        h = checkpoint_unpack(h, out_dtype=dy.dtype)
     if dy.dim() != 2:
         raise ValueError("dy must be a matrix of rows")
     M, N = shape = dy.shape
@@ -627,3 +716,145 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | N
             ldy, ldh, lds, ldx, _TORCH_DTYPE.get(dtype, 0), w_t, eps, _raw_stream(dev),
             ws.data_ptr() if need else None, need)
     return out, dw
+
+
+def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+              residual: torch.Tensor | None = None, eps: float = 1e-5, out_dtype: torch.dtype | None = None,
+              out: torch.Tensor | None = None, h: torch.Tensor | None = None, keep: Checkpoint | None = None):
+    """h = x + residual;  y = (h - mean(h)) / sqrt(var(h) + eps) * weight + bias, row by row; returns
+    (y, scale, h).
+
+    As ``rmsnorm``: x [M,N] fp16, bf16 or fp32, ``residual`` of its type, h its rounding; ``weight`` (None:
+    1) and ``bias`` (None: 0) [N], of one type, x's or fp32; y in x's type, or torch.float8_e4m3fn or
+    torch.int8 with one fp32 ``scale`` per row.  The variance is the mean square of the differences from
+    the mean.  ``keep``: receives h in 8 bits, what ``layernorm_backward`` takes in place of h.
+    The gradients: ``layernorm_backward`` (autograd does not see the call).
+    """
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix of rows")
+    if h is not None and residual is None:
+        raise ValueError("h is written only with a residual")
+    M, N = shape = x.shape
+    dtype = x.dtype
+    out_dtype = out_dtype or (out.dtype if out is not None else dtype)
+    if out is None:
+        out = torch.empty_like(x) if out_dtype == dtype else torch.empty(shape, dtype=out_dtype, device=x.device)
+    if residual is not None and h is None:
+        h = torch.empty_like(x)
+    dev = _device_of(x, weight, bias, residual, out, h, keep.data if keep is not None else None)
+    ldx = _rows(x, shape, "x")
+    ldy = _rows(out, shape, "out", out_dtype)
+    ldr = ldh = ldk = N
+    pr = ph = pw = pb = ps = pk = scale = None
+    if residual is not None:
+        ldr, ldh = _rows(residual, shape, "residual", dtype), _rows(h, shape, "h", dtype)
+        pr, ph = residual.data_ptr(), h.data_ptr()
+    w_t = TS_F32
+    if weight is not None:
+        _vector(weight, N, "weight")
+        pw, w_t = weight.data_ptr(), _TORCH_DTYPE[weight.dtype]
+    if bias is not None:
+        _vector(bias, N, "bias", weight.dtype if weight is not None else None)
+        pb, w_t = bias.data_ptr(), _TORCH_DTYPE[bias.dtype]
+    if out_dtype == torch.float8_e4m3fn or out_dtype == torch.int8:
+        scale = torch.empty(M, dtype=torch.float32, device=x.device)
+        ps = scale.data_ptr()
+    if keep is not None:
+        pk, ldk = keep.data.data_ptr(), keep._rows(shape, "keep")
+    _launch(dev, _lib.ts_layernorm, x.data_ptr(), pr, pw, pb, out.data_ptr(), ph, ps, pk, M, N, ldx, ldr, ldy, ldh, ldk,
+            _TORCH_DTYPE.get(dtype, 0), w_t, _DTYPE.get(out_dtype, 0), eps, _raw_stream(dev))
+    return out, scale, (h if h is not None else x)
+
+
+def layernorm_backward(dy: torch.Tensor, h: torch.Tensor | Checkpoint, weight: torch.Tensor | None = None,
+                       eps: float = 1e-5, dh: torch.Tensor | None = None, dweight: bool = True, dbias: bool = True,
+                       dbias_dtype: torch.dtype | None = None, out: torch.Tensor | None = None):
+    """Gradients of ``layernorm`` given dy; returns (dx, dweight, dbias).
+
+    dx = dL/dh + ``dh`` (the gradient that reaches h along the residual stream, None: 0).  dy and dh are
+    [M,N] of one type, h of the same or a ``Checkpoint``; dx has dy's type (``out`` may be dy or dh).
+    dweight and dbias, the column sums of dy (h - mean) / deviation and of dy, have weight's type, without a
+    weight ``dbias_dtype`` (fp32) and dweight is None; summed in fp32 in a fixed order.  The 8-bit output
+    of the forward pass is differentiated as y itself (straight through).
+    """
+    if dy.dim() != 2:
+        raise ValueError("dy must be a matrix of rows")
+    M, N = shape = dy.shape
+    dtype = dy.dtype
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dy.device)
+    kept = type(h) is Checkpoint
+    hd = h.data if kept else h
+    dev = _device_of(dy, hd, weight, dh, out)
+    ldy, ldx = _rows(dy, shape, "dy"), _rows(out, shape, "out", dtype)
+    ldh = h._rows(shape, "h") if kept else _rows(h, shape, "h", dtype)
+    lds = _rows(dh, shape, "dh", dtype) if dh is not None else N
+    sums = dbias_dtype or torch.float32
+    pw = dw = db = None
+    if weight is not None:
+        _vector(weight, N, "weight")
+        if dbias_dtype not in (None, weight.dtype):
+            raise ValueError("dbias has weight's type")
+        pw, sums = weight.data_ptr(), weight.dtype
+        if dweight:
+            dw = torch.empty(N, dtype=sums, device=dy.device)
+    if dbias:
+        db = torch.empty(N, dtype=sums, device=dy.device)
+    need = _lib.ts_layernorm_backward_workspace(M, N) if dw is not None or db is not None or N > 16384 else 0
+    ws = _scratch(need, dy)
+    _launch(dev, _lib.ts_layernorm_backward, dy.data_ptr(), hd.data_ptr(), pw, dh.data_ptr() if dh is not None else None,
+            out.data_ptr(), dw.data_ptr() if dw is not None else None, db.data_ptr() if db is not None else None, M, N,
+            ldy, ldh, lds, ldx, _TORCH_DTYPE.get(dtype, 0), TS_Q8 if kept else _TORCH_DTYPE.get(dtype, 0),
+            _DTYPE.get(sums, 0), eps, _raw_stream(dev), ws.data_ptr() if need else None, need)
+    return out, dw, db
+
+
+def quantize_rows(x: torch.Tensor, out_dtype: torch.dtype = torch.int8, out: torch.Tensor | None = None):
+    """x [M,N] (fp16, bf16, fp32) in 8 bits with one fp32 scale per row; returns (codes, scale).
+
+    scale = max|x| / 127 (torch.int8) or / 448 (torch.float8_e4m3fn), at least 2^-100; codes = x / scale
+    rounded to nearest even: the operand and scale_a of ``gemm_scaled`` where no norm stands before the
+    product.  A row with an infinity or a NaN has such a scale, and a product of it is NaN.
+    """
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix of rows")
+    M, N = shape = x.shape
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=x.device)
+    dev = _device_of(x, out)
+    ldx, ldy = _rows(x, shape, "x"), _rows(out, shape, "out", out_dtype)
+    scale = torch.empty(M, dtype=torch.float32, device=x.device)
+    _launch(dev, _lib.ts_quantize_rows, x.data_ptr(), out.data_ptr(), scale.data_ptr(), M, N, ldx, ldy,
+            _TORCH_DTYPE.get(x.dtype, 0), _DTYPE.get(out_dtype, 0), _raw_stream(dev))
+    return out, scale
+
+
+def checkpoint_pack(x: torch.Tensor, out: Checkpoint | None = None) -> Checkpoint:
+    """x [M,N] (fp16, bf16, fp32) in 8 bits (``out`` or a new ``Checkpoint``): 33/32 bytes a value."""
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix of rows")
+    M, N = shape = x.shape
+    ldx = _rows(x, shape, "x")
+    if out is None:
+        out = Checkpoint.empty(M, N, x.device)
+    dev = _device_of(x, out.data)
+    _launch(dev, _lib.ts_checkpoint_pack, x.data_ptr(), out.data.data_ptr(), M, N, ldx, out._rows(shape, "out"),
+            _TORCH_DTYPE.get(x.dtype, 0), _raw_stream(dev))
+    return out
+
+
+def checkpoint_unpack(kept: Checkpoint, activation: str = "none", out: torch.Tensor | None = None,
+                      out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """act(value) of what a ``Checkpoint`` keeps, in ``out`` or a new tensor of ``out_dtype`` (fp32).
+
+    The values themselves are exact in bf16 and fp32 (8 significant bits)."""
+    act = _activation(activation)
+    shape = kept.shape
+    out_dtype = out_dtype or (out.dtype if out is not None else torch.float32)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=kept.device)
+    dev = _device_of(kept.data, out)
+    ldo = _rows(out, shape, "out", out_dtype)
+    _launch(dev, _lib.ts_checkpoint_unpack, kept.data.data_ptr(), out.data_ptr(), shape[0], shape[1],
+            kept._rows(shape, "kept"), ldo, _TORCH_DTYPE.get(out_dtype, 0), act, _raw_stream(dev))
+    return out

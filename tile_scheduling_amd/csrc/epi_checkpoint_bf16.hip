@@ -1,0 +1,10 @@
+// Kernel instances with preact in 8 bits: both tiles, bf16 operands, A stored [M][K].
+#include "epilogue_checkpoint.hpp"
+#include "internal.hpp"
+
+namespace ts {
+const void* epi_checkpoint_bf16(int cfg, int out_f32, int path) {
+    if (cfg == CFG_128) return out_f32 ? epi_checkpoint<Cfg128, InBF16, OutF32>(path) : epi_checkpoint<Cfg128, InBF16, OutBF16>(path);
+    return out_f32 ? epi_checkpoint<Cfg256w8, InBF16, OutF32>(path) : epi_checkpoint<Cfg256w8, InBF16, OutBF16>(path);
+}
+}  // namespace ts

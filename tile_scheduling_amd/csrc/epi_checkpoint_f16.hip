@@ -1,0 +1,10 @@
+// Kernel instances with preact in 8 bits: both tiles, fp16 operands, A stored [M][K].
+#include "epilogue_checkpoint.hpp"
+#include "internal.hpp"
+
+namespace ts {
+const void* epi_checkpoint_f16(int cfg, int out_f32, int path) {
+    if (cfg == CFG_128) return out_f32 ? epi_checkpoint<Cfg128, InF16, OutF32>(path) : epi_checkpoint<Cfg128, InF16, OutF16>(path);
+    return out_f32 ? epi_checkpoint<Cfg256w8, InF16, OutF32>(path) : epi_checkpoint<Cfg256w8, InF16, OutF16>(path);
+}
+}  // namespace ts

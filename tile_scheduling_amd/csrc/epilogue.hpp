@@ -19,8 +19,8 @@ namespace ts {
 
 // Activations (same numbering as TS_ACT_* in tsgemm.h).
 enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
-// Element types (same numbering as TS_F16, TS_BF16, TS_F32, TS_E4M3); 0 = absent.
-enum : int { ELT_NONE = 0, ELT_F16 = 1, ELT_BF16 = 2, ELT_F32 = 3, ELT_E4M3 = 4 };
+// Element types (same numbering as TS_F16, TS_BF16, TS_F32, TS_E4M3, TS_I8, TS_Q8); 0 = absent.
+enum : int { ELT_NONE = 0, ELT_F16 = 1, ELT_BF16 = 2, ELT_F32 = 3, ELT_E4M3 = 4, ELT_I8 = 5, ELT_Q8 = 6 };
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
@@ -257,6 +257,10 @@ struct EpiArgs : GemmArgs {
     const float *scale_a, *scale_b;   // 8-bit operands: M and N fp32 (null: 1)
     int bias_type, act, grad;
     int stagger;            // sleeps (320 clocks) between the starts of consecutive groups of programs
+    // preact as rows of 8-bit values and exponents (checkpoint.hpp), written (forward) or read (gradient)
+    // by CheckpointStore and split_finish_kernel in place of aux_out and aux_in; null elsewhere
+    uint8_t* kept;
+    long long ld_kept;      // bytes
 };
 
 // The launch's arguments, read anew from the kernel argument segment: scalars that only the
@@ -391,6 +395,10 @@ struct FusedStore {
                 for (int q = 0; q < NQ; ++q) {
                     float a[4] = {e.acc[i][j][4 * q], e.acc[i][j][4 * q + 1], e.acc[i][j][4 * q + 2], e.acc[i][j][4 * q + 3]};
                     if (PARTS) e.add_parts(a, pt, (i * E::FN + j) * 4 + q, tt);
+                    if (E::INTS) {   // one rounding of the exact sum (none below 2^24)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) a[c] = (float)__builtin_bit_cast(int, a[c]);
+                    }
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         e.acc[i][j][4 * q + c] = E::PAIRS ? __builtin_fmaf(a[c] * sa[i], sb[q][c], bias[q][c]) : a[c] + bias[q][c];
@@ -830,6 +838,7 @@ const void* epi_kernel_by_kind(int kind) {
         return reinterpret_cast<const void*>(&gemm_tiles_kernel<Cfg, TI, TO, PATH, MODE_STREAMK, FusedStore>);
     if constexpr (Cfg::BM == 128) {
         // the sums are fp32 whatever C's type, which for 8-bit operands still chooses the products
+        // (int8: int32, the same for every type of C)
         typedef typename std::conditional<std::is_same<TI, InE4M3>::value && !std::is_same<TO, OutF32>::value, OutBF16, OutF32>::type TS;
         if (kind == EPI_SPLIT) return reinterpret_cast<const void*>(&gemm_split_kernel<Cfg, TI, TS, PATH>);
     }
@@ -843,10 +852,15 @@ const void* epi_kernels_cfg128_e4m3(int out, int path, int kind);
 const void* epi_kernels_cfg256w8_f16(int out_f32, int path, int kind);
 const void* epi_kernels_cfg256w8_bf16(int out_f32, int path, int kind);
 const void* epi_kernels_cfg256w8_e4m3(int out, int path, int kind);
+const void* epi_kernels_cfg128_i8(int out, int path, int kind);
+const void* epi_kernels_cfg256w8_i8(int out, int path, int kind);
+// With CheckpointStore (epilogue_checkpoint.hpp): 16-bit operands, A [M][K].
+const void* epi_checkpoint_f16(int cfg, int out_f32, int path);
+const void* epi_checkpoint_bf16(int cfg, int out_f32, int path);
 
 template <class Cfg, class TI, class TO>
 const void* epi_kernel(int path, int kind) {
-    if constexpr (std::is_same<TI, InE4M3>::value) {
+    if constexpr (is_8bit<TI>()) {
         return epi_kernel_by_kind<Cfg, TI, TO, PATH_EDGE_BT>(kind);
     } else {
         switch (path) {

@@ -11,6 +11,7 @@
 #include <tuple>
 
 #include "../../include/tsgemm.h"
+#include "checkpoint.hpp"
 #include "epilogue.hpp"
 #include "few_rows.hpp"
 #include "split.hpp"
@@ -117,6 +118,7 @@ struct Operand {
 struct EpiPlan {
     Plan p;
     int path, kind, out;
+    bool kept = false;     // preact in 8 bits (TS_Q8)
     int special = 0;       // special form of the epilogue (EPI_SPECIAL + ...), 0: the general one
     int es;                // operand element size in bytes
     Operand a, b;
@@ -128,7 +130,9 @@ struct EpiPlan {
     int64_t off_a, off_b, total;   // workspace offsets of the packed operands, and its size
 };
 
-bool known_type(int32_t t) { return t == TS_F16 || t == TS_BF16 || t == TS_F32 || t == TS_E4M3; }
+bool known_type(int32_t t) { return t == TS_F16 || t == TS_BF16 || t == TS_F32 || t == TS_E4M3 || t == TS_I8; }
+bool eight_bit(int32_t t) { return t == TS_E4M3 || t == TS_I8; }
+constexpr int64_t kMaxKInt8 = (1LL << 17) - 1;   // int32 holds this many products of two int8
 
 // Layout of an operand with `rows` x K (A) or K x `rows` (B) logical elements: s_r and
 // s_k are the strides along its rows (M or N) and along K.
@@ -196,6 +200,8 @@ int special_kind(const ts_epilogue& x, const void* C, int64_t stride_cm, int32_t
 
 const void* epi_kernel_of(const EpiPlan& e, int32_t ab) {
     const int f32 = e.out == TS_F32;
+    if (e.kept && e.kind == EPI_XTILE)
+        return ab == TS_F16 ? epi_checkpoint_f16(e.p.cfg, f32, e.path) : epi_checkpoint_bf16(e.p.cfg, f32, e.path);
     if (e.special && e.kind == EPI_XTILE && e.p.cfg == CFG_256W8) {
         const void* fn = nullptr;
         if (e.path == PATH_EDGE_NN)
@@ -209,11 +215,11 @@ const void* epi_kernel_of(const EpiPlan& e, int32_t ab) {
     if (e.p.cfg == CFG_128) {
         if (ab == TS_F16) return epi_kernels_cfg128_f16(f32, e.path, e.kind);
         if (ab == TS_BF16) return epi_kernels_cfg128_bf16(f32, e.path, e.kind);
-        return epi_kernels_cfg128_e4m3(e.out, e.path, e.kind);
+        return ab == TS_I8 ? epi_kernels_cfg128_i8(e.out, e.path, e.kind) : epi_kernels_cfg128_e4m3(e.out, e.path, e.kind);
     }
     if (ab == TS_F16) return epi_kernels_cfg256w8_f16(f32, e.path, e.kind);
     if (ab == TS_BF16) return epi_kernels_cfg256w8_bf16(f32, e.path, e.kind);
-    return epi_kernels_cfg256w8_e4m3(e.out, e.path, e.kind);
+    return ab == TS_I8 ? epi_kernels_cfg256w8_i8(e.out, e.path, e.kind) : epi_kernels_cfg256w8_e4m3(e.out, e.path, e.kind);
 }
 
 // What planning asks the runtime or computes at length, kept per kernel and per tile grid:
@@ -294,7 +300,7 @@ ts_status epi_plan(const void* A, const void* B, int64_t M, int64_t N, int64_t K
     if (M < 0 || N < 0 || K < 0) return TS_ERR_INVALID_ARG;
     if (M > kMaxExtent || N > kMaxExtent || K > kMaxExtent) return TS_ERR_UNSUPPORTED;
     if (!known_type(ab) || !known_type(c)) return TS_ERR_INVALID_ARG;
-    if (ab == TS_F32 || c == TS_E4M3 || (ab == TS_F16 && c == TS_BF16) || (ab == TS_BF16 && c == TS_F16))
+    if (ab == TS_F32 || eight_bit(c) || (ab == TS_I8 && K > kMaxKInt8) || (ab == TS_F16 && c == TS_BF16) || (ab == TS_BF16 && c == TS_F16))
         return TS_ERR_UNSUPPORTED;
     ts_schedule s = {TS_ORDER_AUTO, 1, TS_MODE_AUTO, 0, 0, TS_TILE_AUTO, TS_INDEX_DIVIDE};
     if (sp) s = *sp;
@@ -310,11 +316,11 @@ ts_status epi_plan(const void* A, const void* B, int64_t M, int64_t N, int64_t K
     if (s.tile_config != TS_TILE_AUTO && s.tile_config != TS_TILE_128x128x64 && s.tile_config != TS_TILE_256x256x64_W8)
         return TS_ERR_UNSUPPORTED;
 
-    e->es = ab == TS_E4M3 ? 1 : 2;
+    e->es = eight_bit(ab) ? 1 : 2;
     e->out = c;
-    ts_status st = operand_layout(M, K, sam, sak, ab == TS_E4M3, &e->a);
+    ts_status st = operand_layout(M, K, sam, sak, eight_bit(ab), &e->a);
     if (st != TS_OK) return st;
-    st = operand_layout(N, K, sbn, sbk, ab == TS_E4M3, &e->b);
+    st = operand_layout(N, K, sbn, sbk, eight_bit(ab), &e->b);
     if (st != TS_OK) return st;
     e->path = e->a.kmaj ? (e->b.kmaj ? PATH_EDGE_BT : PATH_EDGE_NN) : (e->b.kmaj ? PATH_EDGE_ATBT : PATH_EDGE_AT);
 
@@ -407,15 +413,21 @@ bool grid_needs_device(const EpiPlan& e) { return e.p.mode != TS_MODE_TILED && e
 ts_status check_epilogue(const ts_epilogue* x, const void* C, int64_t M, int64_t N, int32_t ab, int32_t c) {
     if (!x) return TS_OK;
     const int ce = c == TS_F32 ? 4 : 2;
+    if (x->preact_dtype != 0 && x->preact_dtype != c && x->preact_dtype != TS_Q8) return TS_ERR_INVALID_ARG;
+    if (x->preact && x->preact_dtype == TS_Q8) {
+        if (eight_bit(ab)) return TS_ERR_UNSUPPORTED;
+        if (M > 1 && (x->stride_pm < kept_row(N) || x->stride_pm % 16 != 0)) return TS_ERR_INVALID_ARG;
+        if ((uintptr_t)x->preact % 16) return TS_ERR_ALIGNMENT;
+    }
     if (x->activation < TS_ACT_NONE || x->activation > TS_ACT_SILU || (x->grad != 0 && x->grad != 1))
         return TS_ERR_INVALID_ARG;
     if (x->bias && x->bias_dtype != TS_F16 && x->bias_dtype != TS_BF16 && x->bias_dtype != TS_F32)
         return TS_ERR_INVALID_ARG;
     if (x->grad && (!x->preact || x->bias || x->residual)) return TS_ERR_INVALID_ARG;
     if (!x->grad && x->preact && (x->preact == C || x->preact == x->residual)) return TS_ERR_INVALID_ARG;
-    if ((x->scale_a || x->scale_b) && ab != TS_E4M3) return TS_ERR_INVALID_ARG;
+    if ((x->scale_a || x->scale_b) && !eight_bit(ab)) return TS_ERR_INVALID_ARG;
     if (x->residual && M > 1 && x->stride_rm < N) return TS_ERR_INVALID_ARG;
-    if (x->preact && M > 1 && x->stride_pm < N) return TS_ERR_INVALID_ARG;
+    if (x->preact && x->preact_dtype != TS_Q8 && M > 1 && x->stride_pm < N) return TS_ERR_INVALID_ARG;
     if ((uintptr_t)x->bias % (x->bias_dtype == TS_F32 ? 4 : 2) || (uintptr_t)x->residual % ce ||
         (uintptr_t)x->preact % ce || (uintptr_t)x->scale_a % 4 || (uintptr_t)x->scale_b % 4)
         return TS_ERR_ALIGNMENT;
@@ -471,16 +483,21 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
     if (M <= 1) stride_cm = N;
     if (stride_cm < N) return TS_ERR_INVALID_ARG;
     if (M > 1 && (stride_cm > kMaxStride || (epi && ((epi->residual && epi->stride_rm > kMaxStride) ||
-                                                     (epi->preact && epi->stride_pm > kMaxStride)))))
+                                                     (epi->preact && epi->preact_dtype != TS_Q8 && epi->stride_pm > kMaxStride)))))
         return TS_ERR_UNSUPPORTED;
     const int ce = c_dtype == TS_F32 ? 4 : 2;
     if ((uintptr_t)A % e.es || (uintptr_t)B % e.es || (uintptr_t)C % ce) return TS_ERR_ALIGNMENT;
     if (epi && (!in_place_ok(C, epi->residual, true, M, stride_cm, epi->stride_rm) ||
-                !in_place_ok(C, epi->preact, true, M, stride_cm, epi->stride_pm)))
+                !in_place_ok(C, epi->preact, epi->preact_dtype != TS_Q8, M, stride_cm, epi->stride_pm)))
         return TS_ERR_INVALID_ARG;
+    // preact in 8 bits: the products of training, A [M][K] (dA and the forward pass)
+    e.kept = epi && epi->preact && epi->preact_dtype == TS_Q8;
+    if (e.kept && (!e.a.kmaj || e.kind == EPI_STREAMK)) return TS_ERR_UNSUPPORTED;
 
     const ts_epilogue plain = {};
-    e.special = special_kind(epi ? *epi : plain, C, stride_cm, c_dtype);
+    if (!e.kept) e.special = special_kind(epi ? *epi : plain, C, stride_cm, c_dtype);
+    uint8_t* kept = e.kept ? static_cast<uint8_t*>(epi->preact) : nullptr;
+    const int64_t ld_kept = e.kept && M > 1 ? epi->stride_pm : 0;
 
     if (e.few) {
         int dev;
@@ -504,12 +521,14 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
             f.grad = epi->grad;
             f.bias = epi->bias;
             f.bias_type = epi->bias_dtype;
-            f.aux_in = epi->grad ? epi->preact : epi->residual;
+            f.aux_in = !epi->grad ? epi->residual : kept ? nullptr : epi->preact;
             f.ld_in = M > 1 ? (epi->grad ? epi->stride_pm : epi->stride_rm) : N;
-            f.aux_out = epi->grad ? nullptr : epi->preact;
+            f.aux_out = epi->grad || kept ? nullptr : epi->preact;
             f.ld_out = M > 1 ? epi->stride_pm : N;
             f.scale_a = epi->scale_a;
             f.scale_b = epi->scale_b;
+            f.kept = kept;
+            f.ld_kept = ld_kept;
         }
         return launch_few_rows(f, ab_dtype, c_dtype, e.b.kmaj, static_cast<hipStream_t>(stream)) ? TS_OK : TS_ERR_HIP;
     }
@@ -587,12 +606,14 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
         g.grad = epi->grad;
         g.bias = epi->bias;
         g.bias_type = epi->bias_dtype;
-        g.aux_in = epi->grad ? epi->preact : epi->residual;
+        g.aux_in = !epi->grad ? epi->residual : kept ? nullptr : epi->preact;
         g.ld_in = M > 1 ? (epi->grad ? epi->stride_pm : epi->stride_rm) : N;
-        g.aux_out = epi->grad ? nullptr : epi->preact;
+        g.aux_out = epi->grad || kept ? nullptr : epi->preact;
         g.ld_out = M > 1 ? epi->stride_pm : N;
         g.scale_a = epi->scale_a;
         g.scale_b = epi->scale_b;
+        g.kept = kept;
+        g.ld_kept = ld_kept;
     }
     g.stagger = stagger_sleeps(e, g.aux_in != nullptr);
     const int threads = e.p.cfg == CFG_128 ? Cfg128::NT : Cfg256w8::NT;
@@ -604,7 +625,7 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
         g.splits = e.splits;
     }
     if (!enqueue(epi_kernel_of(e, ab_dtype), e.p.s.grid, threads, args, hs) ||
-        (e.kind == EPI_SPLIT && !launch_split_finish(g, c_dtype, hs)))
+        (e.kind == EPI_SPLIT && !launch_split_finish(g, ab_dtype, c_dtype, hs)))
         return TS_ERR_HIP;
     return TS_OK;
 }

@@ -18,8 +18,10 @@
 
 #include <algorithm>
 
+#include "checkpoint.hpp"
 #include "few_rows.hpp"
 #include "plan.hpp"
+#include "rows.hpp"
 #include "schedule.hpp"
 
 namespace ts {
@@ -32,6 +34,9 @@ template <class TI>
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
     if constexpr (std::is_same<TI, InF16>::value)
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else if constexpr (std::is_same<TI, InI8>::value)   // int32 sums in the bits of c, as in Engine
+        return __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b),
+                                                                               __builtin_bit_cast(i32x4, c), 0, 0, 0));
     else
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
@@ -79,14 +84,22 @@ __device__ __forceinline__ u32x4 load16_left(const uint8_t* p, long long left, l
     return v;
 }
 
-// One element of C from its fp32 sum.
-template <class TO>
-__device__ __forceinline__ void finish_element(const FewArgs& g, float v, int m, long long n) {
-    typedef typename Elt<TO>::T T;
+// z of an element from its fp32 sum.
+__device__ __forceinline__ float scaled_element(const FewArgs& g, float v, int m, long long n) {
     if (g.scale_a) v *= g.scale_a[m];
     if (g.scale_b) v *= g.scale_b[n];
     if (g.bias) v += load_any(g.bias, g.bias_type, n);
-    const float in = g.aux_in ? (float)static_cast<const T*>(g.aux_in)[m * g.ld_in + n] : 0.0f;
+    return v;
+}
+// One element of C from its z.
+template <class TO, bool KEPT>
+__device__ __forceinline__ void finish_element(const FewArgs& g, float v, int m, long long n) {
+    typedef typename Elt<TO>::T T;
+    float in = g.aux_in ? (float)static_cast<const T*>(g.aux_in)[m * g.ld_in + n] : 0.0f;
+    if (KEPT && g.grad) {
+        const uint8_t* row = g.kept + m * g.ld_kept;
+        in = (float)(int8_t)row[n] * step_of(row[kept_values(g.N) + n / kBlock]);
+    }
     if (g.grad) {
         act_slopes<1>(g.act, &v, &in);
     } else {
@@ -100,7 +113,7 @@ __device__ __forceinline__ void finish_element(const FewArgs& g, float v, int m,
 // Partial sums of the waves, added in wave order, to C.  acc[x][y]: products of column group x
 // with row group y; lane l holds column position 4 (l / 16) + r, row l mod 16; column position
 // p of group x is column p * STRIDE + x * STEP of the workgroup's.
-template <class TO, int WAVES, int NX, int MT, int STRIDE, int STEP>
+template <class TO, int WAVES, int NX, int MT, int STRIDE, int STEP, bool KEPT, bool INTS = false>
 __device__ __forceinline__ void meet_and_finish(const FewArgs& g, const f32x4 (*acc)[MT], float* red, long long n0) {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     constexpr int TILES = NX * MT;
@@ -116,20 +129,35 @@ __device__ __forceinline__ void meet_and_finish(const FewArgs& g, const f32x4 (*
         const int m = o / COLS, c = o % COLS;
         const int x = STEP == 1 ? c % NX : c / 16, p = STEP == 1 ? c / NX : c % 16;
         const long long n = n0 + p * STRIDE + x * STEP;
-        if (m >= g.M || n >= g.N) continue;
+        const bool in = m < g.M && n < g.N;
+        if (!in && !KEPT) continue;
         const float* r = red + ((x * MT + m / 16) * 64 + (p >> 2) * 16 + m % 16) * 4 + (p & 3);
         float v = r[0];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) v += r[w * TILES * 256];
-        finish_element<TO>(g, v, m, n);
+        for (int w = 1; w < WAVES; ++w) v = INTS ? sum_bits(v, r[w * TILES * 256]) : v + r[w * TILES * 256];
+        if (INTS) v = (float)__builtin_bit_cast(int, v);
+        if (KEPT && !g.grad) {
+            // 32 neighbouring lanes hold a block of a row (the launch takes at least 32 columns a
+            // workgroup, and whole waves are here or not)
+            v = in ? scaled_element(g, v, m, n) : 0.0f;
+            const uint32_t ex = block_exponent(lanes_max<32>(__builtin_bit_cast(uint32_t, v) & 0x7fffffffu));
+            if (m < g.M && n < kept_values(g.N)) {
+                uint8_t* row = g.kept + m * g.ld_kept;
+                row[n] = (uint8_t)__builtin_bit_cast(uint32_t, __builtin_fmaf(v, step_inverse(ex), 12582912.0f));
+                if (n % kBlock == 0) row[kept_values(g.N) + n / kBlock] = (uint8_t)ex;
+            }
+            if (in) finish_element<TO, KEPT>(g, v, m, n);
+        } else if (in) {
+            finish_element<TO, KEPT>(g, scaled_element(g, v, m, n), m, n);
+        }
     }
 }
 
 constexpr int kNtWaves = 8;
-// NX groups of 16 columns, MT groups of 16 rows, U steps in flight.
-template <class TI, class TO, int NX, int MT, int U>
+// NX groups of 16 columns, MT groups of 16 rows, U steps in flight; KEPT: preact in 8 bits (g.kept).
+template <class TI, class TO, int NX, int MT, int U, bool KEPT>
 __global__ void __launch_bounds__(kNtWaves * 64) few_nt_kernel(FewArgs g) {
-    constexpr int ES = std::is_same<TI, InE4M3>::value ? 1 : 2;
+    constexpr int ES = is_8bit<TI>() ? 1 : 2;
     constexpr bool WIDE8 = !std::is_same<TO, OutF32>::value;
     __shared__ __attribute__((aligned(16))) float red[kNtWaves * NX * MT * 256];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -205,12 +233,12 @@ __global__ void __launch_bounds__(kNtWaves * 64) few_nt_kernel(FewArgs g) {
 #pragma unroll
             for (int y = 0; y < MT; ++y) acc[x][y] = mfma_pair16<TI, WIDE8>(fb[x], fa[y], acc[x][y]);
     }
-    meet_and_finish<TO, kNtWaves, NX, MT, 1, 16>(g, acc, red, n0);
+    meet_and_finish<TO, kNtWaves, NX, MT, 1, 16, KEPT, std::is_same<TI, InI8>::value>(g, acc, red, n0);
 }
 
 constexpr int kNnWaves = 16;
 // V columns a lane (16 V a workgroup), U steps of 32 rows of B in flight.
-template <class TI, class TO, int V, int MT, int U>
+template <class TI, class TO, int V, int MT, int U, bool KEPT>
 __global__ void __launch_bounds__(kNnWaves * 64) few_nn_kernel(FewArgs g) {
     typedef typename std::conditional<V == 4, u32x2_a2, u32_a2>::type Vec;
     constexpr int W = V / 2;   // dwords of a lane's piece of a row
@@ -289,7 +317,7 @@ __global__ void __launch_bounds__(kNnWaves * 64) few_nn_kernel(FewArgs g) {
         for (int y = 0; y < MT; ++y) fa[y] = load16_left(reinterpret_cast<const uint8_t*>(a[y] + k), 2 * left, 2LL * (k + kg));
         multiply(w, fa);
     }
-    meet_and_finish<TO, kNnWaves, V, MT, V, 1>(g, acc, red, n0);
+    meet_and_finish<TO, kNnWaves, V, MT, V, 1, KEPT>(g, acc, red, n0);
 }
 
 namespace {
@@ -303,25 +331,30 @@ namespace {
 // Columns a lane of few_nn: two, or four where two make more than 256 workgroups (of 16 waves, one on a
 // CU): 16 rows 8192 x 8192 41.8 / 46.3 us, 12290 x 4096 39.6 / 35.3, 28672 x 4096 77.3 / 59.7.
 constexpr int kGroups = 256;
-template <class TI, class TO, int MT>
+template <class TI, class TO, int MT, bool KEPT>
 const void* nt_kernel(int nx) {
-    if (nx == 4) return reinterpret_cast<const void*>(&few_nt_kernel<TI, TO, 4, MT, (MT == 1 ? 3 : 2)>);
-    if (nx == 2) return reinterpret_cast<const void*>(&few_nt_kernel<TI, TO, 2, MT, 4>);
-    return reinterpret_cast<const void*>(&few_nt_kernel<TI, TO, 1, MT, (MT == 1 ? 8 : 4)>);
+    if (nx == 4) return reinterpret_cast<const void*>(&few_nt_kernel<TI, TO, 4, MT, (MT == 1 ? 3 : 2), KEPT>);
+    if constexpr (!KEPT)   // a block of 32 columns lies in one workgroup
+        if (nx == 1) return reinterpret_cast<const void*>(&few_nt_kernel<TI, TO, 1, MT, (MT == 1 ? 8 : 4), false>);
+    return reinterpret_cast<const void*>(&few_nt_kernel<TI, TO, 2, MT, 4, KEPT>);
 }
-template <class TI, class TO, int MT>
+template <class TI, class TO, int MT, bool KEPT>
 const void* nn_kernel(int v) {
-    if (v == 4) return reinterpret_cast<const void*>(&few_nn_kernel<TI, TO, 4, MT, 2>);
-    return reinterpret_cast<const void*>(&few_nn_kernel<TI, TO, 2, MT, (MT == 1 ? 3 : 2)>);
+    if (v == 4) return reinterpret_cast<const void*>(&few_nn_kernel<TI, TO, 4, MT, 2, KEPT>);
+    return reinterpret_cast<const void*>(&few_nn_kernel<TI, TO, 2, MT, (MT == 1 ? 3 : 2), KEPT>);
+}
+template <class TI, class TO, bool KEPT = false>
+const void* few_kernel(bool b_kmaj, int mt, int width) {
+    if constexpr (is_8bit<TI>()) {
+        return mt == 1 ? nt_kernel<TI, TO, 1, false>(width) : nt_kernel<TI, TO, 2, false>(width);
+    } else {
+        if (b_kmaj) return mt == 1 ? nt_kernel<TI, TO, 1, KEPT>(width) : nt_kernel<TI, TO, 2, KEPT>(width);
+        return mt == 1 ? nn_kernel<TI, TO, 1, KEPT>(width) : nn_kernel<TI, TO, 2, KEPT>(width);
+    }
 }
 template <class TI, class TO>
-const void* few_kernel(bool b_kmaj, int mt, int width) {
-    if constexpr (std::is_same<TI, InE4M3>::value) {
-        return mt == 1 ? nt_kernel<TI, TO, 1>(width) : nt_kernel<TI, TO, 2>(width);
-    } else {
-        if (b_kmaj) return mt == 1 ? nt_kernel<TI, TO, 1>(width) : nt_kernel<TI, TO, 2>(width);
-        return mt == 1 ? nn_kernel<TI, TO, 1>(width) : nn_kernel<TI, TO, 2>(width);
-    }
+const void* few_kernel_16(const FewArgs& g, bool b_kmaj, int mt, int width) {
+    return g.kept ? few_kernel<TI, TO, true>(b_kmaj, mt, width) : few_kernel<TI, TO, false>(b_kmaj, mt, width);
 }
 
 }  // namespace
@@ -330,7 +363,7 @@ bool launch_few_rows(FewArgs& g, int ab, int c, bool b_kmaj, hipStream_t stream)
     const int mt = g.M > 16 ? 2 : 1;
     int width, cols;
     if (b_kmaj) {
-        width = g.N <= 16 * kGroups ? 1 : mt == 1 || g.N <= 32 * kGroups ? 2 : 4;
+        width = g.N <= 16 * kGroups && !g.kept ? 1 : mt == 1 || g.N <= 32 * kGroups ? 2 : 4;
         cols = 16 * width;
     } else {
         width = g.N <= 32 * kGroups ? 2 : 4;
@@ -338,10 +371,12 @@ bool launch_few_rows(FewArgs& g, int ab, int c, bool b_kmaj, hipStream_t stream)
     }
     g.tiles = (int)(((int64_t)g.N + cols - 1) / cols);
     const void* fn;
-    if (ab == ELT_F16) fn = c == ELT_F32 ? few_kernel<InF16, OutF32>(b_kmaj, mt, width) : few_kernel<InF16, OutF16>(b_kmaj, mt, width);
-    else if (ab == ELT_BF16) fn = c == ELT_F32 ? few_kernel<InBF16, OutF32>(b_kmaj, mt, width) : few_kernel<InBF16, OutBF16>(b_kmaj, mt, width);
-    else fn = c == ELT_F32 ? few_kernel<InE4M3, OutF32>(true, mt, width)
+    if (ab == ELT_F16) fn = c == ELT_F32 ? few_kernel_16<InF16, OutF32>(g, b_kmaj, mt, width) : few_kernel_16<InF16, OutF16>(g, b_kmaj, mt, width);
+    else if (ab == ELT_BF16) fn = c == ELT_F32 ? few_kernel_16<InBF16, OutF32>(g, b_kmaj, mt, width) : few_kernel_16<InBF16, OutBF16>(g, b_kmaj, mt, width);
+    else if (ab == ELT_E4M3) fn = c == ELT_F32 ? few_kernel<InE4M3, OutF32>(true, mt, width)
               : c == ELT_F16 ? few_kernel<InE4M3, OutF16>(true, mt, width) : few_kernel<InE4M3, OutBF16>(true, mt, width);
+    else fn = c == ELT_F32 ? few_kernel<InI8, OutF32>(true, mt, width)
+              : c == ELT_F16 ? few_kernel<InI8, OutF16>(true, mt, width) : few_kernel<InI8, OutBF16>(true, mt, width);
     void* args[] = {&g};
     return enqueue(fn, g.tiles, (b_kmaj ? kNtWaves : kNnWaves) * 64, args, stream);
 }

@@ -19,6 +19,8 @@ struct FewArgs {
     const float *scale_a, *scale_b;
     int bias_type, act, grad;
     int tiles, xcds;           // workgroups; XCDs they are dealt over
+    uint8_t* kept;             // preact in 8 bits, as in EpiArgs (16-bit operands)
+    long long ld_kept;
 };
 
 // Enqueues the kernel for operands of type ab (ELT_*) and C of type c; b_kmaj: B stored [N][K].  False

@@ -59,6 +59,9 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 struct InF16 {};
 struct InBF16 {};
 struct InE4M3 {};   // 8-bit operands, carried as 16-bit pairs (see Engine::PAIRS)
+struct InI8 {};     // the same, whole numbers: int32 sums (see Engine::INTS)
+template <class TI>
+constexpr bool is_8bit() { return std::is_same<TI, InE4M3>::value || std::is_same<TI, InI8>::value; }
 struct OutF16 {};
 struct OutBF16 {};
 struct OutF32 {};
@@ -157,6 +160,20 @@ template <>
 __device__ __forceinline__ f32x16 mfma32<InBF16>(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// int8: 32 values of k in the bytes that hold 16 in 16 bits, at the same cycles.  The int32 sums keep
+// the bits of the fp32 accumulators' registers; every sum of up to 131071 products is exact.
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+template <>
+__device__ __forceinline__ f32x16 mfma32<InI8>(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_bit_cast(f32x16, __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a),
+                                                                            __builtin_bit_cast(i32x4, b),
+                                                                            __builtin_bit_cast(i32x16, c), 0, 0, 0));
+}
+__device__ __forceinline__ float sum_bits(float a, float b) {   // of two int32 in fp32 registers
+    return __builtin_bit_cast(float, __builtin_bit_cast(int, a) + __builtin_bit_cast(int, b));
 }
 
 // The 8-bit product of two 16-byte chunks of each operand: v_mfma_f32_32x32x64 with
@@ -350,7 +367,8 @@ struct Engine {
     // 8-bit operands: both k-contiguous, so a row of K bytes is a row of K / 2 16-bit
     // pairs and everything but the product (addresses, slots, fragments) is the 16-bit
     // engine's.  Sizes along K (g.K, lda, ldb, slices) count pairs.
-    static constexpr bool PAIRS = std::is_same<TI, InE4M3>::value;
+    static constexpr bool PAIRS = is_8bit<TI>();
+    static constexpr bool INTS = std::is_same<TI, InI8>::value;   // int32 sums, in the bits of acc
     static constexpr bool WIDE8 = !std::is_same<TO, OutF32>::value;   // 8-bit products; else widened
     static constexpr bool EDGES = PATH != PATH_FULL;   // C stores masked to M x N
     static constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK, NT = Cfg::NT;
@@ -1086,9 +1104,9 @@ struct Engine {
         constexpr int NT_ = NMF > F_NFR ? NMF : F_NFR;
 #pragma unroll
         for (int t = 0; t < NT_; ++t) {
-            if constexpr (PAIRS && !WIDE8) {
+            if constexpr (PAIRS && !INTS && !WIDE8) {
                 if (t < NMF) mfma_widened(S, t);
-            } else if constexpr (PAIRS) {
+            } else if constexpr (PAIRS && !INTS) {
                 // the blocks of sub-steps S and S ^ 1 in one product of twice the K: half
                 // of them in each of the two, every second slot
                 if (t < NMF && t % 2 == 0) mfma_pair(S >> 1, (S & 1) * (NMF / 2) + t / 2);
@@ -1309,14 +1327,14 @@ struct Engine {
                 f32x4, __builtin_amdgcn_raw_buffer_load_b128(part_rsrc(pt.base + (long long)(c + 1) * PART_FLOATS),
                                                              t * 16, u * NT * 16, kDeviceScope));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = (v[e] + p0[e]) + p1[e];
+            for (int e = 0; e < 4; ++e) v[e] = INTS ? sum_bits(sum_bits(v[e], p0[e]), p1[e]) : (v[e] + p0[e]) + p1[e];
         }
         if (c <= pt.last) {
             const f32x4 p = __builtin_bit_cast(
                 f32x4, __builtin_amdgcn_raw_buffer_load_b128(part_rsrc(pt.base + (long long)c * PART_FLOATS), t * 16,
                                                              u * NT * 16, kDeviceScope));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += p[e];
+            for (int e = 0; e < 4; ++e) v[e] = INTS ? sum_bits(v[e], p[e]) : v[e] + p[e];
         }
     }
 

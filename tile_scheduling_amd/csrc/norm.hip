@@ -1,5 +1,5 @@
 // Root-mean-square norm of rows with the residual's addition in front of it, 16-bit, 32-bit
-// or e4m3 output with a scale per row, and its gradients.
+// or 8-bit (e4m3, int8) output with a scale per row, and its gradients.
 //
 //   h = x + residual,  r = 1 / sqrt(mean(h^2) + eps),  y = h r w
 //   dx = r (w dy) - h r^3 mean(w dy h) + dh,  dw = sum over rows of dy h r
@@ -15,14 +15,7 @@
 // dw over 1024 workgroups; one row of 4096 4.9 us.
 #include <hip/hip_runtime.h>
 
-#include <limits.h>
-#include <stdint.h>
-
-#include <algorithm>
-
-#include "../../include/tsgemm.h"
-#include "plan.hpp"
-#include "rows.hpp"
+#include "norm.hpp"
 
 namespace ts {
 
@@ -36,61 +29,9 @@ struct NormArgs {
     long long first;   // workgroups before this launch's
 };
 
-constexpr float kE4M3Max = 448.0f;
-constexpr float kMinScale = 0x1p-100f;   // keeps 1 / scale finite; rows of zeros take it
-
-// Eight floats to e4m3 (round to nearest even; |v| <= 448 up to the rounding of the scale,
-// which rounds back to 448).
-__device__ __forceinline__ u32x2 pack8_e4m3(const float* v) {
-    int lo = 0, hi = 0;
-    lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], lo, false);
-    lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
-    hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], hi, false);
-    hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
-    return u32x2{(uint32_t)lo, (uint32_t)hi};
-}
-typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
-__device__ __forceinline__ void store8_e4m3(uint8_t* p, int valid, const float* v) {
-    const u32x2 w = pack8_e4m3(v);
-    if (valid >= 8) {
-        *reinterpret_cast<u32x2_a1*>(p) = w;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < valid) p[e] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
-    }
-}
-// Largest |v| as its bits, so that a NaN wins.
-__device__ __forceinline__ uint32_t max8_bits(const float* v, uint32_t m) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t b = __builtin_bit_cast(uint32_t, v[e]) & 0x7fffffffu;
-        m = b > m ? b : m;
-    }
-    return m;
-}
-__device__ __forceinline__ float row_scale(uint32_t max_bits) {
-    const float s = __builtin_bit_cast(float, max_bits) / kE4M3Max;
-    return s < kMinScale ? kMinScale : s;   // NaN stays NaN
-}
-
-// y / scale with one rounding: the product with the reciprocal, off by up to a step and a half of
-// fp32, and one correction by its remainder.  (The product alone puts values next to the middle between
-// two e4m3 numbers on the wrong side.)  An infinite scale has the reciprocal 0 and no remainder, so
-// that finite values become 0.
-struct Quotient {
-    float inv, scale;
-    __device__ __forceinline__ explicit Quotient(float s)
-        : inv(1.0f / s), scale(s > 3.4028234e38f ? 0.0f : s) {}
-    __device__ __forceinline__ float operator()(float v) const {
-        const float q = v * inv;
-        return __builtin_fmaf(__builtin_fmaf(-q, scale, v), inv, q);
-    }
-};
-
 // T threads a row (T <= 256: 256 / T rows a workgroup), up to C groups of eight columns a
 // thread, T * C * 8 >= N.
-template <class TX, bool Q, int T, int C>
+template <class TX, int Q, int T, int C>
 __global__ void __launch_bounds__(T < 256 ? 256 : T) rmsnorm_kernel(NormArgs g) {
     typedef typename Elt<TX>::T X;
     constexpr int RPW = T < 256 ? 256 / T : 1;
@@ -127,7 +68,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rmsnorm_kernel(NormArgs g) 
         if (g.weight) load8_vec<TX>(g.weight, g.w_type, n, valid, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[c][e] = v[c][e] * r * w[e];
-        if constexpr (Q) {
+        if constexpr (Q != Q_NONE) {
             if (valid < 8) {   // columns past N: a NaN row makes them NaN too, but they count for nothing
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[c][e] = e < valid ? v[c][e] : 0.0f;
@@ -137,8 +78,8 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rmsnorm_kernel(NormArgs g) 
             store8<TX>(static_cast<X*>(g.y) + m * g.ldy + n, valid, v[c]);
         }
     }
-    if constexpr (Q) {
-        const float s = row_scale(row_max<T>(most, lds));
+    if constexpr (Q != Q_NONE) {
+        const float s = row_scale<Q>(row_max<T>(most, lds));
         const Quotient by(s);
         if (t == 0) g.scale[m] = s;
 #pragma unroll
@@ -147,7 +88,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rmsnorm_kernel(NormArgs g) 
             if (valid <= 0) continue;
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[c][e] = by(v[c][e]);
-            store8_e4m3(static_cast<uint8_t*>(g.y) + m * g.ldy + n, valid, v[c]);
+            store8_q<Q>(static_cast<uint8_t*>(g.y) + m * g.ldy + n, valid, v[c]);
         }
     }
 }
@@ -155,8 +96,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rmsnorm_kernel(NormArgs g) 
 // Rows too long for the registers of a workgroup: the row is read again for each step.  h is
 // written last, by the thread that reads its element, so it may take the place of x or the
 // residual.
-constexpr int kLongThreads = 1024;
-template <class TX, bool Q>
+template <class TX, int Q>
 __global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(NormArgs g) {
     typedef typename Elt<TX>::T X;
     __shared__ float lds[kLongThreads / 64];
@@ -186,7 +126,7 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(NormArgs g) 
     sum = row_sum<kLongThreads>(sum, lds);
     const float r = 1.0f / __builtin_sqrtf(sum / (float)g.N + g.eps);
     Quotient by(1.0f);
-    if constexpr (Q) {
+    if constexpr (Q != Q_NONE) {
         uint32_t most = 0;
         for (long long n = threadIdx.x * 8; n < g.N; n += kLongThreads * 8) {
             const int valid = (int)std::min<long long>(g.N - n, 8);
@@ -197,7 +137,7 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(NormArgs g) 
             for (int e = 0; e < 8; ++e) v[e] = e < valid ? v[e] * r * w[e] : 0.0f;
             most = max8_bits(v, most);
         }
-        const float s = row_scale(row_max<kLongThreads>(most, lds));
+        const float s = row_scale<Q>(row_max<kLongThreads>(most, lds));
         by = Quotient(s);
         if (threadIdx.x == 0) g.scale[m] = s;
     }
@@ -209,10 +149,10 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_long_kernel(NormArgs g) 
         if (g.residual) store8<TX>(static_cast<X*>(g.h) + m * g.ldh + n, valid, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[e];
-        if constexpr (Q) {
+        if constexpr (Q != Q_NONE) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = by(v[e]);
-            store8_e4m3(static_cast<uint8_t*>(g.y) + m * g.ldy + n, valid, v);
+            store8_q<Q>(static_cast<uint8_t*>(g.y) + m * g.ldy + n, valid, v);
         } else {
             store8<TX>(static_cast<X*>(g.y) + m * g.ldy + n, valid, v);
         }
@@ -401,7 +341,7 @@ __global__ void __launch_bounds__(kLongThreads) rmsnorm_grad_dx_kernel(NormGradA
     }
 }
 
-__global__ void __launch_bounds__(1024) reduce_columns_kernel(const float* part, int rows, int N, void* out, int type) {
+__global__ void __launch_bounds__(1024) reduce_columns_kernel(const float* part, int rows, int N, void* out, int type, int first, void* out2) {
     __shared__ float sums[16][16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15;
     const int n = (int)blockIdx.x * 16 + c;
@@ -418,22 +358,22 @@ __global__ void __launch_bounds__(1024) reduce_columns_kernel(const float* part,
     if (threadIdx.x < 16 && n < N) {
 #pragma unroll
         for (int w = 1; w < 16; ++w) s += sums[w][c];
-        store_any(out, type, n, s);
+        if (n < first) {
+            if (out) store_any(out, type, n, s);
+        } else if (out2) {
+            store_any(out2, type, n - first, s);
+        }
     }
 }
-bool launch_reduce_columns(const float* part, int rows, int N, void* out, int type, hipStream_t stream) {
-    void* args[] = {&part, &rows, &N, &out, &type};
+bool launch_reduce_columns(const float* part, int rows, int N, void* out, int type, hipStream_t stream, int first, void* out2) {
+    if (first <= 0) first = N;
+    void* args[] = {&part, &rows, &N, &out, &type, &first, &out2};
     return enqueue(reinterpret_cast<const void*>(&reduce_columns_kernel), (N + 15LL) / 16, 1024, args, stream);
 }
 
 namespace {
 
-// Shapes of the register kernels: threads a row and groups of eight columns a thread.
-struct Shape {
-    int t, c;
-};
-
-template <class TX, bool Q>
+template <class TX, int Q>
 const void* norm_kernel(Shape s) {
 #define TS_NORM(T, C) \
     if (s.t == T && s.c == C) return reinterpret_cast<const void*>(&rmsnorm_kernel<TX, Q, T, C>)
@@ -456,23 +396,6 @@ const void* norm_grad_kernel(Shape s) {
     return nullptr;
 }
 
-// Fewest threads a row whose four groups cover it; with few rows (fewer than would give
-// every CU a workgroup) one group a thread where the workgroup allows it.  {0, 0}: a long
-// row.
-Shape norm_shape(int64_t M, int64_t N, int most) {
-    const int64_t groups = (N + 7) / 8;
-    static const int kThreads[] = {16, 64, 256, 1024};
-    for (int t : kThreads) {
-        const int limit = t == 1024 ? most : 4;
-        const int want = t < 1024 && M * t < 256 * 256 ? 1 : limit;
-        if (groups > (int64_t)t * want) continue;
-        int c = 1;
-        while ((int64_t)t * c < groups) c *= 2;
-        return Shape{t, c};
-    }
-    return Shape{0, 0};
-}
-
 int64_t norm_grad_groups(int64_t M, int64_t N) {
     const Shape s = norm_shape(M, N, 4);
     if (s.t == 0) return std::max<int64_t>(1, std::min<int64_t>((M + 63) / 64, 64));
@@ -480,45 +403,11 @@ int64_t norm_grad_groups(int64_t M, int64_t N) {
     return std::min<int64_t>((M + rpw - 1) / rpw, 1024);
 }
 
-bool row_type(int32_t t) { return t == TS_F16 || t == TS_BF16 || t == TS_F32; }
-int type_size(int32_t t) { return t == TS_F32 ? 4 : t == TS_E4M3 ? 1 : 2; }
-
-ts_status norm_sizes(int64_t M, int64_t N) {
-    if (M < 0 || N < 0) return TS_ERR_INVALID_ARG;
-    if (M > INT_MAX / 2 || N >= 1 << 26) return TS_ERR_UNSUPPORTED;   // N: threads of the launches over columns
-    return TS_OK;
-}
-
-ts_status have_device() {
-    int dev;
-    if (hipGetDevice(&dev) != hipSuccess) {
-        (void)hipGetLastError();
-        return TS_ERR_NO_DEVICE;
-    }
-    return TS_OK;
-}
-
-ts_status launch(const void* fn, int64_t gx, int64_t gy, int threads, void* args, hipStream_t stream) {
-    void* argv[] = {args};
-    return enqueue(fn, gx, threads, argv, stream, gy) ? TS_OK : TS_ERR_HIP;
-}
-
-// One workgroup for every few rows: a launch holds fewer than 2^32 threads, so many rows take
-// more than one.
-template <class Args>
-ts_status launch_rows(const void* fn, int64_t blocks, int threads, Args& g, hipStream_t stream) {
-    const int64_t most = (1LL << 31) / threads;
-    for (g.first = 0; g.first < blocks; g.first += most) {
-        const ts_status st = launch(fn, std::min<int64_t>(blocks - g.first, most), 1, threads, &g, stream);
-        if (st != TS_OK) return st;
-    }
-    return TS_OK;
-}
-
 template <class TX>
-ts_status run_norm(NormArgs& g, bool q, hipStream_t stream) {
+ts_status run_norm(NormArgs& g, int32_t y_dtype, hipStream_t stream) {
     const Shape s = norm_shape(g.M, g.N, 8);
-    const void* fn = q ? norm_kernel<TX, true>(s) : norm_kernel<TX, false>(s);
+    const void* fn = y_dtype == TS_E4M3 ? norm_kernel<TX, Q_E4M3>(s) : y_dtype == TS_I8 ? norm_kernel<TX, Q_I8>(s)
+                     : norm_kernel<TX, Q_NONE>(s);
     if (s.t == 0) return launch_rows(fn, g.M, kLongThreads, g, stream);
     const int rpw = s.t < 256 ? 256 / s.t : 1;
     return launch_rows(fn, ((int64_t)g.M + rpw - 1) / rpw, std::max(s.t, 256), g, stream);
@@ -550,10 +439,10 @@ extern "C" ts_status ts_rmsnorm(const void* x, const void* residual, const void*
                                 int32_t y_dtype, float eps, void* stream) {
     ts_status st = norm_sizes(M, N);
     if (st != TS_OK) return st;
-    if (!row_type(x_dtype) || (weight && !row_type(w_dtype)) || !(row_type(y_dtype) || y_dtype == TS_E4M3) ||
+    if (!row_type(x_dtype) || (weight && !row_type(w_dtype)) || !(row_type(y_dtype) || y_dtype == TS_E4M3 || y_dtype == TS_I8) ||
         !(eps >= 0.0f) || eps > 3.4e38f)
         return TS_ERR_INVALID_ARG;
-    const bool q = y_dtype == TS_E4M3;
+    const bool q = y_dtype == TS_E4M3 || y_dtype == TS_I8;
     if ((!q && y_dtype != x_dtype) || (weight && w_dtype != x_dtype && w_dtype != TS_F32)) return TS_ERR_UNSUPPORTED;
     if (M == 0 || (N == 0 && !q)) return TS_OK;
     // rows without elements still have their scale, the least one: the kernel below reads and
@@ -573,9 +462,9 @@ extern "C" ts_status ts_rmsnorm(const void* x, const void* residual, const void*
     if (st != TS_OK) return st;
     NormArgs g = {x, residual, weight, y, h, scale, (int)M, (int)N, w_dtype, stride_x, stride_r, stride_y, stride_h, eps};
     const hipStream_t hs = static_cast<hipStream_t>(stream);
-    if (x_dtype == TS_F16) return run_norm<OutF16>(g, q, hs);
-    if (x_dtype == TS_BF16) return run_norm<OutBF16>(g, q, hs);
-    return run_norm<OutF32>(g, q, hs);
+    if (x_dtype == TS_F16) return run_norm<OutF16>(g, y_dtype, hs);
+    if (x_dtype == TS_BF16) return run_norm<OutBF16>(g, y_dtype, hs);
+    return run_norm<OutF32>(g, y_dtype, hs);
 }
 
 // Bytes: the partial sums of dw, then (long rows) two numbers per row.

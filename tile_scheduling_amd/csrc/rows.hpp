@@ -95,10 +95,12 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, float* lds) {
 // Column sums of `rows` fp32 rows of N (the partial sums of workgroups, in their order) into
 // N elements of any type.  A workgroup takes 16 columns (with 64, too few workgroups for short
 // rows: 1024 rows of 4096 17.3 us, now 6); 64 lanes take every 64th row of a column and are added in a
-// fixed order, so the result does not depend on timing.
-__global__ void reduce_columns_kernel(const float* part, int rows, int N, void* out, int type);
+// fixed order, so the result does not depend on timing.  Columns from `first` on (0: none) go to out2; a null
+// output is not written.
+__global__ void reduce_columns_kernel(const float* part, int rows, int N, void* out, int type, int first, void* out2);
 
 // Enqueues reduce_columns_kernel; false if that failed.
-bool launch_reduce_columns(const float* part, int rows, int N, void* out, int type, hipStream_t stream);
+bool launch_reduce_columns(const float* part, int rows, int N, void* out, int type, hipStream_t stream, int first = 0,
+                           void* out2 = nullptr);
 
 }  // namespace ts

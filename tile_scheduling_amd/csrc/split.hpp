@@ -5,7 +5,8 @@
 
 namespace ts {
 
-// Enqueues the sum over the splits and the epilogue, C of type c (ELT_*); false if that failed.
-bool launch_split_finish(SplitArgs& g, int c, hipStream_t stream);
+// Enqueues the sum over the splits and the epilogue, operands of type ab and C of type c (ELT_*);
+// false if that failed.
+bool launch_split_finish(SplitArgs& g, int ab, int c, hipStream_t stream);
 
 }  // namespace ts
