@@ -54,7 +54,7 @@ def test_layernorm_backward_workspace():
     need = ts._lib.ts_layernorm_backward_workspace
     assert need(0, 64) == 0 and need(4, 0) == 0 and need(-1, 4) == INV
     assert need(1, 100) == 1024                                  # one workgroup: two rows of 100 fp32
-    assert need(3, 16384) == 3 * 2 * 16384 * 4
+    assert need(3, 16384) == 3 * 2 * 16384 * 4 and need(8192, 4096) == 512 * 2 * 4096 * 4
     assert need(70, 16385) == 2 * 2 * 16385 * 4 // 256 * 256 + 256 + 70 * 16   # long rows: groups of 64, four numbers a row
 
 
