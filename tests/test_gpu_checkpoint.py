@@ -147,7 +147,7 @@ def limit(name):
 
 PRODUCTS = [(1, 1, 1, None), (3, 40, 96, None), (17, 70, 200, None), (32, 300, 72, None), (60, 70, 2048, None),
             (200, 140, 96, None), (300, 33, 1000, None), (129, 260, 264, "128x128x64"), (300, 516, 520, "256x256x64w8"),
-            (512, 512, 256, "256x256x64w8")]
+            (512, 512, 256, "256x256x64w8"), (600, 1100, 272, "256x256x64w8")]
 
 
 @pytest.mark.parametrize("M,N,K,tile", PRODUCTS)

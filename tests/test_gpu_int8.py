@@ -95,6 +95,48 @@ def test_every_schedule_gives_the_same_bits(tile, out):
     R.check(c, *R.forward(z, zerr, "gelu", res, out), "C")
 
 
+@pytest.mark.parametrize("out", [H, B, F])
+@pytest.mark.parametrize("K,pad", [(272, 0), (333, 0), (400, 7)])
+def test_every_epilogue_on_the_256_tile(K, pad, out):
+    # tiles inside and on both edges, several a program
+    M, N = 600, 1100
+    n = R.gen(K)
+    a, b = codes(11, M, K), codes(12, N, K)
+    sa, sb = 0.01 * (1 + n(M).abs()), (1 + n(N).abs()) / K
+    res = n(M, N).to(out)
+    sched = ts.Schedule(order="auto", mode="auto", num_programs=3, tile="256x256x64w8")
+    for name in R.ACTS:
+        for bias in (None, n(N), n(N).to(out)):
+            z, zerr = expect(a, b.t(), sa, sb, bias)
+            for r in (None, res):
+                say(K, pad, out, name, bias is not None, r is not None)
+                cd, cb = R.padded(torch.zeros(M, N).to(out), "cuda", pad, pad, fill=3.0)
+                rd = None if r is None else R.padded(r, "cuda", pad, pad)[0]
+                c = ts.gemm_scaled(a.cuda(), b.cuda().t(), sa.cuda(), sb.cuda(), bias=None if bias is None else bias.cuda(),
+                                   activation=name, residual=rd, out=cd, schedule=sched)
+                R.check(c, *R.forward(z, zerr, name, r, out), "C")
+                if r is not None:   # in the residual's place
+                    rd2 = R.padded(r, "cuda", pad, pad)[0]
+                    ts.gemm_scaled(a.cuda(), b.cuda().t(), sa.cuda(), sb.cuda(), bias=None if bias is None else bias.cuda(),
+                                   activation=name, residual=rd2, out=rd2, schedule=sched)
+                    assert torch.equal(rd2, c)
+                cd.fill_(3.0)
+                assert bool((cb == 3.0).all())
+        # one scale alone, and preact beside C
+        for s1, s2 in ((sa, None), (None, sb)):
+            pre = torch.empty(M, N, dtype=out, device="cuda")
+            c = ts.gemm_scaled(a.cuda(), b.cuda().t(), None if s1 is None else s1.cuda(), None if s2 is None else s2.cuda(),
+                               activation=name, preact=pre, out_dtype=out, schedule=sched)
+            d = ts.gemm_scaled(a.cuda(), b.cuda().t(), None if s1 is None else s1.cuda(), None if s2 is None else s2.cuda(),
+                               activation=name, out_dtype=out, schedule=sched)
+            assert torch.equal(c, d)
+            z, zerr = expect(a, b.t(), torch.ones(M) if s1 is None else s1, torch.ones(N) if s2 is None else s2, None)
+            fits = z.abs() < 6e4   # (fp16: without a scale the sums are larger than its values)
+            over = torch.where(fits, zerr + R.rounded(z.abs() + zerr, out), torch.full_like(z, float("inf")))
+            R.check(torch.where(fits.cuda(), pre.double(), torch.zeros((), dtype=torch.float64, device="cuda")),
+                    torch.where(fits, z, torch.zeros_like(z)), over, "preact")
+
+
 @pytest.mark.parametrize("pad,offset", [(0, 1), (3, 0), (16, 16), (5, 3)])
 @pytest.mark.parametrize("M,N,K", [(3, 40, 96), (60, 70, 200), (300, 140, 1000)])
 def test_strides_and_guards(M, N, K, pad, offset):

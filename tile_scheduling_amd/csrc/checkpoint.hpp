@@ -53,6 +53,12 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
     const uint32_t b = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true);   // 2 3 0 1
     return b > v ? b : v;
 }
+// Larger of lanes l and l ^ 32.
+__device__ __forceinline__ uint32_t halves_max(uint32_t v) {
+    // the upper half of the first operand changes places with the lower half of the second
+    const auto s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return s[0] > s[1] ? s[0] : s[1];
+}
 // Eight columns n .. n + 7 of a row (n a multiple of 8) whose exponents begin at `values`; none
 // where n is at or behind N.
 struct Kept8 {

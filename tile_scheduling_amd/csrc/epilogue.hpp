@@ -831,6 +831,7 @@ const void* epi_special_bf16_nn(int out_f32, int kind);
 const void* epi_special_f16_tn(int out_f32, int kind);
 const void* epi_special_bf16_tn(int out_f32, int kind);
 const void* epi_special_bf16_nt(int out_f32, int kind);
+const void* epi_special_i8(int out, int fam, int residual);   // epilogue_int8.hpp
 
 template <class Cfg, class TI, class TO, int PATH>
 const void* epi_kernel_by_kind(int kind) {
@@ -854,9 +855,10 @@ const void* epi_kernels_cfg256w8_bf16(int out_f32, int path, int kind);
 const void* epi_kernels_cfg256w8_e4m3(int out, int path, int kind);
 const void* epi_kernels_cfg128_i8(int out, int path, int kind);
 const void* epi_kernels_cfg256w8_i8(int out, int path, int kind);
-// With CheckpointStore (epilogue_checkpoint.hpp): 16-bit operands, A [M][K].
-const void* epi_checkpoint_f16(int cfg, int out_f32, int path);
-const void* epi_checkpoint_bf16(int cfg, int out_f32, int path);
+// With CheckpointStore (epilogue_checkpoint.hpp), or its special form for a family (-1: none): 16-bit
+// operands, A [M][K].
+const void* epi_checkpoint_f16(int cfg, int out_f32, int path, int fam);
+const void* epi_checkpoint_bf16(int cfg, int out_f32, int path, int fam);
 
 template <class Cfg, class TI, class TO>
 const void* epi_kernel(int path, int kind) {

@@ -119,6 +119,7 @@ struct EpiPlan {
     Plan p;
     int path, kind, out;
     bool kept = false;     // preact in 8 bits (TS_Q8)
+    int kept_fam = -1;     // the family of its special form (forward, no residual), -1: the general one
     int special = 0;       // special form of the epilogue (EPI_SPECIAL + ...), 0: the general one
     int es;                // operand element size in bytes
     Operand a, b;
@@ -187,9 +188,11 @@ int stagger_sleeps(const EpiPlan& e, bool reads) {
 
 // The special form of an epilogue, 0 if it has none.  They exist where the 256 tile runs (see
 // SpecialStore): one use of aux_in or aux_out at most, 16-bit operands, A stored [M][K].
+int family_of(int32_t activation) {
+    return activation == TS_ACT_NONE ? FAM_NONE : activation == TS_ACT_RELU ? FAM_RELU : activation == TS_ACT_GELU ? FAM_ERF : FAM_SIGMOID;
+}
 int special_kind(const ts_epilogue& x, const void* C, int64_t stride_cm, int32_t c) {
-    const int fam = x.activation == TS_ACT_NONE ? FAM_NONE : x.activation == TS_ACT_RELU ? FAM_RELU
-                    : x.activation == TS_ACT_GELU ? FAM_ERF : FAM_SIGMOID;
+    const int fam = family_of(x.activation);
     if (!x.grad && x.residual && x.preact) return 0;
     int aux = x.grad ? AUX_GRAD : x.residual ? AUX_RESIDUAL : x.preact ? AUX_PREACT : AUX_NONE;
     if (aux == AUX_PREACT && c != TS_F32 && (fam == FAM_ERF || fam == FAM_SIGMOID) && (uintptr_t)C % 128 == 0 &&
@@ -201,13 +204,17 @@ int special_kind(const ts_epilogue& x, const void* C, int64_t stride_cm, int32_t
 const void* epi_kernel_of(const EpiPlan& e, int32_t ab) {
     const int f32 = e.out == TS_F32;
     if (e.kept && e.kind == EPI_XTILE)
-        return ab == TS_F16 ? epi_checkpoint_f16(e.p.cfg, f32, e.path) : epi_checkpoint_bf16(e.p.cfg, f32, e.path);
+        return ab == TS_F16 ? epi_checkpoint_f16(e.p.cfg, f32, e.path, e.kept_fam) : epi_checkpoint_bf16(e.p.cfg, f32, e.path, e.kept_fam);
     if (e.special && e.kind == EPI_XTILE && e.p.cfg == CFG_256W8) {
         const void* fn = nullptr;
         if (e.path == PATH_EDGE_NN)
             fn = ab == TS_F16 ? epi_special_f16_nn(f32, e.special) : ab == TS_BF16 ? epi_special_bf16_nn(f32, e.special) : nullptr;
         if (e.path == PATH_EDGE_BT)
             fn = ab == TS_F16 ? epi_special_f16_nt(f32, e.special) : ab == TS_BF16 ? epi_special_bf16_nt(f32, e.special) : nullptr;
+        if (ab == TS_I8 && !f32) {
+            const int aux = (e.special - EPI_SPECIAL) / 4, fam = (e.special - EPI_SPECIAL) % 4;
+            if (aux == AUX_NONE || aux == AUX_RESIDUAL) fn = epi_special_i8(e.out, fam, aux == AUX_RESIDUAL);
+        }
         if (e.path == PATH_EDGE_AT)
             fn = ab == TS_F16 ? epi_special_f16_tn(f32, e.special) : ab == TS_BF16 ? epi_special_bf16_tn(f32, e.special) : nullptr;
         if (fn) return fn;
@@ -496,6 +503,7 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
 
     const ts_epilogue plain = {};
     if (!e.kept) e.special = special_kind(epi ? *epi : plain, C, stride_cm, c_dtype);
+    if (e.kept && !epi->grad && !epi->residual && (M <= 1 || epi->stride_pm <= kMaxStride)) e.kept_fam = family_of(epi->activation);
     uint8_t* kept = e.kept ? static_cast<uint8_t*>(epi->preact) : nullptr;
     const int64_t ld_kept = e.kept && M > 1 ? epi->stride_pm : 0;
 

@@ -4,6 +4,7 @@
 
 #include "checkpoint.hpp"
 #include "epilogue.hpp"
+#include "internal.hpp"
 
 namespace ts {
 
@@ -47,8 +48,7 @@ struct CheckpointStore {
                     const uint32_t a = __builtin_bit_cast(uint32_t, v[q][c]) & 0x7fffffffu;
                     most = a > most ? a : most;
                 }
-            const uint32_t other = __shfl_xor(most, 32, 64);
-            const uint32_t ex = block_exponent(other > most ? other : most);
+            const uint32_t ex = block_exponent(halves_max(most));
             const float inv = step_inverse(ex);
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
@@ -156,10 +156,101 @@ struct CheckpointStore {
     }
 };
 
+// The forward form for one activation family, 16-bit C and no residual, on the 256 tile: straight code as
+// SpecialStore's (see there), for tiles inside M x N.  Against CheckpointStore, bf16, gelu, 4096 x 8192 x 4096
+// 234 / 262 us; against preact in 16 bits 4096 x 8192 x 4096 234 / 226, 4096 x 16384 x 1024 182 / 168.
+template <int FAM>
+struct SpecialCheckpointStore {
+    typedef EpiArgs Args;
+    typedef FusedStore G;
+    typedef SpecialStore<FAM, AUX_NONE> S;
+    static constexpr int MIN_WAVES = 2;
+    static constexpr bool RENEW = true;
+    static __device__ __forceinline__ void start(const EpiArgs& g) { G::start(g); }
+    static constexpr int NQ = G::NQ;
+
+    template <bool PARTS, class E>
+    static __device__ __forceinline__ void store(E& e, const EpiArgs& g0, int m0, int n0, const typename E::Parts& pt) {
+        const EpiArgs& g = fresh_args();
+        typedef typename E::OutType TO;
+        typedef typename Elt<TO>::T T;
+        static_assert(sizeof(T) == 2 && E::FN == 2, "both blocks of a row staged together");
+        if (m0 + E::BM > g.M || n0 + E::BN > g.N) {
+            CheckpointStore::store<PARTS>(e, g0, m0, n0, pt);
+            return;
+        }
+        const G::Tile t = G::tile_of(e, g, m0, n0);
+        typename S::template Walk<E> w(t, g.C, g.ldc);
+        // the rows' values, 16 rows an access, and their exponents, one row a lane
+        const uint32_t ld = (uint32_t)g.ld_kept;   // 16 rows of it fit in 31 bits (host)
+        uint8_t* kv = g.kept + t.m * g.ld_kept + t.n;
+        uint8_t* ke = g.kept + t.m * g.ld_kept + kept_values(t.N) + t.n / kBlock;
+        const uint32_t lane_v = (uint32_t)(t.ln >> 2) * ld + (uint32_t)(t.ln & 3) * 16u, lane_e = (uint32_t)t.r32 * ld;
+        float bias[E::FN * NQ][4], one[NQ][4];
+#pragma unroll
+        for (int j = 0; j < E::FN; ++j) G::template columns<E>(g, t, j, one, bias + j * NQ);
+        const Sigmoid coeff = sigmoid_of(g.act);
+#pragma unroll
+        for (int i = 0; i < E::FM; ++i) {
+            uint32_t ex[E::FN];
+#pragma unroll
+            for (int j = 0; j < E::FN; ++j) {
+                float v[NQ][4];
+                uint32_t most = 0;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    S::z_of(e, i, j, q, bias, v[q]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t a = __builtin_bit_cast(uint32_t, v[q][c]) & 0x7fffffffu;
+                        most = a > most ? a : most;
+                    }
+                }
+                ex[j] = block_exponent(halves_max(most));
+                const float inv = step_inverse(ex[j]);
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    const int at = 32 * j + 8 * q + 4 * t.hk;
+                    *reinterpret_cast<uint32_t*>(CheckpointStore::chunk(t, t.r32, at >> 4) + (at & 15)) = kept_pack4(v[q], inv);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                *reinterpret_cast<u32x4*>(kv + (uint32_t)u * 16u * ld + lane_v) =
+                    *reinterpret_cast<const u32x4*>(CheckpointStore::chunk(t, 16 * u + (t.ln >> 2), t.ln & 3));
+            if (t.hk == 0) *reinterpret_cast<uint16_t*>(ke + lane_e) = (uint16_t)(ex[0] | ex[1] << 8);
+            kv += 32 * g.ld_kept;
+            ke += 32 * g.ld_kept;
+            asm volatile("" : "+s"(kv), "+s"(ke));
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int x = 0; x < E::FN * NQ; ++x) {
+                float v[4];
+                S::z_of(e, i, x / NQ, x % NQ, bias, v);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[c] = fam_value<FAM>(v[c], coeff);
+                Out<TO>::store4(reinterpret_cast<T*>(G::quad_lds(t, (4 * t.hk + 32 * (x / NQ) + 8 * (x % NQ)) * 2)), v, 4, true);
+            }
+            w.store(t);
+            w.next(i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+};
+
 template <class Cfg, class TI, class TO>
 const void* epi_checkpoint(int path) {
     if (path == PATH_EDGE_BT) return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg, TI, TO, PATH_EDGE_BT, false, CheckpointStore>);
     return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg, TI, TO, PATH_EDGE_NN, false, CheckpointStore>);
+}
+template <class TI, class TO, int PATH>
+const void* epi_checkpoint_special(int fam) {
+    switch (fam) {
+        case FAM_RELU: return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg256w8, TI, TO, PATH, false, SpecialCheckpointStore<FAM_RELU>>);
+        case FAM_ERF: return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg256w8, TI, TO, PATH, false, SpecialCheckpointStore<FAM_ERF>>);
+        case FAM_SIGMOID: return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg256w8, TI, TO, PATH, false, SpecialCheckpointStore<FAM_SIGMOID>>);
+        default: return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg256w8, TI, TO, PATH, false, SpecialCheckpointStore<FAM_NONE>>);
+    }
 }
 
 }  // namespace ts
