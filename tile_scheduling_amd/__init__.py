@@ -1,9 +1,10 @@
 """Python binding of libtsgemm (tiled GEMM with tile-order schedules, MI355X).
 
-Argument marshalling only: every step of the computation runs in the HIP
-kernels of ``libtsgemm.so``.  PyTorch supplies device memory and streams.  The
-library is built in-tree by ``python -m tile_scheduling_amd.build``; importing
-this package without it raises ImportError, and there is no fallback path.
+Argument marshalling only (ctypes here, the operators' in ``_binding``): every step of
+the computation runs in the HIP kernels of ``libtsgemm.so``.  PyTorch supplies device
+memory and streams.  Both libraries are built in-tree by ``python -m
+tile_scheduling_amd.build``; importing this package without them raises ImportError, and
+there is no fallback path.
 
     import torch, tile_scheduling_amd as ts
     c = ts.gemm(a, b, out_dtype=torch.float16,
@@ -24,13 +25,16 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python -m tile_scheduling_amd.build`")
 
 _lib = ctypes.CDLL(LIB_PATH)
+try:
+    from . import _binding   # the operators' calls, checked and made in C++ (csrc/binding.cpp)
+except ImportError as e:
+    raise ImportError(f"{e}: build the package with `python -m tile_scheduling_amd.build`") from e
 
 _i32, _i64, _p = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 
 # status codes, element types and schedule enums (include/tsgemm.h)
 TS_OK, TS_ERR_INVALID_ARG, TS_ERR_UNSUPPORTED, TS_ERR_ALIGNMENT, TS_ERR_HIP, TS_ERR_NO_DEVICE = 0, -1, -2, -3, -4, -5
 TS_F16, TS_BF16, TS_F32, TS_E4M3, TS_I8, TS_Q8 = 1, 2, 3, 4, 5, 6
-FEW_ROWS = 32   # products of up to this many rows mostly need no workspace (ts_gemm_epilogue)
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 ORDERS = {"row_major": 0, "grouped": 1, "auto": 2}
 MODES = {"tiled": 0, "persistent": 1, "crosstile": 2, "streamk": 3, "auto": 4}
@@ -353,63 +357,7 @@ def schedule_trace_host(M: int, N: int, K: int, schedule: Schedule, cu_count: in
 
 # ---- operators around the product ------------------------------------------------------
 
-_DTYPE = {**_TORCH_DTYPE, torch.float8_e4m3fn: TS_E4M3, torch.int8: TS_I8}
-
-
-# Calls of a few microseconds of GPU time are bound by what surrounds them on the host, so the
-# checks below read each attribute once, and the stream comes as its raw handle.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _device_of(first: torch.Tensor, *others) -> int:
-    """Index of the one GPU that every given tensor (None: absent) is on."""
-    index = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != index:
-            raise ValueError("all tensors must be on the same GPU")
-    if index < 0:
-        raise ValueError("tensors must be on a GPU")
-    return index
-
-
-def _launch(index: int, fn, *args) -> None:
-    """fn(*args) with GPU `index` current; raises on an error status."""
-    if torch.cuda.current_device() == index:
-        st = fn(*args)
-    else:
-        with torch.cuda.device(index):
-            st = fn(*args)
-    if st != TS_OK:
-        raise TsError(st)
-
-
-def _scratch(nbytes: int, like: torch.Tensor):
-    """A workspace of the call's own, from torch's allocator: calls on other streams, and
-    graphs captured one after the other, never share one."""
-    if nbytes < 0:
-        raise TsError(int(nbytes))
-    return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None
-
-
-def _rows(t: torch.Tensor, shape, what: str, dtype=None) -> int:
-    """Row stride of a matrix with unit column stride, after its checks."""
-    if t.shape != shape:
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
-    row, col = t.stride()
-    if col != 1 and shape[1] > 1:
-        raise ValueError(f"{what} must have unit stride along its rows")
-    return row
-
-
-def _vector(t: torch.Tensor, n: int, what: str, dtype=None) -> None:
-    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{what} must be a contiguous vector of {n}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
-    if t.dtype not in _TORCH_DTYPE:
-        raise ValueError(f"{what} is {t.dtype}")
+_binding.set_error(TsError)
 
 
 class Checkpoint:
@@ -439,7 +387,7 @@ class Checkpoint:
     @classmethod
     def empty(cls, m: int, n: int, device=None) -> "Checkpoint":
         """Room for an [m, n] matrix (rows of whole 64-byte lines)."""
-        return cls(torch.empty((m, -(-33 * -(-n // 32) // 64) * 64), dtype=torch.uint8, device=device or "cuda"), n)
+        return _kept(torch.empty((m, -(-33 * -(-n // 32) // 64) * 64), dtype=torch.uint8, device=device or "cuda"), n)
 
     @property
     def shape(self):
@@ -449,10 +397,17 @@ class Checkpoint:
     def device(self):
         return self.data.device
 
-    def _rows(self, shape, what: str) -> int:
-        if self.shape != shape:
-            raise ValueError(f"{what} has shape {tuple(self.shape)}, expected {tuple(shape)}")
-        return self.data.stride(0)
+
+def _data(t):
+    """A tensor's or a Checkpoint's storage, and the columns that it holds (-1: as many as the tensor has)."""
+    return (t.data, t.n) if type(t) is Checkpoint else (t, -1)
+
+
+def _kept(data: torch.Tensor, n: int) -> Checkpoint:
+    """A Checkpoint of data that this library made."""
+    k = Checkpoint.__new__(Checkpoint)
+    k.data, k.n = data, n
+    return k
 
 
 def _activation(name) -> int:
@@ -461,52 +416,12 @@ def _activation(name) -> int:
     return ACTIVATIONS[name]
 
 
-def _product(a, b, out, out_dtype, epi: _Epilogue, schedule, residual=None, preact=None, bias=None, scale_a=None,
+def _product(a, b, out, out_dtype, act: str, grad: int, schedule, residual=None, preact=None, bias=None, scale_a=None,
              scale_b=None):
-    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[0]:
-        raise ValueError(f"shapes {tuple(a.shape)} @ {tuple(b.shape)} do not multiply")
-    if a.dtype != b.dtype:
-        raise ValueError(f"A is {a.dtype}, B is {b.dtype}")
-    kept = type(preact) is Checkpoint
-    dev = _device_of(a, b, out, bias, residual, preact.data if kept else preact, scale_a, scale_b)
-    (M, K), N = a.shape, b.shape[1]
-    shape = (M, N)
-    if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=a.device)
-    elif out.shape != shape or out.dtype != out_dtype:
-        raise ValueError("out has the wrong shape or type")
-    if residual is not None:
-        epi.residual, epi.stride_rm = residual.data_ptr(), _rows(residual, shape, "residual", out_dtype)
-    if kept:
-        epi.preact, epi.stride_pm, epi.preact_dtype = preact.data.data_ptr(), preact._rows(shape, "preact"), TS_Q8
-    elif preact is not None:
-        epi.preact, epi.stride_pm = preact.data_ptr(), _rows(preact, shape, "preact", out_dtype)
-    if bias is not None:
-        _vector(bias, N, "bias")
-        epi.bias, epi.bias_dtype = bias.data_ptr(), _TORCH_DTYPE[bias.dtype]
-    if scale_a is not None:
-        _vector(scale_a, M, "scale_a", torch.float32)
-        epi.scale_a = scale_a.data_ptr()
-    if scale_b is not None:
-        _vector(scale_b, N, "scale_b", torch.float32)
-        epi.scale_b = scale_b.data_ptr()
-    s = ctypes.byref(schedule._c()) if schedule is not None else None
-    ab_t, c_t = _DTYPE.get(a.dtype, 0), _DTYPE.get(out_dtype, 0)
-    pa, pb, pc = a.data_ptr(), b.data_ptr(), out.data_ptr()
-    if (pc == pa or pc == pb) and M and N and K:
-        raise ValueError("out must not be an operand of the product")
-    if preact is not None and not epi.grad and epi.preact in (pa, pb) and M and N and K:
-        raise ValueError("preact must not be an operand of the product")
-    sam, sak = a.stride()
-    sbk, sbn = b.stride()
-    scm, scn = out.stride()
-    ws, need = None, 0
-    if M > FEW_ROWS or s is not None or sak != 1 or K <= 1 or N >= 1 << 26 or (sbk != 1 and K >= 4096):
-        need = _lib.ts_gemm_epilogue_workspace(pa, pb, M, N, K, sam, sak, sbk, sbn, ab_t, c_t, s)
-        ws = _scratch(need, a)
-    _launch(dev, _lib.ts_gemm_epilogue, pa, pb, pc, M, N, K, sam, sak, sbk, sbn, scm, scn, ab_t, c_t,
-            ctypes.byref(epi), s, _raw_stream(dev), ws.data_ptr() if need else None, need)
-    return out
+    s = schedule._c() if schedule is not None else None
+    preact, n = _data(preact)
+    return _binding.product(a, b, out, out_dtype, _activation(act), grad, ctypes.addressof(s) if s is not None else 0,
+                            residual, preact, n, bias, scale_a, scale_b)
 
 
 def gemm_epilogue(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = None, activation: str = "none",
@@ -524,9 +439,8 @@ def gemm_epilogue(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = 
     are reshaped by the caller.  The gradients: ``gemm_epilogue_backward`` (autograd does not see
     the call, as it does not see ``gemm``).
     """
-    epi = _Epilogue(_activation(activation))
-    return _product(a, b, out, out_dtype or (out.dtype if out is not None else a.dtype), epi, schedule, residual, preact,
-                    bias)
+    return _product(a, b, out, out_dtype or (out.dtype if out is not None else None), activation, 0, schedule, residual,
+                    preact, bias)
 
 
 def gemm_dact(a: torch.Tensor, b: torch.Tensor, preact: torch.Tensor | Checkpoint, activation: str,
@@ -537,7 +451,7 @@ def gemm_dact(a: torch.Tensor, b: torch.Tensor, preact: torch.Tensor | Checkpoin
     ``Checkpoint`` it has A's type (or ``out``'s)."""
     kept = type(preact) is Checkpoint
     dtype = preact.dtype if not kept else out.dtype if out is not None else a.dtype
-    return _product(a, b, out, dtype, _Epilogue(_activation(activation), 1), schedule, preact=preact)
+    return _product(a, b, out, dtype, activation, 1, schedule, preact=preact)
 
 
 def gemm_scaled(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor | None = None,
@@ -555,9 +469,8 @@ def gemm_scaled(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor | None =
     """
     if a.dtype != torch.float8_e4m3fn and a.dtype != torch.int8:
         raise ValueError(f"A is {a.dtype}, expected torch.float8_e4m3fn or torch.int8")
-    epi = _Epilogue(_activation(activation))
-    return _product(a, b, out, out_dtype or (out.dtype if out is not None else torch.bfloat16), epi, schedule, residual,
-                    preact, bias, scale_a, scale_b)
+    return _product(a, b, out, out_dtype or (out.dtype if out is not None else torch.bfloat16), activation, 0, schedule,
+                    residual, preact, bias, scale_a, scale_b)
 
 
 def act_grad(dc: torch.Tensor, preact: torch.Tensor | Checkpoint | None = None, activation: str = "none",
@@ -573,42 +486,8 @@ def act_grad(dc: torch.Tensor, preact: torch.Tensor | Checkpoint | None = None, 
     With activation "none", ``preact`` is read for ``act_out`` only, and dZ is dC itself (not a copy)
     unless ``out`` or ``out_dtype`` asks for one.
     """
-    act = _activation(activation)
-    if dc.dim() != 2:
-        raise ValueError("dC must be a matrix")
-    M, N = shape = dc.shape
-    reads = act or act_out is not None
-    if reads and preact is None:
-        raise ValueError("preact is needed for this activation")
-    if not reads:
-        preact = None
-    kept = type(preact) is Checkpoint
-    ldc = _rows(dc, shape, "dC")
-    ldz = preact._rows(shape, "preact") if kept else _rows(preact, shape, "preact", dc.dtype) if preact is not None else N
-    if out is None and (act or out_dtype not in (None, dc.dtype)):
-        out = torch.empty(shape, dtype=out_dtype or dc.dtype, device=dc.device)
-    z = preact.data if kept else preact
-    dev = _device_of(dc, z, out, act_out)
-    ldo = _rows(out, shape, "out", out_dtype) if out is not None else N
-    db = torch.empty(N, dtype=dbias_dtype, device=dc.device) if dbias else None
-    if out is None and db is None and act_out is None:
-        return dc, None
-    need = _lib.ts_act_grad_workspace(M, N) if dbias else 0
-    ws = _scratch(need, dc)
-    in_t = _DTYPE.get(dc.dtype, 0)
-    out_t = _DTYPE.get(out.dtype, 0) if out is not None else _DTYPE.get(act_out.dtype, 0) if act_out is not None else in_t
-    pz, po = z.data_ptr() if z is not None else None, out.data_ptr() if out is not None else None
-    pd, pw = db.data_ptr() if dbias else None, ws.data_ptr() if need else None
-    if kept or act_out is not None:
-        pv, ldv = None, N
-        if act_out is not None:
-            pv, ldv = act_out.data_ptr(), _rows(act_out, shape, "act_out", out.dtype if out is not None else None)
-        _launch(dev, _lib.ts_act_grad_value, dc.data_ptr(), pz, po, pv, pd, M, N, ldc, ldz, ldo, ldv, in_t,
-                TS_Q8 if kept else in_t, out_t, _DTYPE.get(dbias_dtype, 0), act, _raw_stream(dev), pw, need)
-    else:
-        _launch(dev, _lib.ts_act_grad, dc.data_ptr(), pz, po, pd, M, N, ldc, ldz, ldo, in_t, out_t,
-                _DTYPE.get(dbias_dtype, 0), act, _raw_stream(dev), pw, need)
-    return (out if out is not None else dc), db
+    preact, n = _data(preact)
+    return _binding.act_grad(dc, preact, n, _activation(activation), out, out_dtype, dbias, dbias_dtype, act_out)
 
 
 def gemm_epilogue_backward(dc: torch.Tensor, a: torch.Tensor | Checkpoint, b: torch.Tensor,
@@ -650,35 +529,7 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch
     scale_a of ``gemm_scaled``.  Else scale is None.  The gradients: ``rmsnorm_backward``
     (autograd does not see the call).
     """
-    if x.dim() != 2:
-        raise ValueError("x must be a matrix of rows")
-    if h is not None and residual is None:
-        raise ValueError("h is written only with a residual")
-    M, N = shape = x.shape
-    dtype = x.dtype
-    out_dtype = out_dtype or (out.dtype if out is not None else dtype)
-    if out is None:
-        out = torch.empty_like(x) if out_dtype == dtype else torch.empty(shape, dtype=out_dtype, device=x.device)
-    if residual is not None and h is None:
-        h = torch.empty_like(x)
-    dev = _device_of(x, weight, residual, out, h)
-    ldx = _rows(x, shape, "x")
-    ldy = _rows(out, shape, "out", out_dtype)
-    ldr = ldh = N
-    pr = ph = pw = ps = scale = None
-    if residual is not None:
-        ldr, ldh = _rows(residual, shape, "residual", dtype), _rows(h, shape, "h", dtype)
-        pr, ph = residual.data_ptr(), h.data_ptr()
-    w_t = TS_F32
-    if weight is not None:
-        _vector(weight, N, "weight")
-        pw, w_t = weight.data_ptr(), _TORCH_DTYPE[weight.dtype]
-    if out_dtype == torch.float8_e4m3fn or out_dtype == torch.int8:
-        scale = torch.empty(M, dtype=torch.float32, device=x.device)
-        ps = scale.data_ptr()
-    _launch(dev, _lib.ts_rmsnorm, x.data_ptr(), pr, pw, out.data_ptr(), ph, ps, M, N, ldx, ldr, ldy, ldh,
-            _TORCH_DTYPE.get(dtype, 0), w_t, _DTYPE.get(out_dtype, 0), eps, _raw_stream(dev))
-    return out, scale, (h if h is not None else x)
+    return _binding.rmsnorm(x, weight, residual, eps, out_dtype, out, h)
 
 
 def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor | Checkpoint, weight: torch.Tensor | None = None, eps: float = 1e-6,
@@ -694,28 +545,7 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor | Checkpoint, weight: tor
     """
     if type(h) is Checkpoint:
         h = checkpoint_unpack(h, out_dtype=dy.dtype)
-    if dy.dim() != 2:
-        raise ValueError("dy must be a matrix of rows")
-    M, N = shape = dy.shape
-    dtype = dy.dtype
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dy.device)
-    dev = _device_of(dy, h, weight, dh, out)
-    ldy, ldh, ldx = _rows(dy, shape, "dy"), _rows(h, shape, "h", dtype), _rows(out, shape, "out", dtype)
-    lds = _rows(dh, shape, "dh", dtype) if dh is not None else N
-    dw, w_t = None, TS_F32
-    if weight is not None:
-        _vector(weight, N, "weight")
-        w_t = _TORCH_DTYPE[weight.dtype]
-        if dweight:
-            dw = torch.empty(N, dtype=weight.dtype, device=dy.device)
-    need = _lib.ts_rmsnorm_backward_workspace(M, N) if dw is not None or N > 32768 else 0
-    ws = _scratch(need, dy)
-    _launch(dev, _lib.ts_rmsnorm_backward, dy.data_ptr(), h.data_ptr(), weight.data_ptr() if weight is not None else None,
-            dh.data_ptr() if dh is not None else None, out.data_ptr(), dw.data_ptr() if dw is not None else None, M, N,
-            ldy, ldh, lds, ldx, _TORCH_DTYPE.get(dtype, 0), w_t, eps, _raw_stream(dev),
-            ws.data_ptr() if need else None, need)
-    return out, dw
+    return _binding.rmsnorm_backward(dy, h, weight, eps, dh, dweight, out)
 
 
 def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
@@ -730,40 +560,8 @@ def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.T
     the mean.  ``keep``: receives h in 8 bits, what ``layernorm_backward`` takes in place of h.
     The gradients: ``layernorm_backward`` (autograd does not see the call).
     """
-    if x.dim() != 2:
-        raise ValueError("x must be a matrix of rows")
-    if h is not None and residual is None:
-        raise ValueError("h is written only with a residual")
-    M, N = shape = x.shape
-    dtype = x.dtype
-    out_dtype = out_dtype or (out.dtype if out is not None else dtype)
-    if out is None:
-        out = torch.empty_like(x) if out_dtype == dtype else torch.empty(shape, dtype=out_dtype, device=x.device)
-    if residual is not None and h is None:
-        h = torch.empty_like(x)
-    dev = _device_of(x, weight, bias, residual, out, h, keep.data if keep is not None else None)
-    ldx = _rows(x, shape, "x")
-    ldy = _rows(out, shape, "out", out_dtype)
-    ldr = ldh = ldk = N
-    pr = ph = pw = pb = ps = pk = scale = None
-    if residual is not None:
-        ldr, ldh = _rows(residual, shape, "residual", dtype), _rows(h, shape, "h", dtype)
-        pr, ph = residual.data_ptr(), h.data_ptr()
-    w_t = TS_F32
-    if weight is not None:
-        _vector(weight, N, "weight")
-        pw, w_t = weight.data_ptr(), _TORCH_DTYPE[weight.dtype]
-    if bias is not None:
-        _vector(bias, N, "bias", weight.dtype if weight is not None else None)
-        pb, w_t = bias.data_ptr(), _TORCH_DTYPE[bias.dtype]
-    if out_dtype == torch.float8_e4m3fn or out_dtype == torch.int8:
-        scale = torch.empty(M, dtype=torch.float32, device=x.device)
-        ps = scale.data_ptr()
-    if keep is not None:
-        pk, ldk = keep.data.data_ptr(), keep._rows(shape, "keep")
-    _launch(dev, _lib.ts_layernorm, x.data_ptr(), pr, pw, pb, out.data_ptr(), ph, ps, pk, M, N, ldx, ldr, ldy, ldh, ldk,
-            _TORCH_DTYPE.get(dtype, 0), w_t, _DTYPE.get(out_dtype, 0), eps, _raw_stream(dev))
-    return out, scale, (h if h is not None else x)
+    keep, n = _data(keep)
+    return _binding.layernorm(x, weight, bias, residual, eps, out_dtype, out, h, keep, n)
 
 
 def layernorm_backward(dy: torch.Tensor, h: torch.Tensor | Checkpoint, weight: torch.Tensor | None = None,
@@ -777,36 +575,8 @@ def layernorm_backward(dy: torch.Tensor, h: torch.Tensor | Checkpoint, weight: t
     weight ``dbias_dtype`` (fp32) and dweight is None; summed in fp32 in a fixed order.  The 8-bit output
     of the forward pass is differentiated as y itself (straight through).
     """
-    if dy.dim() != 2:
-        raise ValueError("dy must be a matrix of rows")
-    M, N = shape = dy.shape
-    dtype = dy.dtype
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dy.device)
-    kept = type(h) is Checkpoint
-    hd = h.data if kept else h
-    dev = _device_of(dy, hd, weight, dh, out)
-    ldy, ldx = _rows(dy, shape, "dy"), _rows(out, shape, "out", dtype)
-    ldh = h._rows(shape, "h") if kept else _rows(h, shape, "h", dtype)
-    lds = _rows(dh, shape, "dh", dtype) if dh is not None else N
-    sums = dbias_dtype or torch.float32
-    pw = dw = db = None
-    if weight is not None:
-        _vector(weight, N, "weight")
-        if dbias_dtype not in (None, weight.dtype):
-            raise ValueError("dbias has weight's type")
-        pw, sums = weight.data_ptr(), weight.dtype
-        if dweight:
-            dw = torch.empty(N, dtype=sums, device=dy.device)
-    if dbias:
-        db = torch.empty(N, dtype=sums, device=dy.device)
-    need = _lib.ts_layernorm_backward_workspace(M, N) if dw is not None or db is not None or N > 16384 else 0
-    ws = _scratch(need, dy)
-    _launch(dev, _lib.ts_layernorm_backward, dy.data_ptr(), hd.data_ptr(), pw, dh.data_ptr() if dh is not None else None,
-            out.data_ptr(), dw.data_ptr() if dw is not None else None, db.data_ptr() if db is not None else None, M, N,
-            ldy, ldh, lds, ldx, _TORCH_DTYPE.get(dtype, 0), TS_Q8 if kept else _TORCH_DTYPE.get(dtype, 0),
-            _DTYPE.get(sums, 0), eps, _raw_stream(dev), ws.data_ptr() if need else None, need)
-    return out, dw, db
+    h, n = _data(h)
+    return _binding.layernorm_backward(dy, h, n, weight, eps, dh, dweight, dbias, dbias_dtype, out)
 
 
 def quantize_rows(x: torch.Tensor, out_dtype: torch.dtype = torch.int8, out: torch.Tensor | None = None):
@@ -816,30 +586,14 @@ def quantize_rows(x: torch.Tensor, out_dtype: torch.dtype = torch.int8, out: tor
     rounded to nearest even: the operand and scale_a of ``gemm_scaled`` where no norm stands before the
     product.  A row with an infinity or a NaN has such a scale, and a product of it is NaN.
     """
-    if x.dim() != 2:
-        raise ValueError("x must be a matrix of rows")
-    M, N = shape = x.shape
-    if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=x.device)
-    dev = _device_of(x, out)
-    ldx, ldy = _rows(x, shape, "x"), _rows(out, shape, "out", out_dtype)
-    scale = torch.empty(M, dtype=torch.float32, device=x.device)
-    _launch(dev, _lib.ts_quantize_rows, x.data_ptr(), out.data_ptr(), scale.data_ptr(), M, N, ldx, ldy,
-            _TORCH_DTYPE.get(x.dtype, 0), _DTYPE.get(out_dtype, 0), _raw_stream(dev))
-    return out, scale
+    return _binding.quantize_rows(x, out_dtype, out)
 
 
 def checkpoint_pack(x: torch.Tensor, out: Checkpoint | None = None) -> Checkpoint:
     """x [M,N] (fp16, bf16, fp32) in 8 bits (``out`` or a new ``Checkpoint``): 33/32 bytes a value."""
-    if x.dim() != 2:
-        raise ValueError("x must be a matrix of rows")
-    M, N = shape = x.shape
-    ldx = _rows(x, shape, "x")
     if out is None:
-        out = Checkpoint.empty(M, N, x.device)
-    dev = _device_of(x, out.data)
-    _launch(dev, _lib.ts_checkpoint_pack, x.data_ptr(), out.data.data_ptr(), M, N, ldx, out._rows(shape, "out"),
-            _TORCH_DTYPE.get(x.dtype, 0), _raw_stream(dev))
+        return _kept(_binding.checkpoint_pack(x, None, -1), x.shape[1])
+    _binding.checkpoint_pack(x, out.data, out.n)
     return out
 
 
@@ -848,13 +602,4 @@ def checkpoint_unpack(kept: Checkpoint, activation: str = "none", out: torch.Ten
     """act(value) of what a ``Checkpoint`` keeps, in ``out`` or a new tensor of ``out_dtype`` (fp32).
 
     The values themselves are exact in bf16 and fp32 (8 significant bits)."""
-    act = _activation(activation)
-    shape = kept.shape
-    out_dtype = out_dtype or (out.dtype if out is not None else torch.float32)
-    if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=kept.device)
-    dev = _device_of(kept.data, out)
-    ldo = _rows(out, shape, "out", out_dtype)
-    _launch(dev, _lib.ts_checkpoint_unpack, kept.data.data_ptr(), out.data_ptr(), shape[0], shape[1],
-            kept._rows(shape, "kept"), ldo, _TORCH_DTYPE.get(out_dtype, 0), act, _raw_stream(dev))
-    return out
+    return _binding.checkpoint_unpack(kept.data, kept.n, _activation(activation), out, out_dtype)

@@ -1,4 +1,4 @@
-"""Build libtsgemm.so (HIP kernels + C ABI) for gfx950, in-tree.
+"""Build libtsgemm.so (HIP kernels + C ABI) for gfx950, and the Python module _binding.so over it, in-tree.
 
     python -m tile_scheduling_amd.build      # or: python tile_scheduling_amd/build.py
 
@@ -19,6 +19,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtsgemm.so")
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = "gfx950"
 
 HIPFLAGS = [
@@ -151,7 +152,30 @@ def build(verbose: bool = False, extra=(), jobs: int = 0, incremental: bool = Fa
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    build_binding(verbose)
     return LIB
+
+
+def build_binding(verbose: bool = False) -> str:
+    """The Python module of the operators' calls (csrc/binding.cpp), against the torch that is installed."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    lib_dir = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-unknown-pragmas", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [f"-I{d}" for d in cpp_extension.include_paths() + [sysconfig.get_paths()["include"],
+            os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_hipcc()))), "include")]]
+    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{lib_dir}", "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python",
+            f"-L{HERE}", "-l:libtsgemm.so", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":
