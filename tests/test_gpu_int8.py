@@ -137,8 +137,8 @@ def test_every_epilogue_on_the_256_tile(K, pad, out):
                     torch.where(fits, z, torch.zeros_like(z)), over, "preact")
 
 
-@pytest.mark.parametrize("pad,offset", [(0, 1), (3, 0), (16, 16), (5, 3)])
-@pytest.mark.parametrize("M,N,K", [(3, 40, 96), (60, 70, 200), (300, 140, 1000)])
+@pytest.mark.parametrize("pad,offset", [(0, 1), (3, 0), (4, 4), (16, 16), (5, 3)])
+@pytest.mark.parametrize("M,N,K", [(3, 40, 96), (60, 70, 200), (300, 140, 1000), (140, 300, 1004), (260, 8200, 196)])
 def test_strides_and_guards(M, N, K, pad, offset):
     a, b = codes(5, M, K), codes(6, N, K)
 

@@ -166,11 +166,20 @@ def test_valid_calls_reach_the_device():
             assert epilogue(M=M, strides=s, epi=dict(KEPT, activation=2, grad=1)) == DEV
 
 
-def test_workspace_of_int8_is_that_of_e4m3():
-    for M, N, K in ((4, 64, 64), (100, 64, 100), (100, 64, 2048), (300, 516, 2051)):
-        a, b = (ts._lib.ts_gemm_epilogue_workspace(FAKE, FAKE, M, N, K, K, 1, 1, K, ab, ts.TS_BF16, None)
-                for ab in (I8, ts.TS_E4M3))
-        assert a == b >= 0
+def test_workspace_of_int8():
+    def need(M, N, K, ld=None, ab=I8, a=FAKE, b=FAKE):
+        ld = ld or K
+        return ts._lib.ts_gemm_epilogue_workspace(a, b, M, N, K, ld, 1, 1, ld, ab, ts.TS_BF16, None)
+
+    up = lambda v: -(-v // 256) * 256
+    for M, N, K in ((4, 64, 64), (100, 64, 64), (100, 64, 2048), (300, 516, 2051)):   # whole chunks, or rows of odd bytes
+        assert need(M, N, K) == need(M, N, K, ab=ts.TS_E4M3) >= 0
+    # rows of 4-byte words: one operand, that of fewer rows, is copied with zeros behind K
+    assert need(100, 64, 100) == up(64 * 112) and need(64, 100, 100) == up(64 * 112)
+    assert need(100, 64, 100, ld=112) == up(64 * 112)                 # whatever lies behind K
+    assert need(100, 64, 96, ld=100) == 0                             # no chunk reaches behind K
+    assert need(100, 64, 102, ld=104) == up(100 * 112) + up(64 * 112)
+    assert need(100, 64, 100, a=FAKE + 2) == up(100 * 112) and need(100, 64, 100, b=FAKE + 1) == up(64 * 112)
 
 
 def test_python_refusals_need_no_gpu():

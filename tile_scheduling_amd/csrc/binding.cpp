@@ -146,7 +146,12 @@ struct Launch {
     void* stream;
     explicit Launch(c10::Device d) : guard(d), stream(c10::hip::getCurrentHIPStream(d.index()).stream()) {}
 };
-void check(int64_t status) {
+// One call of the library, other Python threads running meanwhile (a full queue makes a launch wait).
+template <class F>
+void run(F&& f) {
+    PyThreadState* state = PyEval_SaveThread();
+    const ts_status status = f();
+    PyEval_RestoreThread(state);
     if (status != TS_OK) throw Failed{status};
 }
 Tensor empty(at::IntArrayRef size, ScalarType type, const Tensor& like) { return at::empty(size, like.options().dtype(type)); }
@@ -267,8 +272,10 @@ PyObject* product(PyObject* const* p) {
     if (M > kFewRows || s || a.stride(1) != 1 || K <= 1 || N >= 1 << 26 || (b.stride(0) != 1 && K >= 4096))
         need = ts_gemm_epilogue_workspace(pa, pb, M, N, K, a.stride(0), a.stride(1), b.stride(0), b.stride(1), ab_t, c_t, s);
     const Scratch ws(need, a);
-    check(ts_gemm_epilogue(pa, pb, c.data_ptr(), M, N, K, a.stride(0), a.stride(1), b.stride(0), b.stride(1), c.stride(0),
-                           c.stride(1), ab_t, c_t, &e, s, l.stream, ws.ptr(), ws.bytes));
+    run([&] {
+        return ts_gemm_epilogue(pa, pb, c.data_ptr(), M, N, K, a.stride(0), a.stride(1), b.stride(0), b.stride(1),
+                                c.stride(0), c.stride(1), ab_t, c_t, &e, s, l.stream, ws.ptr(), ws.bytes);
+    });
     return out ? same(p[2]) : wrap(made);
 }
 
@@ -299,9 +306,11 @@ PyObject* act_grad(PyObject* const* p) {
     const Tensor db = dbias ? empty({N}, db_t, dc) : Tensor();
     const Scratch ws(dbias ? ts_act_grad_workspace(M, N) : 0, dc);
     void* dz = out ? out->data_ptr() : make ? made.data_ptr() : nullptr;
-    check(ts_act_grad_value(dc.data_ptr(), ptr(preact), dz, ptr(value), dbias ? db.data_ptr() : nullptr, M, N, ldc, ldz, ldo, ldv,
-                            row_code(in), kept ? TS_Q8 : row_code(in), row_code(out_t), row_code(db_t), act, l.stream, ws.ptr(),
-                            ws.bytes));
+    run([&] {
+        return ts_act_grad_value(dc.data_ptr(), ptr(preact), dz, ptr(value), dbias ? db.data_ptr() : nullptr, M, N,
+                                 ldc, ldz, ldo, ldv, row_code(in), kept ? TS_Q8 : row_code(in), row_code(out_t),
+                                 row_code(db_t), act, l.stream, ws.ptr(), ws.bytes);
+    });
     return tuple({out ? same(p[4]) : make ? wrap(made) : same(p[0]), wrap_or_none(db)});
 }
 
@@ -350,8 +359,11 @@ PyObject* rmsnorm(PyObject* const* p) {
     const float eps = real(p[3]);
     Launch l(device_of(n.x, w, n.residual, n.out, n.h));
     n.make();
-    check(ts_rmsnorm(n.x.data_ptr(), ptr(n.residual), ptr(w), n.y, n.h_ptr(), n.scale_ptr(), n.M, n.N, n.ldx, n.ldr, n.ldy, n.ldh,
-                     row_code(n.type), w ? code(w->scalar_type()) : TS_F32, code(n.y_t), eps, l.stream));
+    run([&] {
+        return ts_rmsnorm(n.x.data_ptr(), ptr(n.residual), ptr(w), n.y, n.h_ptr(), n.scale_ptr(), n.M, n.N, n.ldx,
+                          n.ldr, n.ldy, n.ldh, row_code(n.type), w ? code(w->scalar_type()) : TS_F32, code(n.y_t),
+                          eps, l.stream);
+    });
     return n.result();
 }
 
@@ -365,9 +377,12 @@ PyObject* layernorm(PyObject* const* p) {
     const int64_t ldk = keep ? kept_rows(*keep, number(p[9]), n.M, n.N, "keep") : n.N;
     Launch l(device_of(n.x, w, b, n.residual, n.out, n.h, keep));
     n.make();
-    check(ts_layernorm(n.x.data_ptr(), ptr(n.residual), ptr(w), ptr(b), n.y, n.h_ptr(), n.scale_ptr(), ptr(keep), n.M, n.N, n.ldx,
-                       n.ldr, n.ldy, n.ldh, ldk, row_code(n.type), w ? code(w->scalar_type()) : b ? code(b->scalar_type()) : TS_F32,
-                       code(n.y_t), eps, l.stream));
+    run([&] {
+        return ts_layernorm(n.x.data_ptr(), ptr(n.residual), ptr(w), ptr(b), n.y, n.h_ptr(), n.scale_ptr(),
+                            ptr(keep), n.M, n.N, n.ldx, n.ldr, n.ldy, n.ldh, ldk, row_code(n.type), w ?
+                            code(w->scalar_type()) : b ? code(b->scalar_type()) : TS_F32, code(n.y_t), eps,
+                            l.stream);
+    });
     return n.result();
 }
 
@@ -407,9 +422,12 @@ PyObject* rmsnorm_backward(PyObject* const* p) {
     void* dx = n.dx();
     const Tensor dw = n.weight && flag(p[5]) ? empty({n.N}, n.weight->scalar_type(), n.dy) : Tensor();
     const Scratch ws(dw.defined() || n.N > 32768 ? ts_rmsnorm_backward_workspace(n.M, n.N) : 0, n.dy);
-    check(ts_rmsnorm_backward(n.dy.data_ptr(), n.h.data_ptr(), ptr(n.weight), ptr(n.dh), dx, dw.defined() ? dw.data_ptr() : nullptr,
-                              n.M, n.N, n.ldy, n.ldh, n.lds, n.ldx, row_code(n.type),
-                              n.weight ? code(n.weight->scalar_type()) : TS_F32, eps, l.stream, ws.ptr(), ws.bytes));
+    run([&] {
+        return ts_rmsnorm_backward(n.dy.data_ptr(), n.h.data_ptr(), ptr(n.weight), ptr(n.dh), dx, dw.defined() ?
+                                   dw.data_ptr() : nullptr, n.M, n.N, n.ldy, n.ldh, n.lds, n.ldx, row_code(n.type),
+                                   n.weight ? code(n.weight->scalar_type()) : TS_F32, eps, l.stream, ws.ptr(),
+                                   ws.bytes);
+    });
     return tuple({n.dx_object(), wrap_or_none(dw)});
 }
 
@@ -423,9 +441,12 @@ PyObject* layernorm_backward(PyObject* const* p) {
     void* dx = n.dx();
     const Tensor dw = n.weight && flag(p[6]) ? empty({n.N}, sums, n.dy) : Tensor(), db = flag(p[7]) ? empty({n.N}, sums, n.dy) : Tensor();
     const Scratch ws(dw.defined() || db.defined() || n.N > 16384 ? ts_layernorm_backward_workspace(n.M, n.N) : 0, n.dy);
-    check(ts_layernorm_backward(n.dy.data_ptr(), n.h.data_ptr(), ptr(n.weight), ptr(n.dh), dx, dw.defined() ? dw.data_ptr() : nullptr,
-                                db.defined() ? db.data_ptr() : nullptr, n.M, n.N, n.ldy, n.ldh, n.lds, n.ldx, row_code(n.type),
-                                n.kept ? TS_Q8 : row_code(n.type), row_code(sums), eps, l.stream, ws.ptr(), ws.bytes));
+    run([&] {
+        return ts_layernorm_backward(n.dy.data_ptr(), n.h.data_ptr(), ptr(n.weight), ptr(n.dh), dx, dw.defined() ?
+                                     dw.data_ptr() : nullptr, db.defined() ? db.data_ptr() : nullptr, n.M, n.N,
+                                     n.ldy, n.ldh, n.lds, n.ldx, row_code(n.type), n.kept ? TS_Q8 :
+                                     row_code(n.type), row_code(sums), eps, l.stream, ws.ptr(), ws.bytes);
+    });
     return tuple({n.dx_object(), wrap_or_none(dw), wrap_or_none(db)});
 }
 
@@ -438,8 +459,11 @@ PyObject* quantize_rows(PyObject* const* p) {
     const int64_t ldx = rows(x, M, N, "x"), ldy = out ? rows(*out, M, N, "out", to) : N;
     Launch l(device_of(x, out));
     const Tensor made = out ? Tensor() : empty({M, N}, to, x), scale = empty({M}, at::kFloat, x);
-    check(ts_quantize_rows(x.data_ptr(), out ? out->data_ptr() : made.data_ptr(), static_cast<float*>(scale.data_ptr()), M, N, ldx,
-                           ldy, row_code(x.scalar_type()), code(to), l.stream));
+    run([&] {
+        return ts_quantize_rows(x.data_ptr(), out ? out->data_ptr() : made.data_ptr(),
+                                static_cast<float*>(scale.data_ptr()), M, N, ldx, ldy, row_code(x.scalar_type()),
+                                code(to), l.stream);
+    });
     return tuple({out ? same(p[2]) : wrap(made), wrap(scale)});
 }
 
@@ -454,7 +478,10 @@ PyObject* checkpoint_pack(PyObject* const* p) {
     Launch l(device_of(x, out));
     const Tensor made = out ? Tensor() : empty({M, kept_pitch(N)}, at::kByte, x);
     const Tensor& d = out ? *out : made;
-    check(ts_checkpoint_pack(x.data_ptr(), d.data_ptr(), M, N, ldx, d.stride(0), row_code(x.scalar_type()), l.stream));
+    run([&] {
+        return ts_checkpoint_pack(x.data_ptr(), d.data_ptr(), M, N, ldx, d.stride(0), row_code(x.scalar_type()),
+                                  l.stream);
+    });
     return out ? same(p[1]) : wrap(made);
 }
 
@@ -462,12 +489,15 @@ PyObject* checkpoint_pack(PyObject* const* p) {
 PyObject* checkpoint_unpack(PyObject* const* p) {
     const Tensor &d = tensor(p[0], "kept"), *out = maybe(p[3], "out");
     const int64_t M = d.size(0), N = number(p[1]);
+    const int32_t act = (int32_t)number(p[2]);
     const ScalarType to = dtype(p[4], out ? out->scalar_type() : at::kFloat);
     const int64_t ldo = out ? rows(*out, M, N, "out", to) : N;
     Launch l(device_of(d, out));
     const Tensor made = out ? Tensor() : empty({M, N}, to, d);
-    check(ts_checkpoint_unpack(d.data_ptr(), out ? out->data_ptr() : made.data_ptr(), M, N, d.stride(0), ldo, row_code(to),
-                               (int32_t)number(p[2]), l.stream));
+    run([&] {
+        return ts_checkpoint_unpack(d.data_ptr(), out ? out->data_ptr() : made.data_ptr(), M, N, d.stride(0), ldo,
+                                    row_code(to), act, l.stream);
+    });
     return out ? same(p[3]) : wrap(made);
 }
 

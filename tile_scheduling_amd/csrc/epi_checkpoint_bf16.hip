@@ -4,9 +4,13 @@
 
 namespace ts {
 const void* epi_checkpoint_bf16(int cfg, int out_f32, int path, int fam) {
-    if (cfg == CFG_256W8 && !out_f32 && fam >= 0)
-        return path == PATH_EDGE_BT ? epi_checkpoint_special<InBF16, OutBF16, PATH_EDGE_BT>(fam)
-                                    : epi_checkpoint_special<InBF16, OutBF16, PATH_EDGE_NN>(fam);
+    if (!out_f32 && fam >= 0) {
+        if (cfg == CFG_128)
+            return path == PATH_EDGE_BT ? epi_checkpoint_special<Cfg128, InBF16, OutBF16, PATH_EDGE_BT>(fam)
+                                        : epi_checkpoint_special<Cfg128, InBF16, OutBF16, PATH_EDGE_NN>(fam);
+        return path == PATH_EDGE_BT ? epi_checkpoint_special<Cfg256w8, InBF16, OutBF16, PATH_EDGE_BT>(fam)
+                                    : epi_checkpoint_special<Cfg256w8, InBF16, OutBF16, PATH_EDGE_NN>(fam);
+    }
     if (cfg == CFG_128) return out_f32 ? epi_checkpoint<Cfg128, InBF16, OutF32>(path) : epi_checkpoint<Cfg128, InBF16, OutBF16>(path);
     return out_f32 ? epi_checkpoint<Cfg256w8, InBF16, OutF32>(path) : epi_checkpoint<Cfg256w8, InBF16, OutBF16>(path);
 }

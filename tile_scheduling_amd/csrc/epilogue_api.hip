@@ -173,6 +173,30 @@ ts_status operand_pack(Operand* o, uintptr_t base, int es, int tile) {
     return TS_OK;
 }
 
+// int8 operands whose rows lie on 4 bytes need no copy for their own sake: the loads take 16 bytes at that
+// alignment, and what the last chunk of a row reads of the next one is finite and meets zeros, if the other
+// operand is copied (K of a multiple of 16: there is no such chunk).  The operand of more rows stays as it is.
+// Both copied / one, us: 5000 x 12290 x 1000 94.7 / 91.3, 2048 x 8192 x 4092 76.5 / 71.3, 64 x 1984 x 740 14.9 / 14.1.
+void int8_unpack(Operand* a, Operand* b, uintptr_t base_a, uintptr_t base_b, int tile) {
+    const int64_t K = a->cols;
+    auto direct = [&](const Operand& o, uintptr_t base) {
+        return base % 4 == 0 && o.ld % 4 == 0 && K % 4 == 0 && tile * o.ld < kOffsetLimit;
+    };
+    auto leave = [](Operand* o) {
+        o->pack = false;
+        o->packed_bytes = 0;
+    };
+    const bool da = a->pack && direct(*a, base_a), db = b->pack && direct(*b, base_b);
+    if (K % 16 == 0) {
+        if (da) leave(a);
+        if (db) leave(b);
+    } else if (db && (!da || b->rows >= a->rows)) {
+        leave(b);
+    } else if (da) {
+        leave(a);
+    }
+}
+
 // Sleeps (320 clocks, FusedStore::start) between the starts of the eight groups of programs.
 // With fp32 C a 256 tile moves 256 KiB after its K loop, 512 KiB with a matrix read beside it, as
 // long as 9 or 18 K steps at the copy rate while all CUs do it at once; spread over a part of a
@@ -357,6 +381,7 @@ ts_status epi_plan(const void* A, const void* B, int64_t M, int64_t N, int64_t K
     if (st != TS_OK) return st;
     st = operand_pack(&e->b, (uintptr_t)B, e->es, e->b.kmaj ? p.bn : p.bk);
     if (st != TS_OK) return st;
+    if (ab == TS_I8) int8_unpack(&e->a, &e->b, (uintptr_t)A, (uintptr_t)B, p.bm);
     e->kp = e->a.kmaj || e->b.kmaj ? round_up(K, 16 / e->es) : K;
     // the kernels run at least two K steps a tile; slices past K read as zero
     const int64_t nm = cdiv64(M, p.bm), nn = cdiv64(N, p.bn), ks = std::max<int64_t>(2, cdiv64(e->kp, p.bk));

@@ -243,13 +243,13 @@ const void* epi_checkpoint(int path) {
     if (path == PATH_EDGE_BT) return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg, TI, TO, PATH_EDGE_BT, false, CheckpointStore>);
     return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg, TI, TO, PATH_EDGE_NN, false, CheckpointStore>);
 }
-template <class TI, class TO, int PATH>
+template <class Cfg, class TI, class TO, int PATH>
 const void* epi_checkpoint_special(int fam) {
     switch (fam) {
-        case FAM_RELU: return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg256w8, TI, TO, PATH, false, SpecialCheckpointStore<FAM_RELU>>);
-        case FAM_ERF: return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg256w8, TI, TO, PATH, false, SpecialCheckpointStore<FAM_ERF>>);
-        case FAM_SIGMOID: return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg256w8, TI, TO, PATH, false, SpecialCheckpointStore<FAM_SIGMOID>>);
-        default: return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg256w8, TI, TO, PATH, false, SpecialCheckpointStore<FAM_NONE>>);
+        case FAM_RELU: return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg, TI, TO, PATH, false, SpecialCheckpointStore<FAM_RELU>>);
+        case FAM_ERF: return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg, TI, TO, PATH, false, SpecialCheckpointStore<FAM_ERF>>);
+        case FAM_SIGMOID: return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg, TI, TO, PATH, false, SpecialCheckpointStore<FAM_SIGMOID>>);
+        default: return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg, TI, TO, PATH, false, SpecialCheckpointStore<FAM_NONE>>);
     }
 }
 
