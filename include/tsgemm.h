@@ -428,7 +428,8 @@ typedef struct {
  *   8-bit operands a K step holds 128 values.
  *   Up to 32 rows, A stored [M][K] (B stored [K][N]: K below 4096, up to 16 rows below
  *   8192), and a schedule that leaves order, mode, tile and programs to the library: one pass over B with K split over the waves of a workgroup
- *   (sums in another order than the tile kernels', the same on every run), no workspace.
+ *   (sums in another order than the tile kernels', the same on every run), no workspace.  TS_I8, N up to
+ *   8192: up to 64 rows with K up to 4096, 128 with K up to 2048.
  *   With such a schedule and few tiles, K is split among programs (whole fp32 tiles of sums in
  *   the workspace) and a second kernel adds the parts, in order, and applies the epilogue.
  *   workspace: at least ts_gemm_epilogue_workspace bytes for the same arguments,

@@ -35,7 +35,8 @@ def expect(a, b, sa, sb, bias):
 
 
 SHAPES = [(1, 1, 1), (1, 128, 256), (4, 96, 48), (17, 130, 1000), (32, 33, 144), (31, 9000, 80), (129, 257, 144), (200, 300, 77), (33, 64, 2048),
-          (60, 140, 4099), (300, 520, 1000), (512, 512, 384)]
+          (60, 140, 4099), (300, 520, 1000), (512, 512, 384), (64, 300, 77), (100, 33, 1000), (128, 130, 2048), (40, 4100, 4096),
+          (65, 8192, 130), (48, 5, 3)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -64,7 +65,7 @@ def test_sums_are_exact(M, N, K):
     assert torch.equal(ts.gemm_scaled(a.cuda(), b.cuda().t(), out_dtype=F).cpu(), want)
 
 
-@pytest.mark.parametrize("M,N", [(2, 16), (40, 16), (200, 16)])
+@pytest.mark.parametrize("M,N", [(2, 16), (40, 16), (200, 16), (100, 16)])
 def test_largest_sums(M, N):
     K = (1 << 17) - 1
     a, b = torch.full((M, K), -128, dtype=I), torch.full((N, K), -128, dtype=I)
@@ -138,7 +139,7 @@ def test_every_epilogue_on_the_256_tile(K, pad, out):
 
 
 @pytest.mark.parametrize("pad,offset", [(0, 1), (3, 0), (4, 4), (16, 16), (5, 3)])
-@pytest.mark.parametrize("M,N,K", [(3, 40, 96), (60, 70, 200), (300, 140, 1000), (140, 300, 1004), (260, 8200, 196)])
+@pytest.mark.parametrize("M,N,K", [(3, 40, 96), (60, 70, 200), (90, 5000, 130), (300, 140, 1000), (140, 300, 1004), (260, 8200, 196)])
 def test_strides_and_guards(M, N, K, pad, offset):
     a, b = codes(5, M, K), codes(6, N, K)
 

@@ -172,14 +172,17 @@ def test_workspace_of_int8():
         return ts._lib.ts_gemm_epilogue_workspace(a, b, M, N, K, ld, 1, 1, ld, ab, ts.TS_BF16, None)
 
     up = lambda v: -(-v // 256) * 256
-    for M, N, K in ((4, 64, 64), (100, 64, 64), (100, 64, 2048), (300, 516, 2051)):   # whole chunks, or rows of odd bytes
+    for M, N, K in ((4, 64, 64), (200, 64, 64), (200, 64, 2048), (300, 516, 2051)):   # whole chunks, or rows of odd bytes
         assert need(M, N, K) == need(M, N, K, ab=ts.TS_E4M3) >= 0
     # rows of 4-byte words: one operand, that of fewer rows, is copied with zeros behind K
-    assert need(100, 64, 100) == up(64 * 112) and need(64, 100, 100) == up(64 * 112)
-    assert need(100, 64, 100, ld=112) == up(64 * 112)                 # whatever lies behind K
-    assert need(100, 64, 96, ld=100) == 0                             # no chunk reaches behind K
-    assert need(100, 64, 102, ld=104) == up(100 * 112) + up(64 * 112)
-    assert need(100, 64, 100, a=FAKE + 2) == up(100 * 112) and need(100, 64, 100, b=FAKE + 1) == up(64 * 112)
+    assert need(200, 160, 100) == up(160 * 112) and need(160, 200, 100) == up(160 * 112)
+    assert need(200, 160, 100, ld=112) == up(160 * 112)                 # whatever lies behind K
+    assert need(200, 160, 96, ld=100) == 0                              # no chunk reaches behind K
+    assert need(200, 160, 102, ld=104) == up(200 * 112) + up(160 * 112)
+    assert need(200, 160, 100, a=FAKE + 2) == up(200 * 112) and need(200, 160, 100, b=FAKE + 1) == up(160 * 112)
+    # up to 128 rows in one pass over B, as far as that pays
+    assert need(128, 64, 2047) == 0 and need(64, 8192, 4095) == 0 and need(32, 9000, 9001) == 0
+    assert need(129, 64, 2047) > 0 and need(128, 64, 2051) > 0 and need(65, 64, 4095) > 0 and need(64, 8193, 4095) > 0
 
 
 def test_python_refusals_need_no_gpu():

@@ -360,7 +360,7 @@ ts_status epi_plan(const void* A, const void* B, int64_t M, int64_t N, int64_t K
     // (B stored [K][N]: up to the K where the split tiles win, us few / tiles: 16 rows 4096 x 4096 14.9 / 17.6, 8192 x
     // 8192 41.8 / 39.1, 4096 x 14336 66.5 / 37.4; 32 rows 12290 x 1000 12.5 / 16.8, 4096 x 4096 18.5 / 17.6, 28672 x 4096
     // 71.1 / 62.3)
-    e->few = open && M > 0 && M <= kFewRows && N < 1 << 26 && e->a.kmaj &&   // N: threads of a launch
+    e->few = open && M > 0 && M <= few_rows_most(ab == TS_I8, N, K) && N < 1 << 26 && e->a.kmaj &&   // N: threads of a launch
              (e->b.kmaj || K < (M > 16 ? 4096 : 8192));
     e->splits = 1;
     e->sums_bytes = 0;

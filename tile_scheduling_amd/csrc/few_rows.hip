@@ -7,7 +7,8 @@
 // with the rows of A padded to 16: rows past M (and columns past N) repeat the last one and
 // are not stored.  Every load takes any element alignment, so nothing is packed.  Measured, bf16, B [N][K]:
 // 1 x 4096 x 4096 7.7 us (4.4 TB/s), 1 x 28672 x 4096 46 us (5.1 TB/s); e4m3 4 x 8192 x 8192 12.8 us (5.3 TB/s);
-// B [K][N] 13 x 12290 x 1000 8.9 us (2.8 TB/s), 1 x 28672 x 4096 52 us (4.6 TB/s).
+// B [K][N] 13 x 12290 x 1000 8.9 us (2.8 TB/s), 1 x 28672 x 4096 52 us (4.6 TB/s).  int8 operands, whose sums
+// are the same in every order, come here with up to 128 rows where that is faster than tiles.
 //
 //   B [N][K] (few_nt): a wave reads 128 bytes of 16 rows of B a step, lane group g bytes
 //     32 g .. 32 g + 31 of each, which are its k of two 16-bit products or one 8-bit one
@@ -338,6 +339,18 @@ const void* nt_kernel(int nx) {
         if (nx == 1) return reinterpret_cast<const void*>(&few_nt_kernel<TI, TO, 1, MT, (MT == 1 ? 8 : 4), false>);
     return reinterpret_cast<const void*>(&few_nt_kernel<TI, TO, 2, MT, 4, KEPT>);
 }
+// More than 32 rows of int8 operands (few_rows_most).  bf16 C, one group of columns / two / the tiles: 64 rows 1984 x
+// 740 6.3 / 7.7 / 13.8 us, 4096 x 4096 13.3 / 16.8 / 16.4, 5952 x 2368 14.5 / 10.7 / 20.9, 8192 x 8192 44.6 / 29.5 / 28.9; 128 rows
+// 1984 x 740 9.3 / 13.1 / 14.5, 5952 x 2368 25.4 / 18.7 / 23.7, 4096 x 4096 21.4 / 26.4 / 18.3.
+template <class TO>
+const void* many_kernel(int mt, int nx) {
+    if (mt == 4) {
+        if (nx == 1) return reinterpret_cast<const void*>(&few_nt_kernel<InI8, TO, 1, 4, 3, false>);
+        return reinterpret_cast<const void*>(&few_nt_kernel<InI8, TO, 2, 4, 2, false>);
+    }
+    if (nx == 1) return reinterpret_cast<const void*>(&few_nt_kernel<InI8, TO, 1, 8, 1, false>);
+    return reinterpret_cast<const void*>(&few_nt_kernel<InI8, TO, 2, 8, 1, false>);
+}
 template <class TI, class TO, int MT, bool KEPT>
 const void* nn_kernel(int v) {
     if (v == 4) return reinterpret_cast<const void*>(&few_nn_kernel<TI, TO, 4, MT, 2, KEPT>);
@@ -360,9 +373,12 @@ const void* few_kernel_16(const FewArgs& g, bool b_kmaj, int mt, int width) {
 }  // namespace
 
 bool launch_few_rows(FewArgs& g, int ab, int c, bool b_kmaj, hipStream_t stream) {
-    const int mt = g.M > 16 ? 2 : 1;
+    const int mt = g.M > 64 ? 8 : g.M > 32 ? 4 : g.M > 16 ? 2 : 1;
     int width, cols;
-    if (b_kmaj) {
+    if (mt > 2) {
+        width = g.N <= 16 * kGroups ? 1 : 2;
+        cols = 16 * width;
+    } else if (b_kmaj) {
         width = g.N <= 16 * kGroups && !g.kept ? 1 : mt == 1 || g.N <= 32 * kGroups ? 2 : 4;
         cols = 16 * width;
     } else {
@@ -375,6 +391,7 @@ bool launch_few_rows(FewArgs& g, int ab, int c, bool b_kmaj, hipStream_t stream)
     else if (ab == ELT_BF16) fn = c == ELT_F32 ? few_kernel_16<InBF16, OutF32>(g, b_kmaj, mt, width) : few_kernel_16<InBF16, OutBF16>(g, b_kmaj, mt, width);
     else if (ab == ELT_E4M3) fn = c == ELT_F32 ? few_kernel<InE4M3, OutF32>(true, mt, width)
               : c == ELT_F16 ? few_kernel<InE4M3, OutF16>(true, mt, width) : few_kernel<InE4M3, OutBF16>(true, mt, width);
+    else if (mt > 2) fn = c == ELT_F32 ? many_kernel<OutF32>(mt, width) : c == ELT_F16 ? many_kernel<OutF16>(mt, width) : many_kernel<OutBF16>(mt, width);
     else fn = c == ELT_F32 ? few_kernel<InI8, OutF32>(true, mt, width)
               : c == ELT_F16 ? few_kernel<InI8, OutF16>(true, mt, width) : few_kernel<InI8, OutBF16>(true, mt, width);
     void* args[] = {&g};
