@@ -398,8 +398,8 @@ typedef struct {
     void* preact;           /* M x N of C's type, unit column stride, or NULL: written
                                when grad is 0 (neither C nor residual), read when it is 1
                                (may be C).  TS_Q8: rows as ts_checkpoint_pack writes them,
-                               16-byte aligned; 16-bit operands, A stored [M][K], no
-                               TS_MODE_STREAMK; written from the fp32 z                   */
+                               16-byte aligned; 16-bit operands, no TS_MODE_STREAMK;
+                               written from the fp32 z                                    */
     int64_t stride_pm;      /* elements; TS_Q8: bytes, a multiple of 16                   */
     const float* scale_a;   /* 8-bit operands: M fp32, one per row of A; NULL: 1          */
     const float* scale_b;   /* 8-bit operands: N fp32, one per column of B; NULL: 1       */
@@ -524,6 +524,8 @@ int64_t ts_rmsnorm_backward_workspace(int64_t M, int64_t N);
  * var(h) = mean((h - mean(h))^2).  As ts_rmsnorm, and: weight and bias are N contiguous elements
  * of w_dtype or NULL (1 and 0); kept (or NULL) receives h in 8 bits, as ts_checkpoint_pack writes
  * it but from the unrounded sum, stride_kept bytes a row.  kept lies on no other operand.
+ * Sums are in fp32 (here and for the gradients): a row's sum and the sum of its squared differences have
+ * to lie below 3.4e38, and with eps of 0 its variance above 1e-38.
  * TS_ERR_UNSUPPORTED (here and for everything below): N of 2^26 or more, M of 2^30 or more.
  */
 ts_status ts_layernorm(const void* x, const void* residual, const void* weight, const void* bias, void* y, void* h,
@@ -559,7 +561,7 @@ ts_status ts_quantize_rows(const void* x, void* y, float* scale, int64_t M, int6
  * a row share a step 2^e, e the least for which the largest of them is at most 127 steps (-126 at
  * least); a value is round(x / 2^e), ties to even.  A row of N columns: 32 ceil(N / 32) int8 values,
  * zero behind column N, then one byte e + 127 for each 32, or 255 where they hold an infinity or
- * a NaN: all of them then stand for NaN.  Rows are stride_kept bytes apart, a multiple of 16 and
+ * a NaN: all of them then stand for NaN, and their values are anything.  Rows are stride_kept bytes apart, a multiple of 16 and
  * at least ts_checkpoint_row_bytes(N), and 16-byte aligned; what lies behind a row's last exponent
  * is neither read nor written.
  */

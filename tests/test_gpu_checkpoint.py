@@ -141,6 +141,10 @@ def test_act_grad_with_a_16_bit_preact_gives_the_value_too():
     assert same is dcd and torch.equal(u.cpu(), z)
 
 
+def stored(t, transposed):
+    return t.t().contiguous().cuda().t() if transposed else t.cuda()
+
+
 def limit(name):
     return 1.0 if name in ("none", "relu") else R.LIP
 
@@ -151,19 +155,19 @@ PRODUCTS = [(1, 1, 1, None), (3, 40, 96, None), (17, 70, 200, None), (32, 300, 7
 
 
 @pytest.mark.parametrize("M,N,K,tile", PRODUCTS)
-@pytest.mark.parametrize("layout", ["nn", "nt"])
+@pytest.mark.parametrize("layout", ["nn", "nt", "tn", "tt"])
 @pytest.mark.parametrize("dtype,out", [(H, H), (B, B), (B, F), (H, F)])
 def test_product_keeps_its_preact(M, N, K, tile, layout, dtype, out):
     n = R.gen(M + N + K)
     a, b, bias, res = n(M, K).to(dtype), (n(K, N) / K ** 0.5).to(dtype), n(N).to(dtype), n(M, N).to(out)
-    bd = b.cuda() if layout == "nn" else b.t().contiguous().cuda().t()
+    ad, bd = stored(a, layout[0] == "t"), stored(b, layout[1] == "t")
     sched = ts.Schedule(order="auto", mode="auto", tile=tile) if tile else None
     z, zerr = R.product(a, b, bias)
     for name, r in (("gelu", None), ("silu", res), ("relu", None), ("none", res)):
         say(M, N, K, tile, layout, dtype, out, name)
         k = ts.Checkpoint.empty(M, N)
         k.data.fill_(201)
-        c = ts.gemm_epilogue(a.cuda(), bd, bias=bias.cuda(), activation=name, residual=None if r is None else r.cuda(),
+        c = ts.gemm_epilogue(ad, bd, bias=bias.cuda(), activation=name, residual=None if r is None else r.cuda(),
                              preact=k, out_dtype=out, schedule=sched)
         c64, cerr = R.forward(z, zerr, name, r, out)
         R.check(c, c64, cerr, "C")
@@ -181,43 +185,43 @@ def test_product_keeps_its_preact(M, N, K, tile, layout, dtype, out):
 
 
 @pytest.mark.parametrize("M,N,K,tile", PRODUCTS)
-@pytest.mark.parametrize("layout", ["nn", "nt"])
+@pytest.mark.parametrize("layout", ["nn", "nt", "tn", "tt"])
 @pytest.mark.parametrize("dtype", [H, B])
 def test_product_keeps_what_it_would_have_written(M, N, K, tile, layout, dtype):
     # the value before the activation in fp32, packed, is what the product keeps by itself: the same sums
     n = R.gen(M + N + 3 * K)
-    a, b, bias = n(M, K).to(dtype).cuda(), (n(K, N) / K ** 0.5).to(dtype), n(N).to(dtype).cuda()
-    bd = b.cuda() if layout == "nn" else b.t().contiguous().cuda().t()
+    a, b, bias = n(M, K).to(dtype), (n(K, N) / K ** 0.5).to(dtype), n(N).to(dtype).cuda()
+    ad, bd = stored(a, layout[0] == "t"), stored(b, layout[1] == "t")
     sched = ts.Schedule(order="auto", mode="auto", tile=tile) if tile else None
     say(M, N, K, tile, layout, dtype)
     z = torch.empty(M, N, device="cuda")
-    c = ts.gemm_epilogue(a, bd, bias=bias, activation="gelu", preact=z, out_dtype=F, schedule=sched)
+    c = ts.gemm_epilogue(ad, bd, bias=bias, activation="gelu", preact=z, out_dtype=F, schedule=sched)
     k = ts.Checkpoint.empty(M, N)
-    c8 = ts.gemm_epilogue(a, bd, bias=bias, activation="gelu", preact=k, out_dtype=F, schedule=sched)
+    c8 = ts.gemm_epilogue(ad, bd, bias=bias, activation="gelu", preact=k, out_dtype=F, schedule=sched)
     assert torch.equal(c, c8)
     K8.check_bytes(k, z.cpu().double())
 
 
 @pytest.mark.parametrize("M,N,K,tile", PRODUCTS)
 @pytest.mark.parametrize("name", ["none", "relu", "gelu", "gelu_tanh", "silu"])
-@pytest.mark.parametrize("layout,dtype", [("nn", H), ("nt", B)])
+@pytest.mark.parametrize("layout,dtype", [("nn", H), ("nt", B), ("tn", B), ("tt", H)])
 def test_gradient_epilogue_from_checkpoint(M, N, K, tile, name, layout, dtype):
     n = R.gen(M * 5 + N + K)
-    a, b, z = n(M, K).to(dtype).cuda(), (n(K, N) / K ** 0.5).to(dtype), n(M, N)
-    bd = b.cuda() if layout == "nn" else b.t().contiguous().cuda().t()
+    a, b, z = n(M, K).to(dtype), (n(K, N) / K ** 0.5).to(dtype), n(M, N)
+    ad, bd = stored(a, layout[0] == "t"), stored(b, layout[1] == "t")
     sched = ts.Schedule(order="auto", mode="auto", tile=tile) if tile else None
     k = ts.checkpoint_pack(z.cuda())
     say(M, N, K, tile, name, layout, dtype)
     for out in (dtype, F):
         z8 = ts.checkpoint_unpack(k, out_dtype=out)
-        c = ts.gemm_dact(a, bd, k, name, out=torch.empty(M, N, dtype=out, device="cuda"), schedule=sched)
+        c = ts.gemm_dact(ad, bd, k, name, out=torch.empty(M, N, dtype=out, device="cuda"), schedule=sched)
         d, derr = R.product(a, b)
         s = R.slope(K8.unpack(k.data, N), name)
         err = limit(name) * derr + (R.ACT_ERR * (z8.cpu().double().abs() + 1) if name not in ("none", "relu") else 0.0) * (d.abs() + derr)
         want = d * s
         err = err + R.U * want.abs()
         R.check(c, want, err + R.rounded(want.abs() + err, out), "C")
-    assert ts.gemm_dact(a, bd, k, name).dtype == dtype
+    assert ts.gemm_dact(ad, bd, k, name).dtype == dtype
 
 
 def test_backward_from_checkpoints():
@@ -234,6 +238,19 @@ def test_backward_from_checkpoints():
     dx, dw = ts.rmsnorm_backward(dc.cuda(), kz, torch.ones(N, dtype=B, device="cuda"))
     dx0, dw0 = ts.rmsnorm_backward(dc.cuda(), z8, torch.ones(N, dtype=B, device="cuda"))
     assert torch.equal(dx, dx0) and torch.equal(dw, dw0)
+
+
+def test_refusals_of_the_library():
+    a, b = torch.zeros(512, 512, dtype=B, device="cuda"), torch.zeros(512, 512, dtype=B, device="cuda")
+    k = ts.Checkpoint.empty(512, 512)
+    for call in (lambda: ts.gemm_epilogue(a, b, preact=k, schedule=ts.Schedule(mode="streamk", num_programs=7)),
+                 lambda: ts.gemm_scaled(a.to(torch.int8), b.to(torch.int8).t(), preact=k),
+                 lambda: ts.checkpoint_unpack(k, out_dtype=torch.int8)):
+        with pytest.raises(ts.TsError) as e:
+            call()
+        assert e.value.status in (ts.TS_ERR_UNSUPPORTED, ts.TS_ERR_INVALID_ARG) and "TS_" in str(e.value)
+    with pytest.raises(ValueError, match="same GPU"):
+        ts.checkpoint_pack(a, ts.Checkpoint.empty(512, 512, "cpu"))
 
 
 def test_captured_graph_and_streams():

@@ -116,7 +116,6 @@ KEPT = dict(preact=FAKE + (1 << 20), stride_pm=80, preact_dtype=Q8)
     (dict(epi=dict(KEPT, stride_pm=64)), INV), (dict(epi=dict(KEPT, stride_pm=88)), INV),
     (dict(epi=dict(KEPT, preact=FAKE + 8)), ALI), (dict(c=FAKE + (1 << 20), epi=KEPT), INV),
     (dict(c=FAKE + (1 << 20), epi=dict(KEPT, grad=1)), INV),
-    (dict(strides=(1, 64, 64, 1, 64, 1), epi=KEPT), UNS),                           # A stored [K][M]
     (dict(ab=I8, ct=ts.TS_BF16, strides=NT, epi=KEPT), UNS), (dict(ab=ts.TS_E4M3, ct=ts.TS_BF16, strides=NT, epi=KEPT), UNS),
     (dict(M=512, N=512, K=512, strides=(512, 1, 512, 1, 512, 1), sched=ts.Schedule(mode="streamk", num_programs=7), ws=FAKE,
           wb=1 << 24, epi=dict(KEPT, stride_pm=528)), UNS)])
@@ -160,7 +159,7 @@ def test_valid_calls_reach_the_device():
         assert epilogue(ab=I8, ct=ts.TS_BF16, strides=s, epi=epi) == DEV
     assert epilogue(ab=I8, ct=ts.TS_F32, K=(1 << 17) - 16, strides=((1 << 17) - 16, 1, 1, (1 << 17) - 16, 64, 1), ws=FAKE,
                     wb=1 << 30) == DEV
-    for s in (NT, (64, 1, 64, 1, 64, 1)):
+    for s in (NT, (64, 1, 64, 1, 64, 1), (1, 64, 64, 1, 64, 1), (1, 64, 1, 64, 64, 1)):
         for M in (4, 64):
             assert epilogue(M=M, strides=s, epi=dict(KEPT, activation=2)) == DEV
             assert epilogue(M=M, strides=s, epi=dict(KEPT, activation=2, grad=1)) == DEV
@@ -215,6 +214,21 @@ def test_python_refusals_need_no_gpu():
         for f in (ts.layernorm, ts.quantize_rows, ts.checkpoint_pack):
             with pytest.raises(ValueError, match="matrix"):
                 f(bad)
+
+
+def test_arguments_of_other_types():
+    a = torch.zeros(4, 8, dtype=torch.float16)
+    for f in (ts.layernorm, ts.rmsnorm, ts.quantize_rows, ts.checkpoint_pack):
+        with pytest.raises(TypeError, match="tensor"):
+            f("rows")
+    with pytest.raises(TypeError, match="dtype"):
+        ts.layernorm(a, out_dtype="int8")
+    with pytest.raises(TypeError, match="tensor"):
+        ts.gemm_epilogue(a, [1, 2])
+    with pytest.raises(TypeError, match="eps"):
+        ts.layernorm(a, eps="small")
+    with pytest.raises(TypeError, match="tensor"):
+        ts.act_grad(a, 3, "gelu")
 
 
 def test_struct_sizes_match_the_header():

@@ -433,7 +433,7 @@ def gemm_epilogue(a: torch.Tensor, b: torch.Tensor, bias: torch.Tensor | None = 
     ``activation``: "none", "relu", "gelu" (exact), "gelu_tanh" or "silu".  ``bias``: [N],
     fp16/bf16/fp32.  ``residual``: [M,N] of C's type (may be ``out``).  ``preact``: an [M,N]
     tensor of C's type that receives A @ B + bias, for the backward pass, or a ``Checkpoint``
-    that receives it in 8 bits (A's rows contiguous, no stream-K).  A and B may be
+    that receives it in 8 bits (no stream-K).  A and B may be
     transposed views and have any row stride; ``schedule=None`` chooses order, mode and tile.
     Enqueued on the current stream of A's device.  A 2-D product: batched or 1-D operands
     are reshaped by the caller.  The gradients: ``gemm_epilogue_backward`` (autograd does not see

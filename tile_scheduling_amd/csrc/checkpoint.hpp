@@ -33,8 +33,8 @@ __device__ __forceinline__ float step_inverse(uint32_t e) { return __builtin_bit
 __device__ __forceinline__ float step_of(uint32_t e) { return __builtin_bit_cast(float, e == 255u ? 0x7fc00000u : e << 23); }
 
 // Four values as bytes: adding 1.5 2^23 leaves the nearest whole number (ties to even) in the low
-// bits, in two's complement.  The product is exact, so this is the one rounding.  (With a factor of
-// 0 an infinity gives NaN, whose byte is 0.)
+// bits, in two's complement.  The product is exact, so this is the one rounding.  (In a block without a
+// step the bytes are anything.)
 __device__ __forceinline__ uint32_t kept_pack4(const float* x, float inv) {
     uint32_t b[4];
 #pragma unroll

@@ -1,10 +1,10 @@
-// Kernel instances with preact in 8 bits: both tiles, bf16 operands, A stored [M][K].
+// Kernel instances with preact in 8 bits: both tiles, bf16 operands; the special forms A stored [M][K].
 #include "epilogue_checkpoint.hpp"
 #include "internal.hpp"
 
 namespace ts {
 const void* epi_checkpoint_bf16(int cfg, int out_f32, int path, int fam) {
-    if (!out_f32 && fam >= 0) {
+    if (!out_f32 && fam >= 0 && (path == PATH_EDGE_BT || path == PATH_EDGE_NN)) {
         if (cfg == CFG_128)
             return path == PATH_EDGE_BT ? epi_checkpoint_special<Cfg128, InBF16, OutBF16, PATH_EDGE_BT>(fam)
                                         : epi_checkpoint_special<Cfg128, InBF16, OutBF16, PATH_EDGE_NN>(fam);

@@ -856,7 +856,7 @@ const void* epi_kernels_cfg256w8_e4m3(int out, int path, int kind);
 const void* epi_kernels_cfg128_i8(int out, int path, int kind);
 const void* epi_kernels_cfg256w8_i8(int out, int path, int kind);
 // With CheckpointStore (epilogue_checkpoint.hpp), or its special form for a family (-1: none): 16-bit
-// operands, A [M][K].
+// operands.
 const void* epi_checkpoint_f16(int cfg, int out_f32, int path, int fam);
 const void* epi_checkpoint_bf16(int cfg, int out_f32, int path, int fam);
 

@@ -210,11 +210,13 @@ int stagger_sleeps(const EpiPlan& e, bool reads) {
     return reads ? std::min(s.ks, 64) / 4 + 4 : s.ks <= 16 ? s.ks / 4 : 0;
 }
 
-// The special form of an epilogue, 0 if it has none.  They exist where the 256 tile runs (see
-// SpecialStore): one use of aux_in or aux_out at most, 16-bit operands, A stored [M][K].
 int family_of(int32_t activation) {
     return activation == TS_ACT_NONE ? FAM_NONE : activation == TS_ACT_RELU ? FAM_RELU : activation == TS_ACT_GELU ? FAM_ERF : FAM_SIGMOID;
 }
+
+// The special form of an epilogue, 0 if it has none.  They exist where the 256 tile runs (see
+// SpecialStore): one use of aux_in or aux_out at most, 16-bit operands, A stored [M][K]; int8 operands
+// with 16-bit C, plain or with residual.
 int special_kind(const ts_epilogue& x, const void* C, int64_t stride_cm, int32_t c) {
     const int fam = family_of(x.activation);
     if (!x.grad && x.residual && x.preact) return 0;
@@ -522,9 +524,8 @@ extern "C" ts_status ts_gemm_epilogue(const void* A, const void* B, void* C, int
     if (epi && (!in_place_ok(C, epi->residual, true, M, stride_cm, epi->stride_rm) ||
                 !in_place_ok(C, epi->preact, epi->preact_dtype != TS_Q8, M, stride_cm, epi->stride_pm)))
         return TS_ERR_INVALID_ARG;
-    // preact in 8 bits: the products of training, A [M][K] (dA and the forward pass)
     e.kept = epi && epi->preact && epi->preact_dtype == TS_Q8;
-    if (e.kept && (!e.a.kmaj || e.kind == EPI_STREAMK)) return TS_ERR_UNSUPPORTED;
+    if (e.kept && e.kind == EPI_STREAMK) return TS_ERR_UNSUPPORTED;
 
     const ts_epilogue plain = {};
     if (!e.kept) e.special = special_kind(epi ? *epi : plain, C, stride_cm, c_dtype);

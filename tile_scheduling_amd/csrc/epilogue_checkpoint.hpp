@@ -241,6 +241,8 @@ struct SpecialCheckpointStore {
 template <class Cfg, class TI, class TO>
 const void* epi_checkpoint(int path) {
     if (path == PATH_EDGE_BT) return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg, TI, TO, PATH_EDGE_BT, false, CheckpointStore>);
+    if (path == PATH_EDGE_AT) return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg, TI, TO, PATH_EDGE_AT, false, CheckpointStore>);
+    if (path == PATH_EDGE_ATBT) return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg, TI, TO, PATH_EDGE_ATBT, false, CheckpointStore>);
     return reinterpret_cast<const void*>(&gemm_xtile_kernel<Cfg, TI, TO, PATH_EDGE_NN, false, CheckpointStore>);
 }
 template <class Cfg, class TI, class TO, int PATH>
