@@ -36,7 +36,7 @@ __device__ __forceinline__ void keep8(uint8_t* row, int N, long long n, const fl
 // T threads a row (T <= 256: 256 / T rows a workgroup), up to C groups of eight columns a
 // thread, T * C * 8 >= N.  Weights and biases (of type W) are loaded with the row and held as they lie in
 // memory: loaded where they are used, behind the sums, each row waits for them a second time (5000 x 8192
-// with residual to e4m3 73 us, now 59).  Workgroups that walk rows, the weights in registers and the next row on
+// with residual to e4m3 75 us, now 56).  Workgroups that walk rows, the weights in registers and the next row on
 // its way, gain nothing more (58 to 62).  NORM false: y = x, rounded to 8 bits.
 template <class TX, class W, int Q, bool NORM, int T, int C>
 __global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_kernel(LayerArgs g) {
