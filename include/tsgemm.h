@@ -563,7 +563,8 @@ ts_status ts_quantize_rows(const void* x, void* y, float* scale, int64_t M, int6
  * zero behind column N, then one byte e + 127 for each 32, or 255 where they hold an infinity or
  * a NaN: all of them then stand for NaN, and their values are anything.  Rows are stride_kept bytes apart, a multiple of 16 and
  * at least ts_checkpoint_row_bytes(N), and 16-byte aligned; what lies behind a row's last exponent
- * is neither read nor written.
+ * is neither read nor written.  64 steps of 2^122, which no type holds, are read as the largest bf16 number
+ * (255 2^120), and where fp16 is written 2^16 as 65504: finite rows stay finite, within half a step.
  */
 int64_t ts_checkpoint_row_bytes(int64_t N);
 ts_status ts_checkpoint_pack(const void* x, void* kept, int64_t M, int64_t N, int64_t stride_x, int64_t stride_kept,

@@ -298,3 +298,72 @@ def test_beyond_32_bits():
     assert torch.equal(y[rows].double().cpu(), K8.unpack(k.data[rows], N))
     dz, _ = ts.act_grad(y, k, "relu", out=y, dbias=False)
     assert torch.equal(dz[rows].double().cpu(), K8.unpack(k.data[rows], N).clamp_min(0.0))
+
+
+@pytest.mark.parametrize("dtype", [H, B, F])
+@pytest.mark.parametrize("name", R.ACTS)
+def test_largest_values_of_a_type(dtype, name):
+    # from 255/256 of a power of two on a block's largest value is kept as that power, which the type does not hold
+    # where it is its last: the value that is read still lies within half a step
+    top, n = torch.finfo(dtype).max, R.gen(77)
+    low = top if dtype == B else 2.0 ** (16 if dtype == H else 128) * 255 / 256
+    x = n(9, 100).double()
+    x[0, 3], x[1, 40], x[2], x[3] = top, -top, top, -top
+    x[4], x[5] = torch.linspace(-1, 1, 100) * top, torch.linspace(1, -1, 100) * low
+    x[6, 99], x[7, 0], x[8, 64:] = low, -low, torch.linspace(low, top, 36)
+    x = x.to(dtype)
+    dc = n(9, 100).to(dtype)
+    assert bool(x.isfinite().all())
+    k = ts.checkpoint_pack(x.cuda())
+    K8.check_bytes(k, x.double())
+    half = 0.5 * K8.steps(x)[2].repeat_interleave(32, 1)[:, :100]
+    say(dtype, name)
+    for out in (dtype, F):
+        v = ts.checkpoint_unpack(k, out_dtype=out).cpu().double()
+        assert bool(((v - x.double()).abs() <= half + R.rounded(v, dtype) * (out == H)).all())
+    z = ts.checkpoint_unpack(k, out_dtype=dtype).cpu().double()
+    want, err = R.forward(z, torch.zeros_like(z), name, None, dtype)
+    R.check(ts.checkpoint_unpack(k, name, out_dtype=dtype), want, err, "value")
+    u = torch.empty(9, 100, dtype=dtype, device="cuda")
+    dz, _ = ts.act_grad(dc.cuda(), k, name, act_out=u, dbias=False)
+    R.check(u, want, err, "u")
+    s = R.slope(z, name)
+    # the slopes of these values are 0 or 1, but for the block's small ones
+    serr = R.ACT_ERR * (z.abs().clamp_max(64.0) + 1) if name not in ("none", "relu") else 0.0
+    bound = (serr + R.U * s.abs()) * dc.double().abs()
+    R.check(dz, dc.double() * s, bound + R.rounded((dc.double() * s).abs() + bound, dtype), "dz")
+    # the products that read a checkpoint: few rows, tiles (rows repeated), K split
+    eye = torch.eye(9).to(B if dtype == F else dtype)
+    for rows, K, tile in ((9, 9, None), (180, 9, "128x128x64"), (612, 9, "256x256x64w8"), (180, 4096, None)):
+        a = torch.zeros(rows, K, dtype=eye.dtype)
+        a[:, :9] = eye.repeat(rows // 9, 1)
+        b = torch.zeros(K, 100, dtype=eye.dtype)
+        b[:9] = dc.to(eye.dtype)[:, :100]
+        sched = ts.Schedule(order="auto", mode="auto", tile=tile) if tile else None
+        kk = ts.Checkpoint(k.data.repeat(rows // 9, 1), 100)
+        c = ts.gemm_dact(a.cuda(), b.cuda(), kk, name, out=torch.empty(rows, 100, device="cuda"), schedule=sched)
+        d = b[:9].double().repeat(rows // 9, 1)
+        zz, ss = z.repeat(rows // 9, 1), s.repeat(rows // 9, 1)
+        serr = R.ACT_ERR * (zz.abs().clamp_max(64.0) + 1) if name not in ("none", "relu") else 0.0
+        R.check(c, d * ss, (serr + 2 * R.U * ss.abs()) * d.abs() + R.TINY[F], f"gradient {rows} {K}")
+
+
+def test_gradients_from_the_largest_values_of_fp16():
+    g = torch.Generator().manual_seed(5)
+    M, N, K = 40, 96, 64
+    x = 65280.0 + 32.0 * torch.randint(0, 8, (M, N), generator=g)
+    x = (x * (1 - 2 * torch.randint(0, 2, (M, N), generator=g))).to(H)
+    n = R.gen(6)
+    dy, w, b = n(M, N).to(H), (1 + 0.2 * n(N)).to(H), (n(N, K) / N).to(H)
+    k = ts.checkpoint_pack(x.cuda())
+    x8 = ts.checkpoint_unpack(k, out_dtype=H)
+    assert bool(((x8.cpu().double() - x.double()).abs() <= 512.0).all())
+    dx, dw = ts.rmsnorm_backward(dy.cuda(), k, w.cuda())
+    dx0, dw0 = ts.rmsnorm_backward(dy.cuda(), x8, w.cuda())
+    assert bool(dx.isfinite().all()) and bool(dw.isfinite().all()) and torch.equal(dx, dx0) and torch.equal(dw, dw0)
+    assert all(bool(t.isfinite().all()) for t in ts.layernorm_backward(dy.cuda(), k, w.cuda()))
+    dc = (1e-4 * n(M, K)).to(H)
+    da, db, _ = ts.gemm_epilogue_backward(dc.cuda(), k, b.cuda(), dbias=False)
+    want = x8.cpu().double().t() @ dc.double()
+    err = (M + 4) * R.U * (x8.cpu().double().abs().t() @ dc.double().abs())
+    R.check(db, want, err + R.rounded(want.abs() + err, H), "dB")

@@ -367,7 +367,8 @@ class Checkpoint:
     32 neighbours of a row share one step 2^e, the least for which the largest of them is at most
     127 steps; a value is a whole number of steps (int8), off by at most half a step.  A row of ``data``:
     32 ceil(N / 32) values, then a byte e + 127 for each 32; 255: they held an infinity or a NaN, and
-    all of them stand for NaN.  ``checkpoint_pack``, ``layernorm`` and the product (``preact``) write
+    all of them stand for NaN.  A finite value is read as a finite one of its own type (2^128 as the largest
+    bf16 number, in fp16 2^16 as 65504).  ``checkpoint_pack``, ``layernorm`` and the product (``preact``) write
     it; ``checkpoint_unpack``, ``act_grad``, ``gemm_dact``, the products' and the norms' gradients read it.
     Its rows are ``data``'s: a slice of those is a checkpoint of the same rows.
     """
@@ -601,5 +602,6 @@ def checkpoint_unpack(kept: Checkpoint, activation: str = "none", out: torch.Ten
                       out_dtype: torch.dtype | None = None) -> torch.Tensor:
     """act(value) of what a ``Checkpoint`` keeps, in ``out`` or a new tensor of ``out_dtype`` (fp32).
 
-    The values themselves are exact in bf16 and fp32 (8 significant bits)."""
+    The values themselves are exact in bf16 and fp32 (8 significant bits); in fp16 those beyond 2^16 are
+    infinite."""
     return _binding.checkpoint_unpack(kept.data, kept.n, _activation(activation), out, out_dtype)

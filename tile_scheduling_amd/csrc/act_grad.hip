@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(ActGradArgs g) {
                 if constexpr (KEPT) {
                     Kept8 k;
                     k.load(static_cast<const uint8_t*>(g.z) + m * g.ldz, kept_values(g.N), n, true);
-                    k.unpack(z);
+                    k.unpack<std::is_same<TO, OutF16>::value>(z);
                 } else {
                     load8<TI>(static_cast<const I*>(g.z) + m * g.ldz + n, valid, z);
                 }

@@ -42,9 +42,25 @@ __device__ __forceinline__ uint32_t kept_pack4(const float* x, float inv) {
     const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
     return lo | hi;
 }
+// A block whose largest value lies between 255/256 of a power of two and the power keeps it as the power,
+// 64 steps, which its type does not hold where it is the type's last: 2^128 of bf16 and fp32, 2^16 of fp16.  2^128
+// is read as the largest bf16 number, that border itself and a quarter of a step below, and by kernels that write fp16
+// (F16) 2^16 as the largest fp16 number: finite rows come back finite, within half a step.
+constexpr float kLastStep = 0x1p122f, kLastValue = 0x1.fep127f, kLastStepF16 = 0x1p10f, kLastValueF16 = 65504.0f;
+template <int E, bool F16>
+__device__ __forceinline__ void kept_last(float step, float* v) {
+    if (step == kLastStep || (F16 && step == kLastStepF16)) {
+        const bool f16 = step != kLastStep;
+        const float power = f16 ? 0x1p16f : __builtin_inff(), last = f16 ? kLastValueF16 : kLastValue;
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = __builtin_fabsf(v[i]) == power ? __builtin_copysignf(last, v[i]) : v[i];
+    }
+}
+template <bool F16 = false>
 __device__ __forceinline__ void kept_unpack4(uint32_t w, float step, float* v) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(w >> (8 * i)) * step;
+    kept_last<4, F16>(step, v);
 }
 // Largest over lanes l, l ^ 1, l ^ 2, l ^ 3.
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
@@ -73,10 +89,11 @@ struct Kept8 {
             e = row[values + n / kBlock];
         }
     }
+    template <bool F16 = false>
     __device__ __forceinline__ void unpack(float* v) const {
         const float step = step_of(e);
-        kept_unpack4(w[0], step, v);
-        kept_unpack4(w[1], step, v + 4);
+        kept_unpack4<F16>(w[0], step, v);
+        kept_unpack4<F16>(w[1], step, v + 4);
     }
 };
 

@@ -99,7 +99,9 @@ __device__ __forceinline__ void finish_element(const FewArgs& g, float v, int m,
     float in = g.aux_in ? (float)static_cast<const T*>(g.aux_in)[m * g.ld_in + n] : 0.0f;
     if (KEPT && g.grad) {
         const uint8_t* row = g.kept + m * g.ld_kept;
-        in = (float)(int8_t)row[n] * step_of(row[kept_values(g.N) + n / kBlock]);
+        const float step = step_of(row[kept_values(g.N) + n / kBlock]);
+        in = (float)(int8_t)row[n] * step;
+        kept_last<1, false>(step, &in);
     }
     if (g.grad) {
         act_slopes<1>(g.act, &v, &in);
