@@ -270,3 +270,30 @@ def test_block_in_8_bits_captured_and_on_two_streams():
         torch.cuda.synchronize()
         assert torch.equal(again, want)
         block()
+
+
+@pytest.mark.parametrize("N,K", [(300, 2048), (530, 2051), (1100, 4096), (1100, 4001)])
+@pytest.mark.parametrize("out", [H, B, F])
+def test_every_row_count_gives_the_same_bits(N, K, out):
+    # a row's result does not depend on the rows beside it: one pass over B (up to 32, 64 or 128 rows), K split among
+    # programs (from there on) and both tiles round every term alike
+    M = 600
+    n = R.gen(N + K)
+    a, b, sa, sb = codes(21, M, K).cuda(), codes(22, N, K).cuda(), (0.01 * (1 + n(M).abs())).cuda(), ((1 + n(N).abs()) / K).cuda()
+    bias, res = n(N).cuda(), n(M, N).to(out).cuda()
+    tile = lambda t: ts.Schedule(order="auto", mode="auto", tile=t)
+    for name, bi, r, s1, s2 in (("none", None, None, sa, sb), ("none", bias, None, sa, None), ("none", bias, res, None, sb),
+                                ("relu", bias, res, sa, sb), ("gelu", bias, None, sa, sb), ("gelu", bias, res, sa, sb),
+                                ("silu", bias, res, sa, sb), ("gelu_tanh", bias, res, sa, sb)):
+        def product(rows, schedule=None, pre=None):
+            return ts.gemm_scaled(a[:rows], b.t(), None if s1 is None else s1[:rows], s2, bias=bi, activation=name,
+                                  residual=None if r is None else r[:rows], preact=pre, out_dtype=out, schedule=schedule)
+
+        pre = torch.empty(M, N, dtype=out, device="cuda")
+        want = product(M, tile("128x128x64"))
+        say(N, K, out, name, r is not None)
+        assert torch.equal(product(M, tile("256x256x64w8")), want) and torch.equal(product(M, tile("128x128x64"), pre), want)
+        for rows in (1, 5, 17, 33, 64, 65, 128, 129, 200, 300):
+            p = torch.empty(rows, N, dtype=out, device="cuda")
+            assert torch.equal(product(rows), want[:rows]), rows
+            assert torch.equal(product(rows, None, p), want[:rows]) and torch.equal(p, pre[:rows]), rows

@@ -114,6 +114,46 @@ __device__ __forceinline__ void act_slopes(int act, float* v, const float* z) {
     });
 }
 
+// ---- int8 products -----------------------------------------------------------------------
+//
+// Their sums are exact, so with every later term rounded on its own, and in the same order, all schedules, K
+// splits, row counts and tiles (inside C and on its edge) give the same bits: z is one product and one fused
+// multiply-add, a missing scale 1 and a missing bias 0.  Left to itself the compiler joins terms where it sees them
+// in one piece of code: gelu's 1 - q, z gate + residual, what comes last with the conversion to fp16.
+__device__ __forceinline__ float scaled_apart(float sum, float scale_a, float scale_b, float bias) {
+    float z = __builtin_fmaf(sum * scale_a, scale_b, bias);
+    asm("" : "+v"(z));
+    return z;
+}
+// fam_value of such a z.
+template <int FAM>
+__device__ __forceinline__ float value_apart(float z, Sigmoid coeff) {
+    if constexpr (FAM == FAM_ERF) {
+#pragma clang fp contract(off)
+        const float q = tail_scaled(__builtin_fabsf(z)) * __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z);
+        const float r = 1.0f - q;
+        z = z * (z < 0.0f ? q : r);
+    } else {
+        z = fam_value<FAM>(z, coeff);
+    }
+    asm("" : "+v"(z));
+    return z;
+}
+template <int E>
+__device__ __forceinline__ void values_apart(int act, float* v) {
+    const Sigmoid c = sigmoid_of(act);
+    with_family(act, [&](auto fam) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = value_apart<decltype(fam)::value>(v[e], c);
+    });
+}
+__device__ __forceinline__ float sum_apart(float a, float b) {
+#pragma clang fp contract(off)
+    float s = a + b;
+    asm("" : "+v"(s));
+    return s;
+}
+
 // ---- rows of C's type, any alignment -----------------------------------------------------
 
 // 16 bytes at the alignment of their elements: global accesses of gfx950 need no more
@@ -491,7 +531,9 @@ struct FusedStore {
 #pragma unroll
                         for (int q = 0; q < NQ; ++q)
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) v[q][c] = fam_value<decltype(fam)::value>(v[q][c], coeff);
+                            for (int c = 0; c < 4; ++c)
+                                v[q][c] = E::INTS ? value_apart<decltype(fam)::value>(v[q][c], coeff)
+                                                  : fam_value<decltype(fam)::value>(v[q][c], coeff);
                     });
                 if (read) {
                     float w[NQ][4];
@@ -518,7 +560,7 @@ struct FusedStore {
 #pragma unroll
                         for (int q = 0; q < NQ; ++q)
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) v[q][c] += w[q][c];
+                            for (int c = 0; c < 4; ++c) v[q][c] = E::INTS ? sum_apart(v[q][c], w[q][c]) : v[q][c] + w[q][c];
                     }
                 }
 #pragma unroll

@@ -7,31 +7,6 @@
 
 namespace ts {
 
-// fam_value and the residual's sum with every term rounded on its own, as FusedStore's branches leave them.
-// In straight code the compiler joins gelu's 1 - q and z gate + residual to fused multiply-adds, and what comes
-// last with the conversion to fp16; every sum of int8 products is exact, so without that all schedules, and
-// tiles on the edge, give the same bits.
-template <int FAM>
-__device__ __forceinline__ float value_apart(float z, Sigmoid coeff) {
-    asm("" : "+v"(z));
-    if constexpr (FAM == FAM_ERF) {
-#pragma clang fp contract(off)
-        const float q = tail_scaled(__builtin_fabsf(z)) * __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z);
-        const float r = 1.0f - q;
-        z = z * (z < 0.0f ? q : r);
-    } else {
-        z = fam_value<FAM>(z, coeff);
-    }
-    asm("" : "+v"(z));
-    return z;
-}
-__device__ __forceinline__ float sum_apart(float a, float b) {
-#pragma clang fp contract(off)
-    float s = a + b;
-    asm("" : "+v"(s));
-    return s;
-}
-
 // The scales and biases of a lane's 32 columns are held in registers (64) and z is formed where it is used:
 // accumulators that are changed in place spill 80 to 300 registers.  (With the rows of a residual ahead 18 to
 // 55 are, none inside the K loop.)  Against FusedStore, bf16 C, with bias, us: 4096 x 16384 x 4096 none 237 / 252, silu
@@ -86,7 +61,7 @@ struct SpecialInt8Store {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const float sum = e.acc[i][x / NQ][4 * (x % NQ) + c];   // (a bit cast of the vector's element takes its first)
-                    v[c] = value_apart<FAM>(__builtin_fmaf((float)__builtin_bit_cast(int, sum) * sa[i], sb[x][c], bias[x][c]), coeff);
+                    v[c] = value_apart<FAM>(scaled_apart((float)__builtin_bit_cast(int, sum), sa[i], sb[x][c], bias[x][c]), coeff);
                 }
                 if constexpr (RESIDUAL) {
                     float f[8];

@@ -85,15 +85,19 @@ __device__ __forceinline__ u32x4 load16_left(const uint8_t* p, long long left, l
     return v;
 }
 
-// z of an element from its fp32 sum.
+// z of an element from its fp32 sum; INTS: one of int8 products, rounded as on tiles (scaled_apart).
+template <bool INTS>
 __device__ __forceinline__ float scaled_element(const FewArgs& g, float v, int m, long long n) {
+    if constexpr (INTS)
+        return scaled_apart(v, g.scale_a ? g.scale_a[m] : 1.0f, g.scale_b ? g.scale_b[n] : 1.0f,
+                            g.bias ? load_any(g.bias, g.bias_type, n) : 0.0f);
     if (g.scale_a) v *= g.scale_a[m];
     if (g.scale_b) v *= g.scale_b[n];
     if (g.bias) v += load_any(g.bias, g.bias_type, n);
     return v;
 }
 // One element of C from its z.
-template <class TO, bool KEPT>
+template <class TO, bool KEPT, bool INTS>
 __device__ __forceinline__ void finish_element(const FewArgs& g, float v, int m, long long n) {
     typedef typename Elt<TO>::T T;
     float in = g.aux_in ? (float)static_cast<const T*>(g.aux_in)[m * g.ld_in + n] : 0.0f;
@@ -107,8 +111,13 @@ __device__ __forceinline__ void finish_element(const FewArgs& g, float v, int m,
         act_slopes<1>(g.act, &v, &in);
     } else {
         if (g.aux_out) static_cast<T*>(g.aux_out)[m * g.ld_out + n] = (T)v;
-        act_values<1>(g.act, &v);
-        v += in;
+        if constexpr (INTS) {
+            values_apart<1>(g.act, &v);
+            if (g.aux_in) v = sum_apart(v, in);
+        } else {
+            act_values<1>(g.act, &v);
+            v += in;
+        }
     }
     static_cast<T*>(g.C)[m * g.ldc + n] = (T)v;
 }
@@ -142,16 +151,16 @@ __device__ __forceinline__ void meet_and_finish(const FewArgs& g, const f32x4 (*
         if (KEPT && !g.grad) {
             // 32 neighbouring lanes hold a block of a row (the launch takes at least 32 columns a
             // workgroup, and whole waves are here or not)
-            v = in ? scaled_element(g, v, m, n) : 0.0f;
+            v = in ? scaled_element<INTS>(g, v, m, n) : 0.0f;
             const uint32_t ex = block_exponent(lanes_max<32>(__builtin_bit_cast(uint32_t, v) & 0x7fffffffu));
             if (m < g.M && n < kept_values(g.N)) {
                 uint8_t* row = g.kept + m * g.ld_kept;
                 row[n] = (uint8_t)__builtin_bit_cast(uint32_t, __builtin_fmaf(v, step_inverse(ex), 12582912.0f));
                 if (n % kBlock == 0) row[kept_values(g.N) + n / kBlock] = (uint8_t)ex;
             }
-            if (in) finish_element<TO, KEPT>(g, v, m, n);
+            if (in) finish_element<TO, KEPT, INTS>(g, v, m, n);
         } else if (in) {
-            finish_element<TO, KEPT>(g, scaled_element(g, v, m, n), m, n);
+            finish_element<TO, KEPT, INTS>(g, scaled_element<INTS>(g, v, m, n), m, n);
         }
     }
 }

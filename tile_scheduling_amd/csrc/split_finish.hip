@@ -35,22 +35,27 @@ __global__ void __launch_bounds__(256) split_finish_kernel(SplitArgs g) {
         }
     }
     float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-    if constexpr (INTS) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = (float)__builtin_bit_cast(int, v[e]);
-    }
-    if (g.scale_a || g.scale_b) {
-        const float sa = g.scale_a ? g.scale_a[m] : 1.0f;
-        float sb[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+    if constexpr (INTS) {   // rounded as on tiles
+        float sa = 1.0f, sb[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f}, bias[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (g.scale_a) sa = g.scale_a[m];
         if (g.scale_b) load8<OutF32>(g.scale_b + n, valid, sb);
+        if (g.bias) load_columns<8>(g.bias, g.bias_type, n, valid, bias);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = v[e] * sa * sb[e];
-    }
-    if (g.bias) {
-        float bias[8];
-        load_columns<8>(g.bias, g.bias_type, n, valid, bias);
+        for (int e = 0; e < 8; ++e) v[e] = scaled_apart((float)__builtin_bit_cast(int, v[e]), sa, sb[e], bias[e]);
+    } else {
+        if (g.scale_a || g.scale_b) {
+            const float sa = g.scale_a ? g.scale_a[m] : 1.0f;
+            float sb[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+            if (g.scale_b) load8<OutF32>(g.scale_b + n, valid, sb);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += e < valid ? bias[e] : 0.0f;
+            for (int e = 0; e < 8; ++e) v[e] = v[e] * sa * sb[e];
+        }
+        if (g.bias) {
+            float bias[8];
+            load_columns<8>(g.bias, g.bias_type, n, valid, bias);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += e < valid ? bias[e] : 0.0f;
+        }
     }
     uint8_t* kept = KEPT ? g.kept + m * g.ld_kept : nullptr;
     if (KEPT && !g.grad) {
@@ -79,10 +84,11 @@ __global__ void __launch_bounds__(256) split_finish_kernel(SplitArgs g) {
     if (g.grad) {
         act_slopes<8>(g.act, v, w);
     } else {
-        act_values<8>(g.act, v);
+        if constexpr (INTS) values_apart<8>(g.act, v);
+        else act_values<8>(g.act, v);
         if (g.aux_in) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += w[e];
+            for (int e = 0; e < 8; ++e) v[e] = INTS ? sum_apart(v[e], w[e]) : v[e] + w[e];
         }
     }
     store8<TO>(static_cast<T*>(g.C) + m * g.ldc + n, valid, v);
