@@ -340,3 +340,55 @@ def test_layer_forward_and_backward_together():
         # chains of up to six roundings to bf16 (2^-8 at most, 2^-8 / sqrt(3) in the mean square), each carried on with a
         # factor of about one: under 2 % of the output's norm
         assert float((d(got[name]) - t).norm() / t.norm()) < 0.02, name
+
+
+# Rows whose mean is thousands of deviations.  x - mean is exact there (the two are within a factor of two of each
+# other), so what is left of the mean's rounding is the error of its correction, the mean of those differences.
+# A sum here is at most DEEP additions deep: up to 40 of a thread's own, then the exchanges between threads.
+DEEP = 64
+
+
+def far_stats(h, eps):
+    """As stats, for such rows; the mean is off by less than 2^-6 before its correction (DEEP roundings of 2^13)."""
+    c = h - h.mean(1, keepdim=True)
+    r = 1.0 / torch.sqrt((c * c).mean(1, keepdim=True) + eps)
+    cerr = (DEEP + 4) * U * (c.abs() + c.abs().mean(1, keepdim=True) + 2.0 ** -6)
+    rerr = (DEEP + 16) * U
+    return c * r, r, cerr * r + (c * r).abs() * (rerr + 2 * U), rerr
+
+
+def far_rows(M, N):
+    n = R.gen(M + 5 * N)
+    return n(M, N) + 4096.0 + 100.0 * n(M, 1), n
+
+
+@pytest.mark.parametrize("N", [200, 3000, 16384, 40000])
+def test_mean_far_from_zero(N):
+    h, n = far_rows(32, N)
+    w, b = 1 + 0.2 * n(N), 0.3 * n(N)
+    y, _, _ = ts.layernorm(h.cuda(), w.cuda(), b.cuda())
+    u, _, uerr, _ = far_stats(h.double(), 1e-5)
+    want = u * w.double() + b.double()
+    R.check(y, want, uerr * w.double().abs() + 3 * U * ((u * w.double()).abs() + want.abs()), "y")
+
+
+@pytest.mark.parametrize("N", [200, 3000, 12000, 16384, 20000, 40000])
+def test_backward_mean_far_from_zero(N):
+    h, n = far_rows(16, N)
+    u, r, uerr, rerr = far_stats(h.double(), 1e-5)
+    w = 1 + 0.2 * n(N)
+    # dy along u, so that mean(g u) is about one and u's error reaches dx
+    dy = (u + 0.2 * n(16, N)).float()
+    dx, dw, db = ts.layernorm_backward(dy.cuda(), h.cuda(), w.cuda())
+    mean = lambda t: t.mean(1, keepdim=True)
+    y64 = dy.double()
+    g = w.double() * y64
+    mg, mgu = mean(g), mean(g * u)
+    want = r * (g - mg - u * mgu)
+    mguerr = (2 * DEEP + 16) * U * (mean((g * u).abs()) + mean(g.abs()))
+    err = (r * ((g.abs() + mg.abs() + (u * mgu).abs()) * (rerr + 6 * U) + DEEP * U * mean(g.abs()) + uerr * (mgu.abs() + mguerr)
+                + (u.abs() + uerr) * mguerr) + 4 * U * want.abs())
+    R.check(dx, want, err + R.rounded(want.abs() + err, F), "dx")
+    wd, derr = (y64 * u).sum(0), (y64.abs() * uerr).sum(0) + 20 * U * (y64 * u).abs().sum(0)
+    R.check(dw, wd, derr + R.rounded(wd.abs() + derr, F), "dweight")
+    R.check(db, y64.sum(0), 20 * U * y64.abs().sum(0) + R.TINY[F], "dbias")

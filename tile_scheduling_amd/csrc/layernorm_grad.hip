@@ -13,7 +13,7 @@ struct LayerGradArgs {
     const void *dy, *h, *weight, *dh;
     void* dx;
     float* part;    // partial sums, one row of N of dw and one of db per workgroup, or null
-    float* stats;   // long rows: mean, r, r mean(g) and r mean(g u) of every row
+    float* stats;   // long rows: mean, its correction and r of every row, and a place left over
     int M, N, w_type;
     long long ldy, ldh, lds, ldx;   // (h in 8 bits: ldh in bytes)
     float eps;
@@ -84,7 +84,8 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_grad_kernel(Layer
             }
         }
         row_sums<T, 2>(a, lds1);
-        const float mean = a[0] * rn;
+        float mean = a[0] * rn;
+        asm("" : "+v"(mean));   // one number for all its uses, not a product joined to some of them
         float b[3] = {0.0f, 0.0f, 0.0f};   // sums of d, d^2 and g d
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -111,7 +112,6 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_grad_kernel(Layer
         const float r = inverse_deviation(b[0], b[1], (float)g.N, g.eps), off = b[0] * rn;
         const float k1 = r * (a[1] * rn);
         const float k2 = r * (r * (__builtin_fmaf(-off, a[1], b[2]) * rn));
-        const float center = mean + off;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int n = (c * T + t) * 8, valid = g.N - n;
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_grad_kernel(Layer
             dy[c].unpack(y, valid);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float unit = (x[e] - center) * r;
+                const float unit = ((x[e] - mean) - off) * r;   // (mean + off rounds the correction away)
                 dw[c][e] = __builtin_fmaf(y[e], unit, dw[c][e]);
                 db[c][e] += y[e];
                 d[e] = __builtin_fmaf(-unit, k2, __builtin_fmaf(r * w[c][e], y[e], -k1));
@@ -171,48 +171,39 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) layernorm_grad_kernel(Layer
     }
 }
 
-// Long rows, in three steps: the four numbers of each row, the partial sums of dw and db by strips
-// of columns, and dx element by element (last: dx may take the place of dy or dh).
+// Long rows, in three steps: mean and deviation of each row, the partial sums of dw and db by strips of columns,
+// and dx by rows (last: dx may take the place of dy or dh), whose first pass sums g and g d.
 template <class TX, bool HK>
 __global__ void __launch_bounds__(kLongThreads) layernorm_grad_stats_kernel(LayerGradArgs g) {
-    __shared__ float lds1[kLongThreads / 64][2], lds2[kLongThreads / 64][3];
+    __shared__ float lds1[kLongThreads / 64][1], lds2[kLongThreads / 64][2];
     const long long m = g.first + blockIdx.x;
     const float rn = 1.0f / (float)g.N;
     auto each = [&](auto&& f) {
         for (long long n = threadIdx.x * 8; n < g.N; n += kLongThreads * 8) {
             const int valid = (int)std::min<long long>(g.N - n, 8);
             HRow<TX, HK> h;
-            Raw8<TX> dy;
-            float x[8], y[8], w[8];
+            float x[8];
             h.load(g.h, m, g.ldh, n, g.N, valid);
-            dy.load(g.dy, m, g.ldy, n, g.N, valid);
             h.unpack(x, valid);
-            dy.unpack(y, valid);
-            columns8<TX>(g.weight, g.w_type, n, valid, 1.0f, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f(x[e], w[e] * y[e], e < valid);
+            for (int e = 0; e < 8; ++e) f(x[e], e < valid);
         }
     };
-    float a[2] = {0.0f, 0.0f}, b[3] = {0.0f, 0.0f, 0.0f};
-    each([&](float x, float gy, bool) {
-        a[0] += x;
-        a[1] += gy;
-    });
-    row_sums<kLongThreads, 2>(a, lds1);
-    const float mean = a[0] * rn;
-    each([&](float x, float gy, bool in) {
+    float a[1] = {0.0f}, b[2] = {0.0f, 0.0f};
+    each([&](float x, bool) { a[0] += x; });
+    row_sums<kLongThreads, 1>(a, lds1);
+    float mean = a[0] * rn;
+    asm("" : "+v"(mean));   // the number that is stored
+    each([&](float x, bool in) {
         const float d = in ? x - mean : 0.0f;
         b[0] += d;
         b[1] = __builtin_fmaf(d, d, b[1]);
-        b[2] = __builtin_fmaf(gy, d, b[2]);
     });
-    row_sums<kLongThreads, 3>(b, lds2);
+    row_sums<kLongThreads, 2>(b, lds2);
     if (threadIdx.x == 0) {
-        const float r = inverse_deviation(b[0], b[1], (float)g.N, g.eps), off = b[0] * rn;
-        g.stats[4 * m] = mean + off;
-        g.stats[4 * m + 1] = r;
-        g.stats[4 * m + 2] = r * (a[1] * rn);
-        g.stats[4 * m + 3] = r * (r * (__builtin_fmaf(-off, a[1], b[2]) * rn));
+        g.stats[4 * m] = mean;
+        g.stats[4 * m + 1] = b[0] * rn;
+        g.stats[4 * m + 2] = inverse_deviation(b[0], b[1], (float)g.N, g.eps);
     }
 }
 // 256 threads: 64 strips of eight columns x 4 rows; blockIdx.y is the row group.
@@ -234,10 +225,10 @@ __global__ void __launch_bounds__(256) layernorm_grad_columns_kernel(LayerGradAr
             dy.load(g.dy, m, g.ldy, n, g.N, valid);
             h.unpack(x, valid);
             dy.unpack(y, valid);
-            const float mean = g.stats[4 * m], r = g.stats[4 * m + 1];
+            const float mean = g.stats[4 * m], off = g.stats[4 * m + 1], r = g.stats[4 * m + 2];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                s[e] = __builtin_fmaf(y[e], (x[e] - mean) * r, s[e]);
+                s[e] = __builtin_fmaf(y[e], ((x[e] - mean) - off) * r, s[e]);
                 s[8 + e] += y[e];
             }
         }
@@ -258,8 +249,28 @@ __global__ void __launch_bounds__(256) layernorm_grad_columns_kernel(LayerGradAr
 template <class TX, bool HK>
 __global__ void __launch_bounds__(kLongThreads) layernorm_grad_dx_kernel(LayerGradArgs g) {
     typedef typename Elt<TX>::T X;
+    __shared__ float lds[kLongThreads / 64][2];
     const long long m = g.first + blockIdx.x;
-    const float mean = g.stats[4 * m], r = g.stats[4 * m + 1], k1 = g.stats[4 * m + 2], k2 = g.stats[4 * m + 3];
+    const float mean = g.stats[4 * m], off = g.stats[4 * m + 1], r = g.stats[4 * m + 2], rn = 1.0f / (float)g.N;
+    float s[2] = {0.0f, 0.0f};   // sums of g and g d
+    for (long long n = threadIdx.x * 8; n < g.N; n += kLongThreads * 8) {
+        const int valid = (int)std::min<long long>(g.N - n, 8);
+        HRow<TX, HK> h;
+        Raw8<TX> dy;
+        float x[8], y[8], w[8];
+        h.load(g.h, m, g.ldh, n, g.N, valid);
+        dy.load(g.dy, m, g.ldy, n, g.N, valid);
+        h.unpack(x, valid);
+        dy.unpack(y, valid);
+        columns8<TX>(g.weight, g.w_type, n, valid, 1.0f, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            s[0] = __builtin_fmaf(w[e], y[e], s[0]);
+            s[1] = __builtin_fmaf(w[e] * y[e], e < valid ? (x[e] - mean) - off : 0.0f, s[1]);
+        }
+    }
+    row_sums<kLongThreads, 2>(s, lds);
+    const float k1 = r * (s[0] * rn), k2 = r * (r * (s[1] * rn));
     for (long long n = threadIdx.x * 8; n < g.N; n += kLongThreads * 8) {
         const int valid = (int)std::min<long long>(g.N - n, 8);
         HRow<TX, HK> h;
@@ -274,7 +285,7 @@ __global__ void __launch_bounds__(kLongThreads) layernorm_grad_dx_kernel(LayerGr
         for (int e = 0; e < 8; ++e) a[e] = 0.0f;
         if (g.dh) load8<TX>(static_cast<const X*>(g.dh) + m * g.lds + n, valid, a);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] += __builtin_fmaf(-((x[e] - mean) * r), k2, __builtin_fmaf(r * w[e], y[e], -k1));
+        for (int e = 0; e < 8; ++e) a[e] += __builtin_fmaf(-(((x[e] - mean) - off) * r), k2, __builtin_fmaf(r * w[e], y[e], -k1));
         store8<TX>(static_cast<X*>(g.dx) + m * g.ldx + n, valid, a);
     }
 }
@@ -336,7 +347,7 @@ ts_status grad_sizes(int64_t M, int64_t N) {
 
 using namespace ts;
 
-// Bytes: the partial sums of dw and db, then (long rows) four numbers per row.
+// Bytes: the partial sums of dw and db, then (long rows) four fp32 per row.
 extern "C" int64_t ts_layernorm_backward_workspace(int64_t M, int64_t N) {
     ts_status st = grad_sizes(M, N);
     if (st != TS_OK) return st;
