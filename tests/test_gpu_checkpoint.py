@@ -367,3 +367,21 @@ def test_gradients_from_the_largest_values_of_fp16():
     want = x8.cpu().double().t() @ dc.double()
     err = (M + 4) * R.U * (x8.cpu().double().abs().t() @ dc.double().abs())
     R.check(db, want, err + R.rounded(want.abs() + err, H), "dB")
+
+
+@pytest.mark.parametrize("M,N,K,tile", PRODUCTS)
+@pytest.mark.parametrize("layout", ["nn", "nt", "tn", "tt"])
+@pytest.mark.parametrize("dtype", [H, B])
+def test_16_bit_products_keep_the_same_bytes(M, N, K, tile, layout, dtype):
+    # the straight forms of 16-bit C for each activation keep what the general form of fp32 C keeps
+    n = R.gen(M + 2 * N + K)
+    a, b, bias = n(M, K).to(dtype), (n(K, N) / K ** 0.5).to(dtype), n(N).to(dtype).cuda()
+    ad, bd = stored(a, layout[0] == "t"), stored(b, layout[1] == "t")
+    sched = ts.Schedule(order="auto", mode="auto", tile=tile) if tile else None
+    nb = -(-N // 32)
+    for name in R.ACTS:
+        say(M, N, K, tile, layout, dtype, name)
+        k, k32 = ts.Checkpoint.empty(M, N), ts.Checkpoint.empty(M, N)
+        ts.gemm_epilogue(ad, bd, bias=bias, activation=name, preact=k, schedule=sched)
+        ts.gemm_epilogue(ad, bd, bias=bias, activation=name, preact=k32, out_dtype=F, schedule=sched)
+        assert torch.equal(k.data[:, :33 * nb], k32.data[:, :33 * nb])
