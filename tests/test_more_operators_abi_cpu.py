@@ -233,3 +233,17 @@ def test_arguments_of_other_types():
 
 def test_struct_sizes_match_the_header():
     assert ctypes.sizeof(ts._Epilogue) == 4 * 4 + 7 * 8   # four int32, seven pointers and strides
+
+
+def test_arguments_without_a_truth():
+    # the caller's own error comes back, before anything else happens
+    class Unsure:
+        def __bool__(self):
+            raise KeyError("no truth")
+
+    a = torch.zeros(4, 8, dtype=torch.float16)
+    for call in (lambda: ts.act_grad(a, dbias=Unsure()), lambda: ts.act_grad(a, dbias=torch.ones(2)),
+                 lambda: ts.rmsnorm_backward(a, a, a[0], dweight=Unsure()), lambda: ts.layernorm_backward(a, a, a[0], dweight=Unsure()),
+                 lambda: ts.layernorm_backward(a, a, dbias=Unsure())):
+        with pytest.raises((KeyError, RuntimeError), match="no truth|ambiguous"):
+            call()

@@ -34,6 +34,7 @@ struct WrongType : std::runtime_error {   // TypeError
 struct Failed {   // TsError
     int64_t status;
 };
+struct Raised {};   // Python's own error, already set
 
 // ---- arguments ---------------------------------------------------------------------------
 
@@ -59,7 +60,11 @@ float real(PyObject* o) {
     }
     return (float)v;
 }
-bool flag(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool flag(PyObject* o) {
+    const int truth = PyObject_IsTrue(o);
+    if (truth < 0) throw Raised();
+    return truth == 1;
+}
 // A dtype, or `none` for None.
 ScalarType dtype(PyObject* o, ScalarType none) {
     if (o == Py_None) return none;
@@ -187,6 +192,7 @@ PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (n != N) throw WrongType("wrong number of arguments");
         at::AutoDispatchBelowADInplaceOrView below;   // autograd does not see these calls
         return F(a);
+    } catch (const Raised&) {
     } catch (const Failed& e) {
         PyObject* status = PyLong_FromLongLong(e.status);
         PyObject* error = PyObject_CallFunctionObjArgs(g_error, status, nullptr);
@@ -418,9 +424,10 @@ struct NormGrad {
 PyObject* rmsnorm_backward(PyObject* const* p) {
     NormGrad n(p[0], p[1], -1, p[2], p[4], p[6]);
     const float eps = real(p[3]);
+    const bool dweight = flag(p[5]);
     Launch l(device_of(n.dy, &n.h, n.weight, n.dh, n.out));
     void* dx = n.dx();
-    const Tensor dw = n.weight && flag(p[5]) ? empty({n.N}, n.weight->scalar_type(), n.dy) : Tensor();
+    const Tensor dw = n.weight && dweight ? empty({n.N}, n.weight->scalar_type(), n.dy) : Tensor();
     const Scratch ws(dw.defined() || n.N > 32768 ? ts_rmsnorm_backward_workspace(n.M, n.N) : 0, n.dy);
     run([&] {
         return ts_rmsnorm_backward(n.dy.data_ptr(), n.h.data_ptr(), ptr(n.weight), ptr(n.dh), dx, dw.defined() ?
@@ -435,11 +442,12 @@ PyObject* rmsnorm_backward(PyObject* const* p) {
 PyObject* layernorm_backward(PyObject* const* p) {
     NormGrad n(p[0], p[1], number(p[2]), p[3], p[5], p[9]);
     const float eps = real(p[4]);
+    const bool dweight = flag(p[6]), dbias = flag(p[7]);
     const ScalarType asked = dtype(p[8], kAny), sums = n.weight ? n.weight->scalar_type() : asked == kAny ? at::kFloat : asked;
     if (n.weight && asked != kAny && asked != sums) throw Refusal("dbias has weight's type");
     Launch l(device_of(n.dy, &n.h, n.weight, n.dh, n.out));
     void* dx = n.dx();
-    const Tensor dw = n.weight && flag(p[6]) ? empty({n.N}, sums, n.dy) : Tensor(), db = flag(p[7]) ? empty({n.N}, sums, n.dy) : Tensor();
+    const Tensor dw = n.weight && dweight ? empty({n.N}, sums, n.dy) : Tensor(), db = dbias ? empty({n.N}, sums, n.dy) : Tensor();
     const Scratch ws(dw.defined() || db.defined() || n.N > 16384 ? ts_layernorm_backward_workspace(n.M, n.N) : 0, n.dy);
     run([&] {
         return ts_layernorm_backward(n.dy.data_ptr(), n.h.data_ptr(), ptr(n.weight), ptr(n.dh), dx, dw.defined() ?
