@@ -247,3 +247,35 @@ def test_arguments_without_a_truth():
                  lambda: ts.layernorm_backward(a, a, dbias=Unsure())):
         with pytest.raises((KeyError, RuntimeError), match="no truth|ambiguous"):
             call()
+
+
+def test_a_checkpoint_changed_after_its_checks():
+    # data and n can be set anew: every call looks at them again
+    a, w = torch.zeros(4, 64, dtype=torch.float16), torch.zeros(64, 64, dtype=torch.float16)
+
+    def changed(**kw):
+        k = ts.Checkpoint.empty(4, 64, "cpu")
+        for name, v in kw.items():
+            setattr(k, name, v)
+        return k
+
+    def calls(k):
+        return (lambda: ts.checkpoint_unpack(k), lambda: ts.checkpoint_pack(a, k), lambda: ts.act_grad(a, k, "gelu"),
+                lambda: ts.layernorm(a, keep=k), lambda: ts.layernorm_backward(a, k), lambda: ts.rmsnorm_backward(a, k),
+                lambda: ts.gemm_epilogue(a, w, preact=k), lambda: ts.gemm_dact(a, w, k, "gelu"),
+                lambda: ts.gemm_epilogue_backward(a, k, w))
+
+    good = ts.Checkpoint.empty(4, 64, "cpu").data
+    for k in (changed(data=good[:, :48]), changed(data=good.int()), changed(data=good[0]), changed(data=good.t()),
+              changed(data=torch.zeros(256, 4, dtype=torch.uint8).t()), changed(data=good.unsqueeze(0))):
+        for call in calls(k):
+            with pytest.raises(ValueError, match="checkpoint's"):
+                call()
+    big = torch.zeros(4, 4096, dtype=torch.float16)
+    for call in (lambda k: ts.checkpoint_unpack(k), lambda k: ts.checkpoint_pack(big, k), lambda k: ts.act_grad(big, k, "gelu"),
+                 lambda k: ts.layernorm_backward(big, k)):
+        with pytest.raises(ValueError, match="checkpoint's"):
+            call(changed(n=4096))
+    for call in (lambda: ts.checkpoint_unpack(changed(n=-1)), lambda: ts.checkpoint_unpack(changed(n=1 << 62))):
+        with pytest.raises(ValueError, match="checkpoint's"):
+            call()

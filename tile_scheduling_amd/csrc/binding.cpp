@@ -118,8 +118,17 @@ int64_t rows(const Tensor& t, int64_t M, int64_t N, const char* what, ScalarType
     if (N > 1 && t.stride(1) != 1) throw Refusal(std::string(what) + " must have unit stride along its rows");
     return t.stride(0);
 }
+// What a Checkpoint's constructor has seen may have been changed since: whether its data still holds n columns a row.
+// (Rows that are not 16-byte aligned are refused by the library.)
+void kept_data(const Tensor& data, int64_t n) {
+    if (data.dim() != 2 || data.scalar_type() != at::kByte || (data.size(1) > 1 && data.stride(1) != 1) || n < 0 ||
+        n > INT32_MAX || data.size(1) < 33 * ((n + 31) / 32))
+        throw Refusal("a checkpoint's data " + name(data.scalar_type()) + " " + shape(data.sizes()) + " does not hold rows of " +
+                      std::to_string(n) + " columns");
+}
 // A checkpoint's rows: its bytes and the number of columns that they hold.
 int64_t kept_rows(const Tensor& data, int64_t n, int64_t M, int64_t N, const char* what) {
+    kept_data(data, n);
     if (data.size(0) != M || n != N)
         throw Refusal(std::string(what) + " has shape " + shape({data.size(0), n}) + ", expected " + shape({M, N}));
     return data.stride(0);
@@ -234,6 +243,7 @@ PyObject* product(PyObject* const* p) {
     const Tensor *out = maybe(p[2], "out"), *residual = maybe(p[7], "residual"), *preact = maybe(p[8], "preact"),
                  *bias = maybe(p[10], "bias"), *scale_a = maybe(p[11], "scale_a"), *scale_b = maybe(p[12], "scale_b");
     const int64_t kept_n = number(p[9]), M = a.size(0), K = a.size(1), N = b.size(1);
+    if (preact && kept_n >= 0) kept_data(*preact, kept_n);
     const c10::Device dev = device_of(a, &b, out, bias, residual, preact, scale_a, scale_b);
     const ScalarType type = dtype(p[3], a.scalar_type());
     if (out && (out->dim() != 2 || out->size(0) != M || out->size(1) != N || out->scalar_type() != type))
@@ -496,7 +506,9 @@ PyObject* checkpoint_pack(PyObject* const* p) {
 // checkpoint's data, its columns, activation, out, out_dtype
 PyObject* checkpoint_unpack(PyObject* const* p) {
     const Tensor &d = tensor(p[0], "kept"), *out = maybe(p[3], "out");
-    const int64_t M = d.size(0), N = number(p[1]);
+    const int64_t N = number(p[1]);
+    kept_data(d, N);
+    const int64_t M = d.size(0);
     const int32_t act = (int32_t)number(p[2]);
     const ScalarType to = dtype(p[4], out ? out->scalar_type() : at::kFloat);
     const int64_t ldo = out ? rows(*out, M, N, "out", to) : N;
