@@ -1,6 +1,10 @@
 """Layer norm, int8 products, rows in 8 bits on the CPU: every refusal comes before any HIP call, and
 valid calls reach the device check."""
 import ctypes
+import os
+import shutil
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -279,3 +283,31 @@ def test_a_checkpoint_changed_after_its_checks():
     for call in (lambda: ts.checkpoint_unpack(changed(n=-1)), lambda: ts.checkpoint_unpack(changed(n=1 << 62))):
         with pytest.raises(ValueError, match="checkpoint's"):
             call()
+
+
+@pytest.mark.parametrize("module,reason", [(None, "_binding"), ("built_for = 'torch 1.0, Python 2.7'\n", "torch 1.0"),
+                                           ("raise ImportError('undefined symbol')\n", "undefined symbol")])
+def test_package_without_a_fitting_binding(tmp_path, module, reason):
+    # the product and its schedules need the library alone; the operators' calls say what is missing
+    package = tmp_path / "tile_scheduling_amd"
+    package.mkdir()
+    here = os.path.dirname(ts.__file__)
+    shutil.copy(os.path.join(here, "__init__.py"), package)
+    os.symlink(os.path.join(here, "libtsgemm.so"), package / "libtsgemm.so")
+    if module:
+        (package / "_binding.py").write_text(module)
+    code = f"""
+import torch, tile_scheduling_amd as ts
+assert ts.schedule_trace_host(256, 256, 256, ts.Schedule(), 4, 1).shape[1] == 5
+a = torch.zeros(4, 8)
+for call in (lambda: ts.layernorm(a), lambda: ts.gemm_epilogue(a, a.t()), lambda: ts.checkpoint_pack(a)):
+    try:
+        call()
+    except ImportError as e:
+        assert {reason!r} in str(e) and "build.py" in str(e), e
+    else:
+        raise AssertionError("no error")
+print("ended")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "ended" in r.stdout, r.stderr

@@ -2,9 +2,10 @@
 
 Argument marshalling only (ctypes here, the operators' in ``_binding``): every step of
 the computation runs in the HIP kernels of ``libtsgemm.so``.  PyTorch supplies device
-memory and streams.  Both libraries are built in-tree by ``python -m
-tile_scheduling_amd.build``; importing this package without them raises ImportError, and
-there is no fallback path.
+memory and streams.  Both libraries are built in-tree by ``python
+tile_scheduling_amd/build.py``.  Without ``libtsgemm.so`` importing this package raises ImportError,
+without a ``_binding`` built for this torch and Python an operator's call does (the product and its
+schedules do without); there is no fallback path.
 
     import torch, tile_scheduling_amd as ts
     c = ts.gemm(a, b, out_dtype=torch.float16,
@@ -15,20 +16,39 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
+import sys
 
 import torch  # loaded first: libtsgemm binds to the HIP runtime torch already loaded
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtsgemm.so")
+_BUILD = f"python {os.path.join(_HERE, 'build.py')}"
 
 if not os.path.exists(LIB_PATH):
-    raise ImportError(f"{LIB_PATH} is missing: build it with `python -m tile_scheduling_amd.build`")
+    raise ImportError(f"{LIB_PATH} is missing: build it with `{_BUILD}`")
 
 _lib = ctypes.CDLL(LIB_PATH)
+
+
+class _Missing:
+    """In _binding's place: every call of an operator says why."""
+
+    def __init__(self, reason):
+        self._reason = reason
+
+    def __getattr__(self, name):
+        raise ImportError(f"{self._reason}: build the package with `{_BUILD}`")
+
+
 try:
     from . import _binding   # the operators' calls, checked and made in C++ (csrc/binding.cpp)
+
+    _running = f"torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
+    _built = getattr(_binding, "built_for", "an earlier version of it")
+    if _built != _running:
+        _binding = _Missing(f"_binding was built for {_built}, this is {_running}")
 except ImportError as e:
-    raise ImportError(f"{e}: build the package with `python -m tile_scheduling_amd.build`") from e
+    _binding = _Missing(str(e))
 
 _i32, _i64, _p = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 
@@ -357,7 +377,8 @@ def schedule_trace_host(M: int, N: int, K: int, schedule: Schedule, cu_count: in
 
 # ---- operators around the product ------------------------------------------------------
 
-_binding.set_error(TsError)
+if not isinstance(_binding, _Missing):
+    _binding.set_error(TsError)
 
 
 class Checkpoint:

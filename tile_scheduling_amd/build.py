@@ -1,6 +1,6 @@
 """Build libtsgemm.so (HIP kernels + C ABI) for gfx950, and the Python module _binding.so over it, in-tree.
 
-    python -m tile_scheduling_amd.build      # or: python tile_scheduling_amd/build.py
+    python tile_scheduling_amd/build.py      # once built, also: python -m tile_scheduling_amd.build
 
 Each .hip file under csrc/ is compiled to an object in parallel with hipcc, then
 linked into tile_scheduling_amd/libtsgemm.so.  Packed fp32 instructions are
@@ -164,9 +164,11 @@ def build_binding(verbose: bool = False) -> str:
     from torch.utils import cpp_extension
 
     lib_dir = os.path.join(os.path.dirname(torch.__file__), "lib")
+    # it takes the tensors of one torch and the calls of one Python: __init__.py compares
+    target = f"torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-unknown-pragmas", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DTS_BUILT_FOR="{target}"']
     cmd += [f"-I{d}" for d in cpp_extension.include_paths() + [sysconfig.get_paths()["include"],
             os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_hipcc()))), "include")]]
     cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{lib_dir}", "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python",

@@ -538,4 +538,11 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__binding() {
+    PyObject* module = PyModule_Create(&kModule);
+    if (module && PyModule_AddStringConstant(module, "built_for", TS_BUILT_FOR) < 0) {   // the package compares it with what runs
+        Py_DECREF(module);
+        return nullptr;
+    }
+    return module;
+}
