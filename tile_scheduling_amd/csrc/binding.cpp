@@ -17,6 +17,7 @@
 #include <string>
 
 #include "../../include/tsgemm.h"
+#include "limits.hpp"
 
 namespace {
 
@@ -230,8 +231,6 @@ PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // ---- products ----------------------------------------------------------------------------
 
-constexpr int64_t kFewRows = 32;   // products of up to this many rows mostly need no workspace
-
 // a, b, out, out_dtype, activation, grad, schedule (address or 0), residual, preact, columns of a checkpoint's
 // preact (-1: a tensor), bias, scale_a, scale_b
 PyObject* product(PyObject* const* p) {
@@ -284,10 +283,8 @@ PyObject* product(PyObject* const* p) {
     const Tensor made = out ? Tensor() : empty({M, N}, type, a);
     const Tensor& c = out ? *out : made;
     const int32_t ab_t = code(a.scalar_type()), c_t = code(type);
-    int64_t need = 0;
-    if (M > kFewRows || s || a.stride(1) != 1 || K <= 1 || N >= 1 << 26 || (b.stride(0) != 1 && K >= 4096))
-        need = ts_gemm_epilogue_workspace(pa, pb, M, N, K, a.stride(0), a.stride(1), b.stride(0), b.stride(1), ab_t, c_t, s);
-    const Scratch ws(need, a);
+    const Scratch ws(ts_gemm_epilogue_workspace(pa, pb, M, N, K, a.stride(0), a.stride(1), b.stride(0), b.stride(1), ab_t,
+                                                c_t, s), a);
     run([&] {
         return ts_gemm_epilogue(pa, pb, c.data_ptr(), M, N, K, a.stride(0), a.stride(1), b.stride(0), b.stride(1),
                                 c.stride(0), c.stride(1), ab_t, c_t, &e, s, l.stream, ws.ptr(), ws.bytes);
@@ -438,7 +435,7 @@ PyObject* rmsnorm_backward(PyObject* const* p) {
     Launch l(device_of(n.dy, &n.h, n.weight, n.dh, n.out));
     void* dx = n.dx();
     const Tensor dw = n.weight && dweight ? empty({n.N}, n.weight->scalar_type(), n.dy) : Tensor();
-    const Scratch ws(dw.defined() || n.N > 32768 ? ts_rmsnorm_backward_workspace(n.M, n.N) : 0, n.dy);
+    const Scratch ws(dw.defined() || n.N > ts::kRmsGradRow ? ts_rmsnorm_backward_workspace(n.M, n.N) : 0, n.dy);
     run([&] {
         return ts_rmsnorm_backward(n.dy.data_ptr(), n.h.data_ptr(), ptr(n.weight), ptr(n.dh), dx, dw.defined() ?
                                    dw.data_ptr() : nullptr, n.M, n.N, n.ldy, n.ldh, n.lds, n.ldx, row_code(n.type),
@@ -458,7 +455,7 @@ PyObject* layernorm_backward(PyObject* const* p) {
     Launch l(device_of(n.dy, &n.h, n.weight, n.dh, n.out));
     void* dx = n.dx();
     const Tensor dw = n.weight && dweight ? empty({n.N}, sums, n.dy) : Tensor(), db = dbias ? empty({n.N}, sums, n.dy) : Tensor();
-    const Scratch ws(dw.defined() || db.defined() || n.N > 16384 ? ts_layernorm_backward_workspace(n.M, n.N) : 0, n.dy);
+    const Scratch ws(dw.defined() || db.defined() || n.N > ts::kLayerGradRow ? ts_layernorm_backward_workspace(n.M, n.N) : 0, n.dy);
     run([&] {
         return ts_layernorm_backward(n.dy.data_ptr(), n.h.data_ptr(), ptr(n.weight), ptr(n.dh), dx, dw.defined() ?
                                      dw.data_ptr() : nullptr, db.defined() ? db.data_ptr() : nullptr, n.M, n.N,

@@ -353,6 +353,8 @@ const void* nt_kernel(int nx) {
 // More than 32 rows of int8 operands (few_rows_most).  bf16 C, one group of columns / two / the tiles: 64 rows 1984 x
 // 740 6.3 / 7.7 / 13.8 us, 4096 x 4096 13.3 / 16.8 / 16.4, 5952 x 2368 14.5 / 10.7 / 20.9, 8192 x 8192 44.6 / 29.5 / 28.9; 128 rows
 // 1984 x 740 9.3 / 13.1 / 14.5, 5952 x 2368 25.4 / 18.7 / 23.7, 4096 x 4096 21.4 / 26.4 / 18.3.
+// (The limit of 128 rows is 2048 in K although 5952 x 2368 gains: between that and 4096 x 4096, which loses, nothing is
+// measured, nor above 8192 columns.)
 template <class TO>
 const void* many_kernel(int mt, int nx) {
     if (mt == 4) {

@@ -6,8 +6,8 @@
 
 namespace ts {
 
-constexpr int kFewRows = 32;   // largest M of these kernels
-// The same for int8: with more rows, as far as the rows of A, which every workgroup reads, cost less than
+constexpr int kFewRows = 32;   // largest M of these kernels, but for int8 operands
+// Largest M with int8 operands as well: with more rows, as far as the rows of A, which every workgroup reads, cost less than
 // tiles that leave most CUs idle (figures at many_kernel, few_rows.hip).
 inline int few_rows_most(bool int8, long long N, long long K) {
     return int8 && N <= 8192 ? (K <= 2048 ? 128 : K <= 4096 ? 64 : kFewRows) : kFewRows;

@@ -6,6 +6,7 @@
 // quarter for h kept in 8), beside the running sums of dw and db.  Measured: 8192 x 4096 bf16 with dh 51 us (268 MB,
 // 5.2 TB/s) and 6.5 us for the sums of 512 workgroups; 1000 x 2048 fp16 with h in 8 bits 12 and 4 us (latency).
 #include "layernorm.hpp"
+#include "limits.hpp"
 
 namespace ts {
 
@@ -296,6 +297,7 @@ namespace {
 Shape grad_shape(int64_t N) {
     const int64_t groups = (N + 7) / 8;
     static const Shape kShapes[] = {{16, 1}, {16, 2}, {64, 1}, {64, 2}, {256, 1}, {256, 2}, {512, 2}, {1024, 2}};
+    static_assert(kLayerGradRow == 1024 * 2 * 8, "the last shape");
     for (const Shape& s : kShapes)
         if (groups <= (int64_t)s.t * s.c) return s;
     return Shape{0, 0};

@@ -15,6 +15,7 @@
 // dw over 1024 workgroups; one row of 4096 4.9 us.
 #include <hip/hip_runtime.h>
 
+#include "limits.hpp"
 #include "norm.hpp"
 
 namespace ts {
@@ -496,6 +497,7 @@ extern "C" ts_status ts_rmsnorm_backward(const void* dy, const void* h, const vo
     if (!in_place_ok(dx, dy, true, M, stride_dx, stride_dy) || !in_place_ok(dx, h, true, M, stride_dx, stride_h) ||
         !in_place_ok(dx, dh, true, M, stride_dx, stride_dh))
         return TS_ERR_INVALID_ARG;
+    static_assert(kRmsGradRow == 1024 * 4 * 8, "the last shape");
     const bool long_rows = norm_shape(M, N, 4).t == 0;
     const int64_t groups = M > 0 ? norm_grad_groups(M, N) : 0;
     const int64_t part = (groups * N * 4 + 255) / 256 * 256;
