@@ -54,7 +54,8 @@ __global__ void __launch_bounds__(256) checkpoint_unpack_kernel(CheckpointArgs g
     const float step = step_of(row[kept_values(g.N) + n / kBlock]);
     float v[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) kept_unpack4<std::is_same<TY, OutF16>::value>(w[i], step, v + 4 * i);
+    for (int i = 0; i < 4; ++i) kept_unpack4(w[i], step, v + 4 * i);
+    kept_last<16, std::is_same<TY, OutF16>::value>(step, v);
     act_values<16>(g.act, v);
     Y* y = static_cast<Y*>(g.out) + m * g.ld_out + n;
     store8<TY>(y, g.N - n, v);

@@ -115,7 +115,7 @@ struct CheckpointStore {
                 const int nb = t.n + 32 * j;
                 const bool in = m + t.r32 < t.M && nb < t.N;
                 const uint8_t* row = g.kept + (in ? (long long)(m + t.r32) * g.ld_kept : 0);
-                const float step = step_of(in ? row[values + nb / kBlock] : 1u);
+                const float step = slope_step_of(in ? row[values + nb / kBlock] : 1u);
                 float w[NQ][4];
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) kept_quad(t, row, step, in ? nb + 8 * q + 4 * t.hk : t.N, w[q]);

@@ -103,9 +103,7 @@ __device__ __forceinline__ void finish_element(const FewArgs& g, float v, int m,
     float in = g.aux_in ? (float)static_cast<const T*>(g.aux_in)[m * g.ld_in + n] : 0.0f;
     if (KEPT && g.grad) {
         const uint8_t* row = g.kept + m * g.ld_kept;
-        const float step = step_of(row[kept_values(g.N) + n / kBlock]);
-        in = (float)(int8_t)row[n] * step;
-        kept_last<1, false>(step, &in);
+        in = (float)(int8_t)row[n] * slope_step_of(row[kept_values(g.N) + n / kBlock]);
     }
     if (g.grad) {
         act_slopes<1>(g.act, &v, &in);
