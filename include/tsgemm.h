@@ -413,7 +413,8 @@ typedef struct {
  *              activation; no bias, no residual)
  * All of it in fp32 from the fp32 sums (the scales multiply in this order: what overflows on the
  * way is infinite); preact and C are each rounded once, to C's type (preact: or to 8 bits).  TS_I8: the
- * sums are exact whole numbers, rounded once to fp32.  epi == NULL: the plain product.
+ * sums are exact whole numbers, rounded once to fp32, and z is fma(sum * scale_a, scale_b, bias): z, and C
+ * where grad is 0, have the same bits whatever the schedule and the number of rows.  epi == NULL: the plain product.
  *   ab_dtype / c_dtype: TS_F16 -> TS_F16, TS_F32; TS_BF16 -> TS_BF16, TS_F32;
  *   TS_E4M3, TS_I8 -> TS_F16, TS_BF16, TS_F32.  Layouts and strides of A, B and C as in
  *   ts_gemm; with 8-bit operands only A stored [M][K] and B stored [N][K] (stride_bk == 1).
@@ -428,7 +429,7 @@ typedef struct {
  *   8-bit operands a K step holds 128 values.
  *   Up to 32 rows, A stored [M][K] (B stored [K][N]: K below 4096, up to 16 rows below
  *   8192), and a schedule that leaves order, mode, tile and programs to the library: one pass over B with K split over the waves of a workgroup
- *   (sums in another order than the tile kernels', the same on every run), no workspace.  TS_I8, N up to
+ *   (sums in another order than the tile kernels', the same on every run), no workspace.  TS_I8 and N up to
  *   8192: up to 64 rows with K up to 4096, 128 with K up to 2048.
  *   With such a schedule and few tiles, K is split among programs (whole fp32 tiles of sums in
  *   the workspace) and a second kernel adds the parts, in order, and applies the epilogue.

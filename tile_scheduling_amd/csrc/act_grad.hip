@@ -6,7 +6,7 @@
 // every run); up to 16 rows are one group, whose sums are dbias itself.  Bound by memory:
 // 4096 x 8192 bf16 42 us (201 MB, 4.8 TB/s), and 4.7 us for the second launch.
 // KEPT: Z in 8 bits (checkpoint.hpp).  VALUE: act(Z) too, an operand of the next weight's gradient, which
-// the forward pass then need not keep.  Both: 4096 x 16384 bf16 102 us (486 MB, 4.8 TB/s).
+// the forward pass then need not keep.  Both: 4096 x 16384 bf16 104 us (489 MB, 4.7 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <limits.h>

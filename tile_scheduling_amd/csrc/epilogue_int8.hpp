@@ -9,7 +9,7 @@ namespace ts {
 
 // The scales and biases of a lane's 32 columns are held in registers (64) and z is formed where it is used:
 // accumulators that are changed in place spill 80 to 300 registers.  (With the rows of a residual ahead 18 to
-// 55 are, none inside the K loop.)  Against FusedStore, bf16 C, with bias, us: 4096 x 16384 x 4096 none 237 / 252, silu
+// 22 are, none inside the K loop.)  Against FusedStore, bf16 C, with bias, us: 4096 x 16384 x 4096 none 237 / 252, silu
 // 254 / 268, residual 262 / 281; 5000 x 12290 x 1000 91 / 107, 106 / 124, 123 / 133; 4096 x 4096 x 8192 residual 120 / 126.
 template <int FAM, bool RESIDUAL>
 struct SpecialInt8Store {
